@@ -23,6 +23,7 @@ STATUS_NAMES = {
 MOE_DEV_TIMEOUT = 0x1
 MOE_DEV_BAD_EXPERT = 0x2
 MOE_DEV_BAD_SCALE = 0x4
+MOE_DEV_BAD_GROUP = 0x8
 
 
 class MoeError(RuntimeError):
@@ -102,6 +103,115 @@ class MoeW4A8Args(ctypes.Structure):
     ]
 
 
+GROUPED_FORWARD, GROUPED_INPUT_GRADIENT = 0, 1
+GROUPED_PLAIN, GROUPED_SWIGLU = 0, 1
+TYPE_CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+class MoeGroupedArgs(ctypes.Structure):
+    """Mirror of ``struct moe_grouped_args`` (include/moe_train.h)."""
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("w", ctypes.c_void_p),
+        ("y", ctypes.c_void_p),
+        ("pre", ctypes.c_void_p),
+        ("group_start", ctypes.c_void_p),
+        ("group_rows", ctypes.c_void_p),
+        ("route_ids", ctypes.c_void_p),
+        ("route_weights", ctypes.c_void_p),
+        ("device_status", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("ldx", ctypes.c_int64),
+        ("ldy", ctypes.c_int64),
+        ("ldpre", ctypes.c_int64),
+        ("R", ctypes.c_int64),
+        ("E", ctypes.c_int32),
+        ("N", ctypes.c_int32),
+        ("K", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("direction", ctypes.c_int32),
+        ("epilogue", ctypes.c_int32),
+    ]
+
+
+class MoeGroupedWgradArgs(ctypes.Structure):
+    """Mirror of ``struct moe_grouped_wgrad_args``."""
+    _fields_ = [
+        ("dy", ctypes.c_void_p),
+        ("x", ctypes.c_void_p),
+        ("dw", ctypes.c_void_p),
+        ("group_start", ctypes.c_void_p),
+        ("group_rows", ctypes.c_void_p),
+        ("device_status", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("lddy", ctypes.c_int64),
+        ("ldx", ctypes.c_int64),
+        ("E", ctypes.c_int32),
+        ("N", ctypes.c_int32),
+        ("K", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("dw_dtype", ctypes.c_int32),
+        ("accumulate", ctypes.c_int32),
+    ]
+
+
+class MoeSwigluBackwardArgs(ctypes.Structure):
+    """Mirror of ``struct moe_swiglu_backward_args``."""
+    _fields_ = [
+        ("dh", ctypes.c_void_p),
+        ("pre", ctypes.c_void_p),
+        ("dpre", ctypes.c_void_p),
+        ("h", ctypes.c_void_p),
+        ("route_ids", ctypes.c_void_p),
+        ("num_rows", ctypes.c_void_p),
+        ("route_weights", ctypes.c_void_p),
+        ("dweights", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("lddh", ctypes.c_int64),
+        ("ldpre", ctypes.c_int64),
+        ("lddpre", ctypes.c_int64),
+        ("ldh", ctypes.c_int64),
+        ("R", ctypes.c_int64),
+        ("I", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
+class MoeAdamWTensor(ctypes.Structure):
+    """Mirror of ``struct moe_adamw_tensor``."""
+    _fields_ = [
+        ("param", ctypes.c_void_p),
+        ("model", ctypes.c_void_p),
+        ("grad", ctypes.c_void_p),
+        ("exp_avg", ctypes.c_void_p),
+        ("exp_avg_sq", ctypes.c_void_p),
+        ("exp_avg_scale", ctypes.c_void_p),
+        ("exp_avg_sq_scale", ctypes.c_void_p),
+        ("n", ctypes.c_int64),
+        ("weight_decay", ctypes.c_double),
+        ("grad_dtype", ctypes.c_int32),
+        ("model_dtype", ctypes.c_int32),
+    ]
+
+
+class MoeAdamWArgs(ctypes.Structure):
+    """Mirror of ``struct moe_adamw_args``."""
+    _fields_ = [
+        ("table", ctypes.c_void_p),
+        ("grad_scale", ctypes.c_void_p),
+        ("skip", ctypes.c_void_p),
+        ("chunks", ctypes.c_int64),
+        ("step", ctypes.c_int64),
+        ("lr", ctypes.c_double),
+        ("beta1", ctypes.c_double),
+        ("beta2", ctypes.c_double),
+        ("eps", ctypes.c_double),
+        ("seed", ctypes.c_uint32),
+        ("count", ctypes.c_int32),
+        ("state_bits", ctypes.c_int32),
+    ]
+
+
 _libs = {}
 _active = LIB_PATH
 
@@ -144,6 +254,23 @@ _SIGS = {
                                                ctypes.c_void_p, ctypes.c_void_p]),
     "moe_w4a8_workspace_size": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int]),
     "moe_w4a8_forward": (ctypes.c_int, [ctypes.POINTER(MoeW4A8Args), ctypes.c_void_p]),
+    "moe_plan_groups": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                       ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int, ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "moe_gather_rows": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_int64, ctypes.c_void_p,
+                                       ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
+                                       ctypes.c_int, ctypes.c_void_p]),
+    "moe_sum_routes": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_int64, ctypes.c_void_p,
+                                      ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_int,
+                                      ctypes.c_int, ctypes.c_void_p]),
+    "moe_grouped_gemm": (ctypes.c_int, [ctypes.POINTER(MoeGroupedArgs), ctypes.c_void_p]),
+    "moe_grouped_wgrad": (ctypes.c_int, [ctypes.POINTER(MoeGroupedWgradArgs), ctypes.c_void_p]),
+    "moe_swiglu_backward": (ctypes.c_int, [ctypes.POINTER(MoeSwigluBackwardArgs), ctypes.c_void_p]),
+    "moe_adamw_table_bytes": (ctypes.c_size_t, [ctypes.c_int]),
+    "moe_adamw_table_init": (ctypes.c_int, [ctypes.POINTER(MoeAdamWTensor), ctypes.c_int, ctypes.c_int,
+                                            ctypes.c_void_p, ctypes.c_size_t, ctypes.POINTER(ctypes.c_int64),
+                                            ctypes.c_void_p]),
+    "moe_adamw_step": (ctypes.c_int, [ctypes.POINTER(MoeAdamWArgs), ctypes.c_void_p]),
     "moe_debug_bounds_enabled": (ctypes.c_int, []),
     "moe_debug_bounds_selftest": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_void_p,
                                                  ctypes.c_void_p]),
@@ -429,3 +556,224 @@ def make_w4a8_args(a, a_scale, w13, w13_scale, w2, w2_scale, topk_weights, sorte
 
 def moe_w4a8_forward(args, stream=None):
     _check("moe_w4a8_forward", load().moe_w4a8_forward(ctypes.byref(args), _stream(stream)))
+
+
+# ---------------------------------------------------------------- training side (include/moe_train.h)
+#
+# Row buffers may be strided by rows (a slice of wider rows); their elements
+# are contiguous within a row.
+
+def _rows2d(name, t, dtype=None):
+    """(pointer, row stride) of a 2D row buffer; ValueError if it is not one the library can read."""
+    if t.dim() != 2 or t.stride(1) != 1:
+        raise ValueError(f"{name}: a 2D tensor with contiguous rows is expected")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    return t.data_ptr(), t.stride(0)
+
+
+def _dense(name, t, dtype=None, numel=None):
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor is expected")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if numel is not None and t.numel() < numel:
+        raise ValueError(f"{name}: {t.numel()} elements, at least {numel} expected")
+    return t.data_ptr()
+
+
+def _opt(name, t, dtype, numel=None):
+    return None if t is None else _dense(name, t, dtype, numel)
+
+
+def _shape(name, t, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def moe_plan_groups(sorted_token_ids, expert_ids, num_tokens_post_padded, block_m, R, group_start, group_rows,
+                    route_slot=None, stream=None):
+    """First slot and row count of every expert of a plan (int32 [E] each) and,
+    optionally, the slot of every route (int32 [R], -1 where the plan has none)."""
+    E = group_start.numel()
+    _dense("group_start", group_start, torch.int32)
+    _dense("group_rows", group_rows, torch.int32, E)
+    _opt("route_slot", route_slot, torch.int32, R)
+    _check("moe_plan_groups", load().moe_plan_groups(
+        _ptr(sorted_token_ids), sorted_token_ids.numel(), _ptr(expert_ids), expert_ids.numel(),
+        _ptr(num_tokens_post_padded), block_m, R, E, _ptr(group_start), _ptr(group_rows), _ptr(route_slot),
+        _stream(stream)))
+
+
+def moe_gather_rows(x, xs, route_ids, top_k, num_rows=None, stream=None):
+    """xs[s] = x[route_ids[s] // top_k]; zero rows where the id is none of the len(x) * top_k routes."""
+    xp, ldx = _rows2d("x", x)
+    xsp, ldxs = _rows2d("xs", xs, x.dtype)
+    if xs.shape[1] != x.shape[1]:
+        raise ValueError("x and xs differ in width")
+    _dense("route_ids", route_ids, torch.int32, xs.shape[0])
+    _opt("num_rows", num_rows, torch.int32, 1)
+    _check("moe_gather_rows", load().moe_gather_rows(
+        xp, x.shape[0], x.shape[1], ldx, xsp, xs.shape[0], ldxs, _ptr(route_ids), top_k, _ptr(num_rows),
+        TYPE_CODES[x.dtype], _stream(stream)))
+
+
+def moe_sum_routes(y, out, route_slot, top_k, accumulate=False, stream=None):
+    """out[t] = sum of y[route_slot[t * top_k + j]] over j (on top of out[t] with accumulate)."""
+    yp, ldy = _rows2d("y", y)
+    op, ldo = _rows2d("out", out, y.dtype)
+    if out.shape[1] != y.shape[1]:
+        raise ValueError("y and out differ in width")
+    _dense("route_slot", route_slot, torch.int32, out.shape[0] * top_k)
+    _check("moe_sum_routes", load().moe_sum_routes(
+        yp, y.shape[0], y.shape[1], ldy, op, out.shape[0], ldo, _ptr(route_slot), top_k, 1 if accumulate else 0,
+        TYPE_CODES[y.dtype], _stream(stream)))
+
+
+def make_grouped_args(x, w, y, group_start, group_rows, input_gradient=False, epilogue=GROUPED_PLAIN, pre=None,
+                      route_ids=None, route_weights=None, device_status=None):
+    """Fill a ``moe_grouped_args`` from tensors (shapes give the sizes): w [E, N, K];
+    x [rows, K] and y [rows, N] (N / 2 with the SwiGLU epilogue), or with
+    input_gradient x [rows, N] and y [rows, K]."""
+    E, N, K = w.shape
+    rows = x.shape[0]
+    glu = epilogue == GROUPED_SWIGLU
+    args = MoeGroupedArgs()
+    args.x, args.ldx = _rows2d("x", x, w.dtype)
+    args.y, args.ldy = _rows2d("y", y, w.dtype)
+    _shape("x", x, (rows, N if input_gradient else K))
+    _shape("y", y, (rows, K if input_gradient else N // 2 if glu else N))
+    args.w = _dense("w", w)
+    if pre is not None:
+        args.pre, args.ldpre = _rows2d("pre", pre, w.dtype)
+        _shape("pre", pre, (rows, N))
+    args.group_start = _dense("group_start", group_start, torch.int32, E)
+    args.group_rows = _dense("group_rows", group_rows, torch.int32, E)
+    args.route_ids = _opt("route_ids", route_ids, torch.int32, rows)
+    args.route_weights = _opt("route_weights", route_weights, torch.float32, None if route_ids is not None else rows)
+    args.device_status = _opt("device_status", device_status, torch.int32, 1)
+    args.rows, args.R = rows, 0 if route_weights is None else route_weights.numel()
+    args.E, args.N, args.K = E, N, K
+    args.dtype = TYPE_CODES[w.dtype]
+    args.direction = GROUPED_INPUT_GRADIENT if input_gradient else GROUPED_FORWARD
+    args.epilogue = epilogue
+    return args
+
+
+def moe_grouped_gemm(args, stream=None):
+    _check("moe_grouped_gemm", load().moe_grouped_gemm(ctypes.byref(args), _stream(stream)))
+
+
+def make_grouped_wgrad_args(dy, x, dw, group_start, group_rows, accumulate=False, device_status=None):
+    """Fill a ``moe_grouped_wgrad_args``: dy [rows, N], x [rows, K], dw [E, N, K] in their type or FP32."""
+    E, N, K = dw.shape
+    rows = x.shape[0]
+    args = MoeGroupedWgradArgs()
+    args.dy, args.lddy = _rows2d("dy", dy, x.dtype)
+    args.x, args.ldx = _rows2d("x", x)
+    _shape("dy", dy, (rows, N))
+    _shape("x", x, (rows, K))
+    args.dw = _dense("dw", dw)
+    args.group_start = _dense("group_start", group_start, torch.int32, E)
+    args.group_rows = _dense("group_rows", group_rows, torch.int32, E)
+    args.device_status = _opt("device_status", device_status, torch.int32, 1)
+    args.rows, args.E, args.N, args.K = rows, E, N, K
+    args.dtype, args.dw_dtype = TYPE_CODES[x.dtype], TYPE_CODES[dw.dtype]
+    args.accumulate = 1 if accumulate else 0
+    return args
+
+
+def moe_grouped_wgrad(args, stream=None):
+    _check("moe_grouped_wgrad", load().moe_grouped_wgrad(ctypes.byref(args), _stream(stream)))
+
+
+def make_swiglu_backward_args(dh, pre, dpre, h=None, route_ids=None, num_rows=None, route_weights=None,
+                              dweights=None):
+    """Fill a ``moe_swiglu_backward_args``: dh and h [rows, I], pre and dpre [rows, 2I]."""
+    rows, I = dh.shape
+    args = MoeSwigluBackwardArgs()
+    args.dh, args.lddh = _rows2d("dh", dh)
+    args.pre, args.ldpre = _rows2d("pre", pre, dh.dtype)
+    args.dpre, args.lddpre = _rows2d("dpre", dpre, dh.dtype)
+    _shape("pre", pre, (rows, 2 * I))
+    _shape("dpre", dpre, (rows, 2 * I))
+    if h is not None:
+        args.h, args.ldh = _rows2d("h", h, dh.dtype)
+        _shape("h", h, (rows, I))
+    args.route_ids = _opt("route_ids", route_ids, torch.int32, rows)
+    args.num_rows = _opt("num_rows", num_rows, torch.int32, 1)
+    by_route = [t.numel() for t in (route_weights, dweights) if t is not None]
+    need = None if route_ids is not None else rows
+    args.route_weights = _opt("route_weights", route_weights, torch.float32, need)
+    args.dweights = _opt("dweights", dweights, torch.float32, need)
+    # without either, every nonnegative id names a route
+    args.R = min(by_route) if by_route else 2 ** 31 - 1
+    args.rows, args.I, args.dtype = rows, I, TYPE_CODES[dh.dtype]
+    return args
+
+
+def moe_swiglu_backward(args, stream=None):
+    _check("moe_swiglu_backward", load().moe_swiglu_backward(ctypes.byref(args), _stream(stream)))
+
+
+class AdamWTable:
+    """The device table of an AdamW step over `tensors`: dicts with ``param``
+    (float32), ``grad`` and the states ``exp_avg`` and ``exp_avg_sq``; optionally
+    ``model`` (bfloat16 or float16, the rounded copy of param) and
+    ``weight_decay`` (the argument's value otherwise).  States are float32, or
+    8-bit codes (float8_e4m3fn or uint8) with ``exp_avg_scale`` and
+    ``exp_avg_sq_scale``, one float32 per 128 elements.  The table keeps the
+    tensors alive."""
+
+    def __init__(self, tensors, weight_decay=0.0, stream=None):
+        if not tensors:
+            raise ValueError("no tensors")
+        self.state_bits = 32 if tensors[0]["exp_avg"].dtype == torch.float32 else 8
+        codes = (torch.float32,) if self.state_bits == 32 else (torch.float8_e4m3fn, torch.uint8)
+        self.count = len(tensors)
+        self.keep = [dict(t) for t in tensors]
+        host = (MoeAdamWTensor * self.count)()
+        for e, t in zip(host, self.keep):
+            n = t["param"].numel()
+            e.param = _dense("param", t["param"], torch.float32)
+            for name in ("grad", "exp_avg", "exp_avg_sq"):
+                setattr(e, name, _dense(name, t[name]))
+                if t[name].numel() != n:
+                    raise ValueError(f"{name}: {t[name].numel()} elements, expected {n}")
+                if name != "grad" and t[name].dtype not in codes:
+                    raise ValueError(f"{name}: dtype {t[name].dtype}, expected {codes[0]}")
+            model = t.get("model")
+            if model is not None:
+                e.model = _dense("model", model, None, n)
+                e.model_dtype = TYPE_CODES[model.dtype]
+            if self.state_bits == 8:
+                e.exp_avg_scale = _dense("exp_avg_scale", t["exp_avg_scale"], torch.float32, -(-n // 128))
+                e.exp_avg_sq_scale = _dense("exp_avg_sq_scale", t["exp_avg_sq_scale"], torch.float32, -(-n // 128))
+            e.n = n
+            e.grad_dtype = TYPE_CODES[t["grad"].dtype]
+            e.weight_decay = float(t.get("weight_decay", weight_decay))
+        lib = load()
+        self.table = torch.empty(lib.moe_adamw_table_bytes(self.count), dtype=torch.uint8,
+                                 device=tensors[0]["param"].device)
+        chunks = ctypes.c_int64()
+        _check("moe_adamw_table_init", lib.moe_adamw_table_init(
+            host, self.count, self.state_bits, _ptr(self.table), self.table.numel(), ctypes.byref(chunks),
+            _stream(stream)))
+        self.chunks = chunks.value
+
+
+def make_adamw_args(table, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, seed=0, grad_scale=None, skip=None):
+    """Fill a ``moe_adamw_args`` for an AdamWTable; lr, step and seed are the
+    fields a loop rewrites between steps."""
+    args = MoeAdamWArgs()
+    args._table_keepalive = (table, grad_scale, skip)
+    args.table, args.chunks, args.count, args.state_bits = (table.table.data_ptr(), table.chunks, table.count,
+                                                            table.state_bits)
+    args.grad_scale = _opt("grad_scale", grad_scale, torch.float32, 1)
+    args.skip = _opt("skip", skip, torch.int32, 1)
+    args.lr, args.step, args.beta1, args.beta2, args.eps, args.seed = lr, step, beta1, beta2, eps, seed & 0xFFFFFFFF
+    return args
+
+
+def moe_adamw_step(args, stream=None):
+    _check("moe_adamw_step", load().moe_adamw_step(ctypes.byref(args), _stream(stream)))

@@ -1,0 +1,65 @@
+// Shared by the training-side kernels (include/moe_train.h): 16-bit element
+// types and vectors of eight of them.
+#pragma once
+
+#include "../../include/moe_train.h"
+#include "common.cuh"
+
+namespace moe {
+
+inline bool is_half_type(int dtype) { return dtype == MOE_TYPE_BF16 || dtype == MOE_TYPE_FP16; }
+inline bool is_type(int dtype) { return is_half_type(dtype) || dtype == MOE_TYPE_FP32; }
+inline int type_bytes(int dtype) { return dtype == MOE_TYPE_FP32 ? 4 : 2; }
+
+// Whether the byte ranges [a, a + na) and [b, b + nb) share a byte.
+inline bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const auto x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return na > 0 && nb > 0 && x < y + static_cast<uint64_t>(nb) && y < x + static_cast<uint64_t>(na);
+}
+// Bytes from a row buffer's first element to the end of its last row.
+inline int64_t extent_bytes(int64_t rows, int64_t ld, int64_t width, int elem) {
+  return rows > 0 ? ((rows - 1) * ld + width) * elem : 0;
+}
+
+template <typename T> struct Pack2;
+template <> struct Pack2<__nv_bfloat16> {
+  static __device__ __forceinline__ float2 load(uint32_t v) {
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
+  }
+  static __device__ __forceinline__ uint32_t store(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+};
+template <> struct Pack2<__half> {
+  static __device__ __forceinline__ float2 load(uint32_t v) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+  }
+  static __device__ __forceinline__ uint32_t store(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+};
+
+// Eight 16-bit elements of a 16-byte vector as FP32, and back (one rounding).
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = Pack2<T>::load(w[i]);
+    f[2 * i] = p.x;
+    f[2 * i + 1] = p.y;
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(Pack2<T>::store(f[0], f[1]), Pack2<T>::store(f[2], f[3]), Pack2<T>::store(f[4], f[5]),
+                    Pack2<T>::store(f[6], f[7]));
+}
+
+// 1 / (1 + exp(-g)) with the hardware exponential and divide (a few ulp; 0
+// once exp(-g) passes 2^126).
+__device__ __forceinline__ float sigmoid_f32(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+
+}  // namespace moe
