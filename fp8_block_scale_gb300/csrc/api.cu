@@ -40,9 +40,9 @@ bool on_device(const void* p, int device) {
   return false;
 }
 
-CUresult encode_tensor_map_2d_typed(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t inner,
-                                    uint64_t outer, uint64_t row_stride_bytes, uint32_t box_inner,
-                                    uint32_t box_outer, CUtensorMapSwizzle swizzle) {
+CUresult encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, int rank, const void* base,
+                           const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+                           CUtensorMapSwizzle swizzle) {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -54,12 +54,26 @@ CUresult encode_tensor_map_2d_typed(CUtensorMap* map, CUtensorMapDataType dtype,
       fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
   });
   if (fn == nullptr) return CUDA_ERROR_NOT_FOUND;
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {row_stride_bytes};
-  cuuint32_t box[2] = {box_inner, box_outer};
-  cuuint32_t estr[2] = {1, 1};
-  return fn(map, dtype, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  cuuint64_t d[5], st[4];
+  cuuint32_t bx[5], estr[5];
+  if (rank < 2 || rank > 5) return CUDA_ERROR_INVALID_VALUE;
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    bx[i] = box[i];
+    estr[i] = 1;
+    if (i > 0) st[i - 1] = strides[i - 1];
+  }
+  return fn(map, dtype, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, st, bx, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+CUresult encode_tensor_map_2d_typed(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t inner,
+                                    uint64_t outer, uint64_t row_stride_bytes, uint32_t box_inner,
+                                    uint32_t box_outer, CUtensorMapSwizzle swizzle) {
+  const uint64_t dims[2] = {inner, outer};
+  const uint32_t box[2] = {box_inner, box_outer};
+  return encode_tensor_map(map, dtype, 2, base, dims, &row_stride_bytes, box, swizzle);
 }
 
 CUresult encode_tensor_map_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,

@@ -73,6 +73,12 @@ CUresult encode_tensor_map_2d_typed(CUtensorMap* map, CUtensorMapDataType dtype,
                                     uint64_t outer, uint64_t row_stride_bytes, uint32_t box_inner,
                                     uint32_t box_outer, CUtensorMapSwizzle swizzle);
 
+// A tensor of 2 to 5 dimensions, innermost first (strides in bytes, from
+// dimension 1 on).
+CUresult encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, int rank, const void* base,
+                           const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+                           CUtensorMapSwizzle swizzle);
+
 // ---------------------------------------------------------------- bounds checks
 //
 // MOE_IN_BOUNDS(c) guards a global access or a tensor copy whose index is

@@ -1,135 +1,531 @@
-// Products grouped by expert (moe_grouped_gemm, moe_grouped_wgrad): the
-// simple form, FP32 products of 64x64 tiles on the CUDA cores.
+// Products grouped by expert (moe_grouped_gemm, moe_grouped_wgrad) on the
+// tensor cores: tcgen05.mma kind::f16 on pairs of CTAs (cta_group::2), operands
+// by tensor copies, FP32 accumulators in tensor memory.
+//
+// A pair computes tiles D [256 x up to 256].  The M side always is the side
+// without ragged edges: the weights' output rows (forward), their columns
+// (input gradient) or dw's rows (weight gradient); the ragged slots of a group
+// are the N side of the first two, so a tile's width follows the group: a
+// group of n slots is cut into ceil(n / 256) tiles of equal width (a multiple
+// of 32), and the MMAs compute no more columns than that.  In the weight
+// gradient the slots are the contraction.
+//
+//   mode     M (A operand)            N (B operand)     contraction
+//   forward  w rows n, K-major        slots, K-major    K
+//   SwiGLU   w rows, gate and up in alternating groups of 16 (a warp's lanes
+//            0-15 hold gates, lanes 16-31 the matching ups)
+//   dgrad    w columns k, M-major     slots, K-major    N
+//   wgrad    dy columns n, M-major    x columns k, N-major   slots of the group
+//
+// Warps of each CTA: 0 issues the tensor copies, 1 (of the leader) the MMAs,
+// 2-5 drain the accumulators.  Two 256-column accumulators let the drain of
+// one tile overlap the products of the next.  The CTAs are persistent: the
+// tiles of all groups form one sequence, dealt round-robin to the pairs.
+#include <mutex>
+
+#include "tc_pair.cuh"
 #include "train.cuh"
 
 namespace moe {
 namespace {
 
-__device__ __forceinline__ float to_f32(uint16_t v, int dtype) {
-  return dtype == MOE_TYPE_BF16 ? Pack2<__nv_bfloat16>::load(v).x : Pack2<__half>::load(v).x;
-}
-__device__ __forceinline__ uint16_t from_f32(float v, int dtype) {
-  return static_cast<uint16_t>((dtype == MOE_TYPE_BF16 ? Pack2<__nv_bfloat16>::store(v, 0.f)
-                                                       : Pack2<__half>::store(v, 0.f)) & 0xFFFFu);
-}
+enum Mode { kForward, kSwiglu, kDgrad, kWgrad };
 
-// c[i, j] = sum_z a[i * ais + z * azs] b[j * bis + z * bzs], i < mi, j < mj, z < mz, for one 64x64 tile.
-struct Operand {
-  const uint16_t* p;
-  int64_t is, zs;
+constexpr int kThreads = 192;
+constexpr int kEpiWarps = 4;
+constexpr int kTileM = 256, kTileN = 256, kTileZ = 64;   // per pair; contraction elements per stage
+constexpr int kABytes = 128 * kTileZ * 2;                // per CTA and stage
+constexpr int kBBytes = 128 * kTileZ * 2;
+constexpr int kMaxE = 2048;
+
+template <Mode kMode> struct Cfg {
+  static constexpr int kStages = kMode == kWgrad ? 5 : 6;
+  static constexpr int kStoreBytes = kMode == kWgrad ? kEpiWarps * 2 * 4096 : 0;   // tensor-store staging
 };
-__device__ __forceinline__ void tile_product(const Operand a, const Operand b, int i0, int j0, int mi, int mj, int mz,
-                                             int dtype, float (&acc)[4][4], float (*sa)[65], float (*sb)[65]) {
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-  for (int z0 = 0; z0 < mz; z0 += 16) {
-    for (int u = threadIdx.x; u < 1024; u += 256) {
-      const int z = u % 16, i = u / 16;
-      sa[z][i] = i0 + i < mi && z0 + z < mz ? to_f32(a.p[(i0 + i) * a.is + (z0 + z) * a.zs], dtype) : 0.f;
-      sb[z][i] = j0 + i < mj && z0 + z < mz ? to_f32(b.p[(j0 + i) * b.is + (z0 + z) * b.zs], dtype) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int z = 0; z < 16; ++z)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] += sa[z][ty + 16 * i] * sb[z][tx + 16 * j];
-    __syncthreads();
-  }
-}
+constexpr int kMaxStages = 6;
 
-__device__ __forceinline__ bool group_of(const int32_t* start, const int32_t* rows, int e, int64_t cap, int64_t& s0,
-                                         int& n, int32_t* status, bool report) {
-  s0 = start[e];
-  n = rows[e];
+struct Ctl {
+  uint64_t full[kMaxStages];    // operands landed (the leader's counts both CTAs)
+  uint64_t empty[kMaxStages];   // the stage's MMAs are done
+  uint64_t tfull[2];            // accumulator complete
+  uint64_t tempty[2];           // (leader) accumulator drained by every epilogue warp of the pair
+  uint32_t tmem_base;
+  int abort_flag;
+  uint32_t warp_sum[kThreads / 32];
+  uint32_t first[kMaxE + 1];    // tiles before each group
+};
+
+template <Mode kMode>
+constexpr size_t smem_bytes() {
+  return 1024 + static_cast<size_t>(Cfg<kMode>::kStages) * (kABytes + kBBytes) + Cfg<kMode>::kStoreBytes + sizeof(Ctl);
+}
+static_assert(smem_bytes<kForward>() <= 232448 && smem_bytes<kWgrad>() <= 232448, "shared memory budget");
+
+struct Params {
+  const int32_t* group_start;
+  const int32_t* group_rows;
+  const int32_t* route_ids;
+  const float* route_weights;
+  int32_t* status;
+  uint16_t* y;
+  uint16_t* pre;
+  int64_t ldy, ldpre, R;
+  int rows;        // slots of the row buffers
+  int E;
+  int m;           // M extent of the products (2I for SwiGLU)
+  int z;           // contraction extent (0 for wgrad: the group's slots)
+  int n;           // wgrad: N extent
+  uint32_t format; // 0 FP16, 1 BF16
+  int accumulate;  // wgrad: add to dw, leave the dw of empty groups
+};
+
+struct Tile {
+  int e, m0;       // group, first row of the M side
+  int n0, nt;      // first column of the N side, its width
+  int s0, slots;   // the group's first slot and its slots
+  int nkb;         // contraction blocks
+};
+
+// A group's slots; a group outside the buffer counts as empty.
+__device__ __forceinline__ bool group_at(const Params& p, int e, int& s0, int& n) {
+  s0 = p.group_start[e];
+  n = p.group_rows[e];
   if (n == 0) return true;
-  if (s0 < 0 || n < 0 || s0 + n > cap) {
-    if (report && status) atomicOr(status, MOE_DEV_BAD_GROUP);
+  if (s0 < 0 || n < 0 || s0 > p.rows - n) {
     n = 0;
     return false;
   }
   return true;
 }
-
-__global__ void __launch_bounds__(256) grouped_simple_kernel(const moe_grouped_args a) {
-  __shared__ float sa[16][65], sb[16][65];
-  __shared__ float sg[64][65];
-  pdl_wait();
-  const int e = blockIdx.z;
-  int64_t s0;
-  int n;
-  group_of(a.group_start, a.group_rows, e, a.rows, s0, n, a.device_status, threadIdx.x == 0);
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  const bool fwd = a.direction == MOE_GROUPED_FORWARD, glu = a.epilogue == MOE_GROUPED_SWIGLU;
-  const int cols = fwd ? (glu ? a.N / 2 : a.N) : a.K, depth = fwd ? a.K : a.N;
-  const int j0 = blockIdx.x * 64;
-  const uint16_t* we = a.w + static_cast<int64_t>(e) * a.N * a.K;
-  for (int i0 = blockIdx.y * 64; i0 < n; i0 += 64 * gridDim.y) {
-    float acc[4][4];
-    const Operand x = {a.x + s0 * a.ldx, a.ldx, 1};
-    const Operand w = {we, fwd ? a.K : 1, fwd ? 1 : a.K};
-    tile_product(x, w, i0, j0, n, cols, depth, a.dtype, acc, sa, sb);
-    if (glu) {
-      for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) sg[ty + 16 * i][tx + 16 * j] = acc[i][j];
-      __syncthreads();
-      const Operand up = {we + static_cast<int64_t>(cols) * a.K, a.K, 1};
-      tile_product(x, up, i0, j0, n, cols, depth, a.dtype, acc, sa, sb);
-    }
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 4; ++j) {
-        const int ri = i0 + ty + 16 * i, c = j0 + tx + 16 * j;
-        if (ri >= n || c >= cols) continue;
-        const int64_t s = s0 + ri;
-        if (!glu) {
-          a.y[s * a.ldy + c] = from_f32(acc[i][j], a.dtype);
-          continue;
-        }
-        const float g = sg[ty + 16 * i][tx + 16 * j], u = acc[i][j];
-        float wt = 1.f;
-        if (a.route_weights) {
-          int64_t r = s;
-          if (a.route_ids) r = a.route_ids[s];
-          wt = a.route_ids && (r < 0 || r >= a.R) ? 0.f : a.route_weights[r];
-        }
-        a.y[s * a.ldy + c] = from_f32(silu_f32(g) * u * wt, a.dtype);
-        if (a.pre) {
-          a.pre[s * a.ldpre + c] = from_f32(g, a.dtype);
-          a.pre[s * a.ldpre + cols + c] = from_f32(u, a.dtype);
-        }
-      }
-    __syncthreads();
-  }
+template <Mode kMode>
+__device__ __forceinline__ uint32_t tiles_of(const Params& p, int n) {
+  const uint32_t mt = (p.m + kTileM - 1) / kTileM;
+  if (kMode == kWgrad) return n == 0 && p.accumulate ? 0u : mt * ((p.n + kTileN - 1) / kTileN);
+  return mt * ((n + kTileN - 1) / kTileN);
 }
 
-__global__ void __launch_bounds__(256) wgrad_simple_kernel(const moe_grouped_wgrad_args a) {
-  __shared__ float sa[16][65], sb[16][65];
+// Fills ctl->first (all threads).
+template <Mode kMode>
+__device__ __forceinline__ void count_tiles(const Params& p, Ctl* ctl) {
+  const int per = (p.E + kThreads - 1) / kThreads;
+  const int e0 = min(static_cast<int>(threadIdx.x) * per, p.E), e1 = min(e0 + per, p.E);
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  uint32_t sum = 0;
+  bool bad = false;
+  for (int e = e0; e < e1; ++e) {
+    int s0, n;
+    bad |= !group_at(p, e, s0, n);
+    const uint32_t t = tiles_of<kMode>(p, n);
+    ctl->first[e] = sum;
+    sum += t;
+  }
+  if (bad && blockIdx.x == 0 && p.status) atomicOr(p.status, MOE_DEV_BAD_GROUP);
+  uint32_t inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) ctl->warp_sum[warp] = inc;
+  __syncthreads();
+  uint32_t base = inc - sum;
+  for (int w = 0; w < warp; ++w) base += ctl->warp_sum[w];
+  for (int e = e0; e < e1; ++e) ctl->first[e] += base;
+  if (threadIdx.x == kThreads - 1) ctl->first[p.E] = base + sum;
+}
+
+template <Mode kMode>
+__device__ __forceinline__ Tile tile_at(const Params& p, const Ctl* ctl, uint32_t tile) {
+  int lo = 0, hi = p.E;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (ctl->first[mid] <= tile) lo = mid; else hi = mid;
+  }
+  Tile t;
+  t.e = lo;
+  group_at(p, lo, t.s0, t.slots);
+  const int local = static_cast<int>(tile - ctl->first[lo]);
+  if (kMode == kWgrad) {
+    const int nts = (p.n + kTileN - 1) / kTileN;
+    t.m0 = local / nts * kTileM;
+    t.n0 = local % nts * kTileN;
+    t.nt = min(kTileN, p.n - t.n0);
+    t.nkb = (t.slots + kTileZ - 1) / kTileZ;
+  } else {
+    const int nts = (t.slots + kTileN - 1) / kTileN;
+    const int width = ((t.slots + nts - 1) / nts + 31) / 32 * 32;
+    t.m0 = local / nts * kTileM;
+    t.n0 = local % nts * width;
+    t.nt = min(width, t.slots - t.n0);
+    t.nkb = (p.z + kTileZ - 1) / kTileZ;
+  }
+  return t;
+}
+
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  int ok = 0;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag) ? 1 : 0;
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+// Bounded wait while winding down: ignores the abort flag.
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
+  int dummy = 0;
+  mbar_wait(bar, parity, &dummy);
+}
+
+// Two values that this lane holds for columns c and c + 1 of its row, against
+// the neighbour's: the even lane returns rows (lane, lane + 1) of column c,
+// the odd lane rows (lane - 1, lane) of column c + 1.
+template <typename T>
+__device__ __forceinline__ uint32_t pair_rows(float v0, float v1, bool odd) {
+  const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+  return odd ? Pack2<T>::store(got, v1) : Pack2<T>::store(v0, got);
+}
+
+template <Mode kMode, typename T, typename Out>
+__global__ void __launch_bounds__(kThreads, 1)
+    grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const __grid_constant__ CUtensorMap tmAg, const __grid_constant__ CUtensorMap tmBg,
+                   const __grid_constant__ CUtensorMap tmC, const Params p) {
+  constexpr int kStages = Cfg<kMode>::kStages;
+  constexpr bool kAmn = kMode == kDgrad || kMode == kWgrad;   // A stored along M
+  constexpr bool kBmn = kMode == kWgrad;                      // B stored along N
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sA = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sB = sA + kStages * kABytes;
+  uint8_t* sC = sB + kStages * kBBytes;
+  Ctl* ctl = reinterpret_cast<Ctl*>(sC + Cfg<kMode>::kStoreBytes);
+  volatile int* abort_flag = &ctl->abort_flag;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = pair::cluster_rank();
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(smem_u32(&ctl->full[s]), 1);
+      mbar_init(smem_u32(&ctl->empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&ctl->tfull[b]), 1);
+      mbar_init(smem_u32(&ctl->tempty[b]), 2 * kEpiWarps);
+    }
+    ctl->abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) {
+    pair::tmem_alloc(smem_u32(&ctl->tmem_base), 512);
+    pair::tmem_relinquish();
+  }
+  pdl_launch_dependents();
   pdl_wait();
-  const int e = blockIdx.z;
-  int64_t s0;
-  int n;
-  group_of(a.group_start, a.group_rows, e, a.rows, s0, n, a.device_status, threadIdx.x == 0);
-  if (n == 0 && a.accumulate) return;
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
-  float acc[4][4];
-  tile_product({a.dy + s0 * a.lddy, 1, a.lddy}, {a.x + s0 * a.ldx, 1, a.ldx}, i0, j0, a.N, a.K, n, a.dtype, acc, sa, sb);
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int r = i0 + ty + 16 * i, c = j0 + tx + 16 * j;
-      if (r >= a.N || c >= a.K) continue;
-      const int64_t o = (static_cast<int64_t>(e) * a.N + r) * a.K + c;
-      if (a.dw_dtype == MOE_TYPE_FP32) {
-        float* d = static_cast<float*>(a.dw) + o;
-        *d = a.accumulate ? *d + acc[i][j] : acc[i][j];
-      } else {
-        static_cast<uint16_t*>(a.dw)[o] = from_f32(acc[i][j], a.dtype);
+  count_tiles<kMode>(p, ctl);
+  tc_fence_before();
+  __syncthreads();
+  pair::cluster_sync();  // the peer's copies and arrivals target initialised barriers
+  tc_fence_after();
+  const uint32_t tmem_base = ctl->tmem_base;
+  const uint32_t total = ctl->first[p.E];
+  const uint32_t tile0 = blockIdx.x / 2, step = gridDim.x / 2;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    const uint32_t lead_full0 = pair::mapa_shared(smem_u32(&ctl->full[0]), 0);
+    uint32_t it = 0;
+    bool ok = true;
+    for (uint32_t tile = tile0; tile < total && ok; tile += step) {
+      const Tile t = tile_at<kMode>(p, ctl, tile);
+      const int half = (t.nt + 31) / 32 * 16;               // N columns of each CTA
+      const int bbox = kBmn ? (half + 63) / 64 : (half + 31) / 32;
+      const uint32_t bytes = 2u * (kABytes + static_cast<uint32_t>(bbox) * (kBmn ? 8192u : 4096u));
+      const int arow = t.m0 + 128 * static_cast<int>(rank), bcol = t.n0 + static_cast<int>(rank) * half;
+      for (int kb = 0; kb < t.nkb; ++kb, ++it) {
+        const int s = it % kStages;
+        if (!warp_wait(smem_u32(&ctl->empty[s]), ((it / kStages) & 1u) ^ 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const uint32_t full = lead_full0 + 8u * s;
+        const uint32_t a = smem_u32(sA + s * kABytes), b = smem_u32(sB + s * kBBytes);
+        const int z = kb * kTileZ;
+        if (lane == 0 && rank == 0) mbar_arrive_expect_tx(smem_u32(&ctl->full[s]), bytes);
+        if (kMode == kWgrad && t.slots - z < kTileZ) {
+          // the group's last slots: the rows past them (the next group's) read as zeros
+          const int r0 = (lane & 15) * 4;
+          int r[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) r[i] = z + r0 + i < t.slots ? t.s0 + z + r0 + i : -1;
+          const uint32_t at = (lane & 15) * 512u;
+          if (lane < 16) {
+            pair::gather4(a + at, &tmAg, full, arow, r[0], r[1], r[2], r[3]);
+            pair::gather4(a + 8192u + at, &tmAg, full, arow + 64, r[0], r[1], r[2], r[3]);
+          } else {
+            for (int j = 0; j < bbox; ++j)
+              pair::gather4(b + 8192u * j + at, &tmBg, full, bcol + 64 * j, r[0], r[1], r[2], r[3]);
+          }
+          __syncwarp();
+        } else if (lane == 0) {
+          if (kMode == kForward) {
+            pair::load_3d(a, &tmA, full, z, arow, t.e);
+          } else if (kMode == kSwiglu) {
+            // 64 gates and their ups: 16 and 16 in turn
+            const int i0 = t.m0 / 2 + 64 * static_cast<int>(rank);
+            for (int j = 0; j < 4; ++j) pair::load_4d(a + 4096u * j, &tmA, full, z, i0 + 16 * j, 0, t.e);
+          } else if (kMode == kDgrad) {
+            pair::load_3d(a, &tmA, full, arow, z, t.e);
+            pair::load_3d(a + 8192u, &tmA, full, arow + 64, z, t.e);
+          } else {
+            pair::load_2d(a, &tmA, full, arow, t.s0 + z);
+            pair::load_2d(a + 8192u, &tmA, full, arow + 64, t.s0 + z);
+          }
+          if (kBmn) {
+            for (int j = 0; j < bbox; ++j) pair::load_2d(b + 8192u * j, &tmB, full, bcol + 64 * j, t.s0 + z);
+          } else {
+            for (int j = 0; j < bbox; ++j) pair::load_2d(b + 4096u * j, &tmB, full, z, t.s0 + bcol + 32 * j);
+          }
+        }
       }
     }
+    // wind down: let the copies already issued land before the CTA exits
+    if (!ok && lane == 0 && rank == 0)
+      for (uint32_t j = (it > kStages ? it - kStages : 0); j < it; ++j)
+        drain_wait(smem_u32(&ctl->full[j % kStages]), (j / kStages) & 1u);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (leader)
+    if (lane == 0 && rank == 0) {
+      uint32_t it = 0, done = 0;
+      bool ok = true;
+      for (uint32_t tile = tile0; tile < total && ok; tile += step) {
+        const Tile t = tile_at<kMode>(p, ctl, tile);
+        if (t.nkb == 0) continue;
+        const uint32_t idesc = pair::idesc_f16(p.format, kAmn, kBmn, (t.nt + 31) / 32 * 32);
+        const uint32_t tb = done & 1u, d = tmem_base + tb * kTileN;
+        if (!mbar_wait(smem_u32(&ctl->tempty[tb]), ((done >> 1) & 1u) ^ 1u, abort_flag)) break;
+        tc_fence_after();
+        for (int kb = 0; kb < t.nkb; ++kb, ++it) {
+          const int s = it % kStages;
+          if (!mbar_wait(smem_u32(&ctl->full[s]), (it / kStages) & 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = smem_u32(sA + s * kABytes), b = smem_u32(sB + s * kBBytes);
+#pragma unroll
+          for (int kk = 0; kk < kTileZ / 16; ++kk)
+            pair::umma_f16(d, kAmn ? pair::sw128_mnmajor_desc(a + 2048u * kk, 8192u) : sw128_kmajor_desc(a + 32u * kk),
+                           kBmn ? pair::sw128_mnmajor_desc(b + 2048u * kk, 8192u) : sw128_kmajor_desc(b + 32u * kk),
+                           idesc, kb > 0 || kk > 0 ? 1u : 0u);
+          pair::umma_commit(smem_u32(&ctl->empty[s]));
+        }
+        if (ok) {
+          pair::umma_commit(smem_u32(&ctl->tfull[tb]));
+          ++done;
+        }
+      }
+      // no MMA may still be writing TMEM when it is released
+      if (it > 0) drain_wait(smem_u32(&ctl->empty[(it - 1) % kStages]), ((it - 1) / kStages) & 1u);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;   // the lanes of tensor memory that this warp may read
+    const uint32_t lanes = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
+    const bool odd = lane & 1;
+    uint32_t done = 0;
+    bool ok = true;
+    for (uint32_t tile = tile0; tile < total && ok; tile += step) {
+      const Tile t = tile_at<kMode>(p, ctl, tile);
+      const uint32_t tb = done & 1u;
+      if (t.nkb > 0) {
+        ok = warp_wait(smem_u32(&ctl->tfull[tb]), (done >> 1) & 1u, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const uint32_t acc = lanes + tb * kTileN;
+      if (kMode == kForward || kMode == kDgrad) {
+        const int row = t.m0 + 128 * static_cast<int>(rank) + 32 * q + (lane & ~1);
+        uint16_t* out = p.y + (static_cast<int64_t>(t.s0) + t.n0) * p.ldy + row;
+        for (int c = 0; c < t.nt; c += 32) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(acc + c, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const uint32_t w = pair_rows<T>(__uint_as_float(v[j]), __uint_as_float(v[j + 1]), odd);
+            const int col = c + j + (odd ? 1 : 0);
+            if (col < t.nt && row < p.m) *reinterpret_cast<uint32_t*>(out + col * p.ldy) = w;
+          }
+        }
+      } else if (kMode == kSwiglu) {
+        const int I = p.m / 2;
+        const bool up = lane >= 16;
+        const int i = t.m0 / 2 + 64 * static_cast<int>(rank) + 16 * q + (lane & 14);   // even row of the lane's pair
+        const int64_t s0 = static_cast<int64_t>(t.s0) + t.n0;
+        for (int c = 0; c < t.nt; c += 32) {
+          float wt = 1.f;   // of this lane's slot
+          if (p.route_weights && c + lane < t.nt) {
+            int64_t r = s0 + c + lane;
+            if (p.route_ids) r = p.route_ids[r];
+            wt = p.route_ids && (r < 0 || r >= p.R) ? 0.f : p.route_weights[r];
+          }
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(acc + c, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            float h[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              // gate lanes finish the even slot, up lanes the odd one
+              const float v0 = __uint_as_float(v[j + 2 * k]), v1 = __uint_as_float(v[j + 2 * k + 1]);
+              const float got = __shfl_xor_sync(0xffffffffu, up ? v0 : v1, 16);
+              const float g = up ? got : v0, u = up ? v1 : got;
+              const float ws = __shfl_sync(0xffffffffu, wt, j + 2 * k + (up ? 1 : 0));
+              h[k] = g * sigmoid_f32(g) * u * ws;
+              if (p.pre) {
+                const uint32_t w = pair_rows<T>(v0, v1, odd);
+                const int col = c + j + 2 * k + (odd ? 1 : 0);
+                if (col < t.nt && i < I)
+                  *reinterpret_cast<uint32_t*>(p.pre + (s0 + col) * p.ldpre + (up ? I : 0) + i) = w;
+              }
+            }
+            // h[0], h[1]: slots j, j + 2 (gate lanes) or j + 1, j + 3 (up lanes)
+            const uint32_t w = pair_rows<T>(h[0], h[1], odd);
+            const int col = c + j + (odd ? 2 : 0) + (up ? 1 : 0);
+            if (col < t.nt && i < I) *reinterpret_cast<uint32_t*>(p.y + (s0 + col) * p.ldy + i) = w;
+          }
+        }
+      } else {
+        // rows of dw through shared memory (128-byte swizzle) and tensor stores
+        constexpr int kCols = 128 / sizeof(Out);   // columns of one 128-byte box row
+        const int row0 = t.m0 + 128 * static_cast<int>(rank) + 32 * q;
+        for (int c = 0; c < t.nt; c += kCols) {
+          uint8_t* box = sC + ((warp - 2) * 2 + ((c / kCols) & 1)) * 4096;
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          __syncwarp();
+#pragma unroll
+          for (int h = 0; h < kCols / 32; ++h) {
+            uint32_t v[32];
+            if (t.nkb > 0) {
+              tmem_ld_32x32b_x32(acc + c + 32 * h, v);
+              tmem_wait_ld();
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = 0u;
+            }
+            if (sizeof(Out) == 4) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<uint4*>(box + 128 * lane + 16 * (k ^ (lane & 7))) =
+                    make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                float f[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(v[8 * k + j]);
+                *reinterpret_cast<uint4*>(box + 128 * lane + 16 * ((4 * h + k) ^ (lane & 7))) = pack8<T>(f);
+              }
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (row0 < p.m) {
+              if (p.accumulate)
+                pair::reduce_add_3d(&tmC, smem_u32(box), t.n0 + c, row0, t.e);
+              else
+                pair::store_3d(&tmC, smem_u32(box), t.n0 + c, row0, t.e);
+            }
+            bulk_commit();
+          }
+        }
+      }
+      if (t.nkb > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (rank == 1)
+            pair::mbar_arrive_cluster(pair::mapa_shared(smem_u32(&ctl->tempty[tb]), 0));
+          else
+            mbar_arrive(smem_u32(&ctl->tempty[tb]));
+        }
+        ++done;
+      }
+    }
+    if (kMode == kWgrad && lane == 0) bulk_wait_all();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  pair::cluster_sync();  // neither CTA leaves while the pair still touches its memory
+  tc_fence_after();
+  if (threadIdx.x == 0 && ctl->abort_flag && p.status) atomicOr(p.status, MOE_DEV_TIMEOUT);
+  if (warp == 1) pair::tmem_dealloc(tmem_base, 512);
+}
+
+// Launches the kernel with as many pairs as there can be tiles, at most as many
+// as the GPU holds at once (a larger persistent grid would run a second wave).
+template <Mode kMode, typename T, typename Out>
+moe_status launch_grouped(int64_t most_tiles, const DeviceInfo& dev, cudaStream_t stream,
+                          const CUtensorMap (&maps)[5], const Params& p) {
+  constexpr auto kernel = grouped_kernel<kMode, T, Out>;
+  constexpr size_t smem = smem_bytes<kMode>();
+  static std::mutex mu;
+  static int pairs[64] = {};
+  int n;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (pairs[dev.device] == 0) {
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
+          cudaSuccess)
+        return MOE_ERR_CUDA;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(dev.sms / 2 * 2));
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = smem;
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = 2;
+      attr.val.clusterDim.y = 1;
+      attr.val.clusterDim.z = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      int fit = 0;
+      if (cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg) != cudaSuccess || fit < 1) {
+        cudaGetLastError();
+        return MOE_ERR_CUDA;
+      }
+      pairs[dev.device] = fit;
+    }
+    n = pairs[dev.device];
+  }
+  if (most_tiles < n) n = static_cast<int>(most_tiles);
+  MOE_CUDA_TRY(launch_pdl(kernel, dim3(2u * n), dim3(kThreads), smem, stream, 2, maps[0], maps[1], maps[2], maps[3],
+                          maps[4], p));
+  return MOE_OK;
+}
+
+CUtensorMapDataType map_type(int dtype) {
+  return dtype == MOE_TYPE_BF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+         : dtype == MOE_TYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                  : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+}
+// Rows of `width` 16-bit elements, boxes of 64 elements (128 bytes) by `box_rows`.
+bool rows_map(CUtensorMap* m, int dtype, const void* base, int64_t width, int64_t rows, int64_t ld, uint32_t box_rows) {
+  return encode_tensor_map_2d_typed(m, map_type(dtype), base, static_cast<uint64_t>(width),
+                                    static_cast<uint64_t>(rows), static_cast<uint64_t>(ld) * 2, 64, box_rows,
+                                    CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
+}
+// A dense [e, n, k] tensor.
+bool weight_map(CUtensorMap* m, int dtype, const void* base, int64_t e, int64_t n, int64_t k, uint32_t box_k,
+                uint32_t box_n) {
+  const uint64_t eb = static_cast<uint64_t>(type_bytes(dtype));
+  const uint64_t dims[3] = {static_cast<uint64_t>(k), static_cast<uint64_t>(n), static_cast<uint64_t>(e)};
+  const uint64_t strides[2] = {dims[0] * eb, dims[0] * dims[1] * eb};
+  const uint32_t box[3] = {box_k, box_n, 1};
+  return encode_tensor_map(m, map_type(dtype), 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ==
+         CUDA_SUCCESS;
 }
 
 bool ok_sizes(int64_t rows, int E, int N, int K) {
@@ -168,12 +564,47 @@ moe_status moe_grouped_gemm(const moe_grouped_args* a, moe_stream_t stream) {
                         glu ? a->route_ids : nullptr, glu ? a->route_weights : nullptr, a->device_status};
   for (const void* p : ptrs)
     if (p && !on_device(p, dev.device)) return MOE_ERR_DEVICE;
-  moe_grouped_args k = *a;
-  if (!glu) k.route_ids = nullptr, k.route_weights = nullptr, k.pre = nullptr;
-  const unsigned gy = static_cast<unsigned>(a->rows < 64 * 16 ? ceil_div(a->rows, 64) : 16);
-  MOE_CUDA_TRY(launch_pdl(grouped_simple_kernel, dim3(static_cast<unsigned>(ceil_div(out, 64)), gy, a->E), dim3(256), 0,
-                          stream, 1, k));
-  return MOE_OK;
+  Params p = {};
+  p.group_start = a->group_start;
+  p.group_rows = a->group_rows;
+  p.route_ids = glu && a->route_weights ? a->route_ids : nullptr;
+  p.route_weights = glu ? a->route_weights : nullptr;
+  p.status = a->device_status;
+  p.y = a->y;
+  p.pre = pre ? a->pre : nullptr;
+  p.ldy = a->ldy;
+  p.ldpre = a->ldpre;
+  p.R = a->R;
+  p.rows = static_cast<int>(a->rows);
+  p.E = a->E;
+  p.m = fwd ? a->N : a->K;
+  p.z = fwd ? a->K : a->N;
+  p.format = a->dtype == MOE_TYPE_BF16 ? 1u : 0u;
+  CUtensorMap maps[5];
+  bool ok = rows_map(&maps[1], a->dtype, a->x, in, a->rows, a->ldx, 32);
+  if (glu) {
+    const uint64_t K = static_cast<uint64_t>(a->K), I = static_cast<uint64_t>(a->N) / 2;
+    const uint64_t dims[4] = {K, I, 2, static_cast<uint64_t>(a->E)};
+    const uint64_t strides[3] = {2 * K, 2 * K * I, 4 * K * I};
+    const uint32_t box[4] = {64, 16, 2, 1};
+    ok = ok && encode_tensor_map(&maps[0], map_type(a->dtype), 4, a->w, dims, strides, box,
+                                 CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
+  } else {
+    ok = ok && weight_map(&maps[0], a->dtype, a->w, a->E, a->N, a->K, 64, fwd ? 128 : 64);
+  }
+  if (!ok) return MOE_ERR_CUDA;
+  maps[2] = maps[3] = maps[4] = maps[1];  // not used
+  const int64_t mt = ceil_div(p.m, kTileM);
+  const int64_t most = mt * (ceil_div(a->rows, kTileN) + (a->E < a->rows ? a->E : a->rows));
+  const bool bf = a->dtype == MOE_TYPE_BF16;
+  if (glu)
+    return bf ? launch_grouped<kSwiglu, __nv_bfloat16, __nv_bfloat16>(most, dev, stream, maps, p)
+              : launch_grouped<kSwiglu, __half, __half>(most, dev, stream, maps, p);
+  if (fwd)
+    return bf ? launch_grouped<kForward, __nv_bfloat16, __nv_bfloat16>(most, dev, stream, maps, p)
+              : launch_grouped<kForward, __half, __half>(most, dev, stream, maps, p);
+  return bf ? launch_grouped<kDgrad, __nv_bfloat16, __nv_bfloat16>(most, dev, stream, maps, p)
+            : launch_grouped<kDgrad, __half, __half>(most, dev, stream, maps, p);
 }
 
 moe_status moe_grouped_wgrad(const moe_grouped_wgrad_args* a, moe_stream_t stream) {
@@ -195,11 +626,34 @@ moe_status moe_grouped_wgrad(const moe_grouped_wgrad_args* a, moe_stream_t strea
   const void* ptrs[] = {a->dy, a->x, a->dw, a->group_start, a->group_rows, a->device_status};
   for (const void* p : ptrs)
     if (p && !on_device(p, dev.device)) return MOE_ERR_DEVICE;
-  MOE_CUDA_TRY(launch_pdl(wgrad_simple_kernel,
-                          dim3(static_cast<unsigned>(ceil_div(a->K, 64)), static_cast<unsigned>(ceil_div(a->N, 64)),
-                               static_cast<unsigned>(a->E)),
-                          dim3(256), 0, stream, 1, *a));
-  return MOE_OK;
+  Params p = {};
+  p.group_start = a->group_start;
+  p.group_rows = a->group_rows;
+  p.status = a->device_status;
+  p.rows = static_cast<int>(a->rows);
+  p.E = a->E;
+  p.m = a->N;
+  p.n = a->K;
+  p.format = a->dtype == MOE_TYPE_BF16 ? 1u : 0u;
+  p.accumulate = a->accumulate ? 1 : 0;
+  // without slots every group is empty and nothing is read: any address will do
+  const void* dy = a->rows > 0 ? a->dy : static_cast<const uint16_t*>(a->dw);
+  const void* x = a->rows > 0 ? a->x : static_cast<const uint16_t*>(a->dw);
+  const int64_t rows = a->rows > 0 ? a->rows : 1;
+  CUtensorMap maps[5];
+  if (!rows_map(&maps[0], a->dtype, dy, a->N, rows, a->lddy, 64) ||
+      !rows_map(&maps[1], a->dtype, x, a->K, rows, a->ldx, 64) ||
+      !rows_map(&maps[2], a->dtype, dy, a->N, rows, a->lddy, 1) ||
+      !rows_map(&maps[3], a->dtype, x, a->K, rows, a->ldx, 1) ||
+      !weight_map(&maps[4], a->dw_dtype, a->dw, a->E, a->N, a->K, a->dw_dtype == MOE_TYPE_FP32 ? 32 : 64, 32))
+    return MOE_ERR_CUDA;
+  const int64_t most = static_cast<int64_t>(a->E) * ceil_div(p.m, kTileM) * ceil_div(p.n, kTileN);
+  const bool bf = a->dtype == MOE_TYPE_BF16;
+  if (a->dw_dtype == MOE_TYPE_FP32)
+    return bf ? launch_grouped<kWgrad, __nv_bfloat16, float>(most, dev, stream, maps, p)
+              : launch_grouped<kWgrad, __half, float>(most, dev, stream, maps, p);
+  return bf ? launch_grouped<kWgrad, __nv_bfloat16, __nv_bfloat16>(most, dev, stream, maps, p)
+            : launch_grouped<kWgrad, __half, __half>(most, dev, stream, maps, p);
 }
 
 }  // extern "C"
