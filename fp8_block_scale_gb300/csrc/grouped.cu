@@ -12,13 +12,14 @@
 //
 //   mode     M (A operand)            N (B operand)     contraction
 //   forward  w rows n, K-major        slots, K-major    K
-//   SwiGLU   w rows, gate and up in alternating groups of 16 (a warp's lanes
-//            0-15 hold gates, lanes 16-31 the matching ups)
+//   SwiGLU   w rows, gate and up in alternating groups of 8 (a warp's lanes
+//            0-7 and 16-23 hold gates, the eight lanes after each the ups)
 //   dgrad    w columns k, M-major     slots, K-major    N
 //   wgrad    dy columns n, M-major    x columns k, N-major   slots of the group
 //
-// Warps of each CTA: 0 issues the tensor copies, 1 (of the leader) the MMAs,
-// 2-5 drain the accumulators.  Two 256-column accumulators let the drain of
+// Warps of each CTA: 0 issues A's tensor copies, 6 those of B (one thread
+// issues a copy every ~0.1-0.2 us whatever its size, so a stage is one 16 KB
+// copy of each), 1 (of the leader) the MMAs, 2-5 drain the accumulators.  Two 256-column accumulators let the drain of
 // one tile overlap the products of the next.  The CTAs are persistent: the
 // tiles of all groups form one sequence, dealt round-robin to the pairs.
 #include <mutex>
@@ -31,7 +32,7 @@ namespace {
 
 enum Mode { kForward, kSwiglu, kDgrad, kWgrad };
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 224;
 constexpr int kEpiWarps = 4;
 constexpr int kTileM = 256, kTileN = 256, kTileZ = 64;   // per pair; contraction elements per stage
 constexpr int kABytes = 128 * kTileZ * 2;                // per CTA and stage
@@ -77,6 +78,15 @@ struct Params {
   int n;           // wgrad: N extent
   uint32_t format; // 0 FP16, 1 BF16
   int accumulate;  // wgrad: add to dw, leave the dw of empty groups
+  int a_one, b_one; // an MN-major stage of A, B is one copy (its width a multiple of 64), else one per 64 columns
+};
+
+// The tensors of a launch.
+struct Maps {
+  CUtensorMap a;
+  CUtensorMap b[3];    // K-major B: boxes of 32, 64 and 128 slots; wgrad: [0]
+  CUtensorMap ag, bg;  // wgrad: single rows, for gather4
+  CUtensorMap c;       // wgrad: dw
 };
 
 struct Tile {
@@ -184,9 +194,7 @@ __device__ __forceinline__ uint32_t pair_rows(float v0, float v1, bool odd) {
 
 template <Mode kMode, typename T, typename Out>
 __global__ void __launch_bounds__(kThreads, 1)
-    grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                   const __grid_constant__ CUtensorMap tmAg, const __grid_constant__ CUtensorMap tmBg,
-                   const __grid_constant__ CUtensorMap tmC, const Params p) {
+    grouped_kernel(const __grid_constant__ Maps maps, const Params p) {
   constexpr int kStages = Cfg<kMode>::kStages;
   constexpr bool kAmn = kMode == kDgrad || kMode == kWgrad;   // A stored along M
   constexpr bool kBmn = kMode == kWgrad;                      // B stored along N
@@ -210,8 +218,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     ctl->abort_flag = 0;
     fence_barrier_init();
-    tma_prefetch_desc(&tmA);
-    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&maps.a);
+    tma_prefetch_desc(&maps.b[0]);
   }
   if (warp == 1) {
     pair::tmem_alloc(smem_u32(&ctl->tmem_base), 512);
@@ -228,68 +236,92 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t total = ctl->first[p.E];
   const uint32_t tile0 = blockIdx.x / 2, step = gridDim.x / 2;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
+  if (warp == 0 || warp == 6) {
+    // ------------------------------------------------------------ producers (A: warp 0, B: warp 6)
+    const bool isA = warp == 0;
     const uint32_t lead_full0 = pair::mapa_shared(smem_u32(&ctl->full[0]), 0);
     uint32_t it = 0;
     bool ok = true;
-    for (uint32_t tile = tile0; tile < total && ok; tile += step) {
+    // lane 0 issues; wgrad's other lanes come along for the row-by-row copies
+    for (uint32_t tile = tile0; tile < total && ok && (kMode == kWgrad || lane == 0); tile += step) {
       const Tile t = tile_at<kMode>(p, ctl, tile);
       const int half = (t.nt + 31) / 32 * 16;               // N columns of each CTA
-      const int bbox = kBmn ? (half + 63) / 64 : (half + 31) / 32;
-      const uint32_t bytes = 2u * (kABytes + static_cast<uint32_t>(bbox) * (kBmn ? 8192u : 4096u));
+      const int chunks = (half + 63) / 64;                  // N-major B: 64-column boxes
+      const int bsel = half <= 32 ? 0 : half <= 64 ? 1 : 2; // K-major B: box of 32, 64 or 128 slots
+      const uint32_t bbytes = kBmn ? 8192u * (p.b_one ? 2 : chunks) : 4096u << bsel;
       const int arow = t.m0 + 128 * static_cast<int>(rank), bcol = t.n0 + static_cast<int>(rank) * half;
-      for (int kb = 0; kb < t.nkb; ++kb, ++it) {
-        const int s = it % kStages;
-        if (!warp_wait(smem_u32(&ctl->empty[s]), ((it / kStages) & 1u) ^ 1u, abort_flag)) {
+      // wgrad: a last block inside the buffer's first 64 slots cannot be a window that ends with the group
+      const int last = kMode == kWgrad && t.slots % kTileZ && t.s0 + t.slots < kTileZ ? t.nkb - 1 : t.nkb;
+      if (lane == 0) {
+        for (int kb = 0; kb < last; ++kb, ++it) {
+          const int s = it % kStages;
+          if (!mbar_wait(smem_u32(&ctl->empty[s]), ((it / kStages) & 1u) ^ 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t full = lead_full0 + 8u * s;
+          const uint32_t dst = smem_u32((isA ? sA : sB) + s * (isA ? kABytes : kBBytes));
+          const int z = kb * kTileZ;
+          if (isA && rank == 0) mbar_arrive_expect_tx(smem_u32(&ctl->full[s]), 2u * (kABytes + bbytes));
+          if (kMode == kWgrad) {
+            // a window of 64 slots that ends where the group does: the rest reads as zeros
+            const int have = min(kTileZ, t.slots - z), w0 = kTileZ - have, start = t.s0 + z - w0;
+            if (isA) {
+              if (p.a_one)
+                pair::load_4d(dst, &maps.a, full, 0, w0, arow / 64, start);
+              else
+                for (int j = 0; j < 2; ++j) pair::load_3d(dst + 8192u * j, &maps.a, full, arow + 64 * j, w0, start);
+            } else if (p.b_one) {
+              pair::load_4d(dst, &maps.b[0], full, 0, w0, bcol / 64, start);
+            } else {
+              for (int j = 0; j < chunks; ++j)
+                pair::load_3d(dst + 8192u * j, &maps.b[0], full, bcol + 64 * j, w0, start);
+            }
+          } else if (!isA) {
+            pair::load_2d(dst, &maps.b[bsel], full, z, t.s0 + bcol);
+          } else if (kMode == kForward) {
+            pair::load_3d(dst, &maps.a, full, z, arow, t.e);
+          } else if (kMode == kSwiglu) {
+            pair::load_5d(dst, &maps.a, full, z, 0, 0, arow / 16, t.e);
+          } else if (p.a_one) {
+            pair::load_4d(dst, &maps.a, full, 0, z, arow / 64, t.e);
+          } else {
+            for (int j = 0; j < 2; ++j) pair::load_3d(dst + 8192u * j, &maps.a, full, arow + 64 * j, z, t.e);
+          }
+        }
+      }
+      if (kMode == kWgrad) {
+        it = __shfl_sync(0xffffffffu, it, 0);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+      }
+      if (kMode == kWgrad && last < t.nkb) {
+        // row by row instead; row -1 reads as zeros
+        const int s = it % kStages, z = last * kTileZ;
+        if (!ok || !warp_wait(smem_u32(&ctl->empty[s]), ((it / kStages) & 1u) ^ 1u, abort_flag)) {
           ok = false;
           break;
         }
         const uint32_t full = lead_full0 + 8u * s;
-        const uint32_t a = smem_u32(sA + s * kABytes), b = smem_u32(sB + s * kBBytes);
-        const int z = kb * kTileZ;
-        if (lane == 0 && rank == 0) mbar_arrive_expect_tx(smem_u32(&ctl->full[s]), bytes);
-        if (kMode == kWgrad && t.slots - z < kTileZ) {
-          // the group's last slots: the rows past them (the next group's) read as zeros
-          const int r0 = (lane & 15) * 4;
-          int r[4];
+        const uint32_t dst = smem_u32((isA ? sA : sB) + s * (isA ? kABytes : kBBytes)) + (lane & 15) * 512u;
+        if (isA && rank == 0 && lane == 0) mbar_arrive_expect_tx(smem_u32(&ctl->full[s]), 2u * (kABytes + bbytes));
+        const int r0 = z + (lane & 15) * 4;
+        int r[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) r[i] = z + r0 + i < t.slots ? t.s0 + z + r0 + i : -1;
-          const uint32_t at = (lane & 15) * 512u;
-          if (lane < 16) {
-            pair::gather4(a + at, &tmAg, full, arow, r[0], r[1], r[2], r[3]);
-            pair::gather4(a + 8192u + at, &tmAg, full, arow + 64, r[0], r[1], r[2], r[3]);
-          } else {
-            for (int j = 0; j < bbox; ++j)
-              pair::gather4(b + 8192u * j + at, &tmBg, full, bcol + 64 * j, r[0], r[1], r[2], r[3]);
-          }
-          __syncwarp();
-        } else if (lane == 0) {
-          if (kMode == kForward) {
-            pair::load_3d(a, &tmA, full, z, arow, t.e);
-          } else if (kMode == kSwiglu) {
-            // 64 gates and their ups: 16 and 16 in turn
-            const int i0 = t.m0 / 2 + 64 * static_cast<int>(rank);
-            for (int j = 0; j < 4; ++j) pair::load_4d(a + 4096u * j, &tmA, full, z, i0 + 16 * j, 0, t.e);
-          } else if (kMode == kDgrad) {
-            pair::load_3d(a, &tmA, full, arow, z, t.e);
-            pair::load_3d(a + 8192u, &tmA, full, arow + 64, z, t.e);
-          } else {
-            pair::load_2d(a, &tmA, full, arow, t.s0 + z);
-            pair::load_2d(a + 8192u, &tmA, full, arow + 64, t.s0 + z);
-          }
-          if (kBmn) {
-            for (int j = 0; j < bbox; ++j) pair::load_2d(b + 8192u * j, &tmB, full, bcol + 64 * j, t.s0 + z);
-          } else {
-            for (int j = 0; j < bbox; ++j) pair::load_2d(b + 4096u * j, &tmB, full, z, t.s0 + bcol + 32 * j);
-          }
-        }
+        for (int i = 0; i < 4; ++i) r[i] = r0 + i < t.slots ? t.s0 + r0 + i : -1;
+        const int j = lane / 16;   // 64-column box
+        if (isA)
+          pair::gather4(dst + 8192u * j, &maps.ag, full, arow + 64 * j, r[0], r[1], r[2], r[3]);
+        else if (8192u * j < bbytes)
+          pair::gather4(dst + 8192u * j, &maps.bg, full, bcol + 64 * j, r[0], r[1], r[2], r[3]);
+        __syncwarp();
+        ++it;
       }
     }
     // wind down: let the copies already issued land before the CTA exits
     if (!ok && lane == 0 && rank == 0)
       for (uint32_t j = (it > kStages ? it - kStages : 0); j < it; ++j)
         drain_wait(smem_u32(&ctl->full[j % kStages]), (j / kStages) & 1u);
+    __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader)
     if (lane == 0 && rank == 0) {
@@ -358,8 +390,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else if (kMode == kSwiglu) {
         const int I = p.m / 2;
-        const bool up = lane >= 16;
-        const int i = t.m0 / 2 + 64 * static_cast<int>(rank) + 16 * q + (lane & 14);   // even row of the lane's pair
+        const bool up = lane & 8;
+        // even row of the lane's pair
+        const int i = t.m0 / 2 + 64 * static_cast<int>(rank) + 16 * q + (lane & 16) / 2 + (lane & 6);
         const int64_t s0 = static_cast<int64_t>(t.s0) + t.n0;
         for (int c = 0; c < t.nt; c += 32) {
           float wt = 1.f;   // of this lane's slot
@@ -378,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 2; ++k) {
               // gate lanes finish the even slot, up lanes the odd one
               const float v0 = __uint_as_float(v[j + 2 * k]), v1 = __uint_as_float(v[j + 2 * k + 1]);
-              const float got = __shfl_xor_sync(0xffffffffu, up ? v0 : v1, 16);
+              const float got = __shfl_xor_sync(0xffffffffu, up ? v0 : v1, 8);
               const float g = up ? got : v0, u = up ? v1 : got;
               const float ws = __shfl_sync(0xffffffffu, wt, j + 2 * k + (up ? 1 : 0));
               h[k] = g * sigmoid_f32(g) * u * ws;
@@ -433,9 +466,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) {
             if (row0 < p.m) {
               if (p.accumulate)
-                pair::reduce_add_3d(&tmC, smem_u32(box), t.n0 + c, row0, t.e);
+                pair::reduce_add_3d(&maps.c, smem_u32(box), t.n0 + c, row0, t.e);
               else
-                pair::store_3d(&tmC, smem_u32(box), t.n0 + c, row0, t.e);
+                pair::store_3d(&maps.c, smem_u32(box), t.n0 + c, row0, t.e);
             }
             bulk_commit();
           }
@@ -468,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // as the GPU holds at once (a larger persistent grid would run a second wave).
 template <Mode kMode, typename T, typename Out>
 moe_status launch_grouped(int64_t most_tiles, const DeviceInfo& dev, cudaStream_t stream,
-                          const CUtensorMap (&maps)[5], const Params& p) {
+                          const Maps& maps, const Params& p) {
   constexpr auto kernel = grouped_kernel<kMode, T, Out>;
   constexpr size_t smem = smem_bytes<kMode>();
   static std::mutex mu;
@@ -501,8 +534,7 @@ moe_status launch_grouped(int64_t most_tiles, const DeviceInfo& dev, cudaStream_
     n = pairs[dev.device];
   }
   if (most_tiles < n) n = static_cast<int>(most_tiles);
-  MOE_CUDA_TRY(launch_pdl(kernel, dim3(2u * n), dim3(kThreads), smem, stream, 2, maps[0], maps[1], maps[2], maps[3],
-                          maps[4], p));
+  MOE_CUDA_TRY(launch_pdl(kernel, dim3(2u * n), dim3(kThreads), smem, stream, 2, maps, p));
   return MOE_OK;
 }
 
@@ -524,6 +556,27 @@ bool weight_map(CUtensorMap* m, int dtype, const void* base, int64_t e, int64_t 
   const uint64_t dims[3] = {static_cast<uint64_t>(k), static_cast<uint64_t>(n), static_cast<uint64_t>(e)};
   const uint64_t strides[2] = {dims[0] * eb, dims[0] * dims[1] * eb};
   const uint32_t box[3] = {box_k, box_n, 1};
+  return encode_tensor_map(m, map_type(dtype), 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ==
+         CUDA_SUCCESS;
+}
+
+// Windows of 64 rows: row i of the window that starts at row j is row i + j,
+// and rows past the window read as zeros.  A block of a group's last rows is
+// the end of the window that ends with the group.  Boxes of 64 columns, or of
+// two such boxes one after the other (`one`; the width is a multiple of 64).
+bool window_map(CUtensorMap* m, int dtype, const void* base, int64_t width, int64_t rows, int64_t ld, bool one) {
+  const uint64_t row = static_cast<uint64_t>(ld) * 2, starts = static_cast<uint64_t>(rows > 64 ? rows - 63 : 1);
+  const uint64_t high = static_cast<uint64_t>(rows < 64 ? rows : 64);
+  if (one) {
+    const uint64_t dims[4] = {64, high, static_cast<uint64_t>(width) / 64, starts};
+    const uint64_t strides[3] = {row, 128, row};
+    const uint32_t box[4] = {64, 64, 2, 1};
+    return encode_tensor_map(m, map_type(dtype), 4, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ==
+           CUDA_SUCCESS;
+  }
+  const uint64_t dims[3] = {static_cast<uint64_t>(width), high, starts};
+  const uint64_t strides[2] = {row, row};
+  const uint32_t box[3] = {64, 64, 1};
   return encode_tensor_map(m, map_type(dtype), 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ==
          CUDA_SUCCESS;
 }
@@ -580,20 +633,30 @@ moe_status moe_grouped_gemm(const moe_grouped_args* a, moe_stream_t stream) {
   p.m = fwd ? a->N : a->K;
   p.z = fwd ? a->K : a->N;
   p.format = a->dtype == MOE_TYPE_BF16 ? 1u : 0u;
-  CUtensorMap maps[5];
-  bool ok = rows_map(&maps[1], a->dtype, a->x, in, a->rows, a->ldx, 32);
+  Maps maps;
+  bool ok = true;
+  for (int i = 0; i < 3; ++i) ok = ok && rows_map(&maps.b[i], a->dtype, a->x, in, a->rows, a->ldx, 32u << i);
+  const uint64_t K = static_cast<uint64_t>(a->K), N = static_cast<uint64_t>(a->N), E = static_cast<uint64_t>(a->E);
   if (glu) {
-    const uint64_t K = static_cast<uint64_t>(a->K), I = static_cast<uint64_t>(a->N) / 2;
-    const uint64_t dims[4] = {K, I, 2, static_cast<uint64_t>(a->E)};
-    const uint64_t strides[3] = {2 * K, 2 * K * I, 4 * K * I};
-    const uint32_t box[4] = {64, 16, 2, 1};
-    ok = ok && encode_tensor_map(&maps[0], map_type(a->dtype), 4, a->w, dims, strides, box,
+    // rows 8 i + j of the gate, then of the up half, j < 8
+    const uint64_t dims[5] = {K, 8, 2, N / 16, E};
+    const uint64_t strides[4] = {2 * K, N * K, 16 * K, 2 * N * K};
+    const uint32_t box[5] = {64, 8, 2, 8, 1};
+    ok = ok && encode_tensor_map(&maps.a, map_type(a->dtype), 5, a->w, dims, strides, box,
+                                 CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
+  } else if (!fwd && a->K % 64 == 0) {
+    // two 64-column boxes as one copy
+    p.a_one = 1;
+    const uint64_t dims[4] = {64, N, K / 64, E};
+    const uint64_t strides[3] = {2 * K, 128, 2 * N * K};
+    const uint32_t box[4] = {64, 64, 2, 1};
+    ok = ok && encode_tensor_map(&maps.a, map_type(a->dtype), 4, a->w, dims, strides, box,
                                  CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
   } else {
-    ok = ok && weight_map(&maps[0], a->dtype, a->w, a->E, a->N, a->K, 64, fwd ? 128 : 64);
+    ok = ok && weight_map(&maps.a, a->dtype, a->w, a->E, a->N, a->K, 64, fwd ? 128 : 64);
   }
   if (!ok) return MOE_ERR_CUDA;
-  maps[2] = maps[3] = maps[4] = maps[1];  // not used
+  maps.ag = maps.bg = maps.c = maps.a;  // not used
   const int64_t mt = ceil_div(p.m, kTileM);
   const int64_t most = mt * (ceil_div(a->rows, kTileN) + (a->E < a->rows ? a->E : a->rows));
   const bool bf = a->dtype == MOE_TYPE_BF16;
@@ -640,13 +703,16 @@ moe_status moe_grouped_wgrad(const moe_grouped_wgrad_args* a, moe_stream_t strea
   const void* dy = a->rows > 0 ? a->dy : static_cast<const uint16_t*>(a->dw);
   const void* x = a->rows > 0 ? a->x : static_cast<const uint16_t*>(a->dw);
   const int64_t rows = a->rows > 0 ? a->rows : 1;
-  CUtensorMap maps[5];
-  if (!rows_map(&maps[0], a->dtype, dy, a->N, rows, a->lddy, 64) ||
-      !rows_map(&maps[1], a->dtype, x, a->K, rows, a->ldx, 64) ||
-      !rows_map(&maps[2], a->dtype, dy, a->N, rows, a->lddy, 1) ||
-      !rows_map(&maps[3], a->dtype, x, a->K, rows, a->ldx, 1) ||
-      !weight_map(&maps[4], a->dw_dtype, a->dw, a->E, a->N, a->K, a->dw_dtype == MOE_TYPE_FP32 ? 32 : 64, 32))
+  p.a_one = a->N % 64 == 0;
+  p.b_one = a->K % 128 == 0;   // (each CTA's half then starts and ends at a multiple of 64)
+  Maps maps;
+  if (!window_map(&maps.a, a->dtype, dy, a->N, rows, a->lddy, p.a_one) ||
+      !window_map(&maps.b[0], a->dtype, x, a->K, rows, a->ldx, p.b_one) ||
+      !rows_map(&maps.ag, a->dtype, dy, a->N, rows, a->lddy, 1) ||
+      !rows_map(&maps.bg, a->dtype, x, a->K, rows, a->ldx, 1) ||
+      !weight_map(&maps.c, a->dw_dtype, a->dw, a->E, a->N, a->K, a->dw_dtype == MOE_TYPE_FP32 ? 32 : 64, 32))
     return MOE_ERR_CUDA;
+  maps.b[1] = maps.b[2] = maps.b[0];  // not used
   const int64_t most = static_cast<int64_t>(a->E) * ceil_div(p.m, kTileM) * ceil_div(p.n, kTileN);
   const bool bf = a->dtype == MOE_TYPE_BF16;
   if (a->dw_dtype == MOE_TYPE_FP32)
