@@ -23,6 +23,7 @@
 // one tile overlap the products of the next.  The CTAs are persistent: the
 // tiles of all groups form one sequence, dealt round-robin to the pairs.
 #include <mutex>
+#include <type_traits>
 
 #include "tc_pair.cuh"
 #include "train.cuh"
@@ -32,7 +33,7 @@ namespace {
 
 enum Mode { kForward, kSwiglu, kDgrad, kWgrad };
 
-constexpr int kThreads = 224;
+constexpr int kThreads = 288;
 constexpr int kEpiWarps = 4;
 constexpr int kTileM = 256, kTileN = 256, kTileZ = 64;   // per pair; contraction elements per stage
 constexpr int kABytes = 128 * kTileZ * 2;                // per CTA and stage
@@ -41,18 +42,23 @@ constexpr int kMaxE = 2048;
 
 template <Mode kMode> struct Cfg {
   static constexpr int kStages = kMode == kWgrad ? 5 : 6;
-  static constexpr int kStoreBytes = kMode == kWgrad ? kEpiWarps * 2 * 4096 : 0;   // tensor-store staging
+  // tensor-store staging; the few-slots path's sums
+  static constexpr int kStoreBytes = kMode == kWgrad ? kEpiWarps * 2 * 4096 : kMode == kDgrad ? 0 : 16384;
 };
 constexpr int kMaxStages = 6;
+constexpr int kSumBuffers = 4;
 
 struct Ctl {
   uint64_t full[kMaxStages];    // operands landed (the leader's counts both CTAs)
   uint64_t empty[kMaxStages];   // the stage's MMAs are done
   uint64_t tfull[2];            // accumulator complete
+  uint64_t sfull[kSumBuffers], sempty[kSumBuffers];   // few slots: a unit's sums
   uint64_t tempty[2];           // (leader) accumulator drained by every epilogue warp of the pair
   uint32_t tmem_base;
   int abort_flag;
   uint32_t warp_sum[kThreads / 32];
+  int warp_most[kThreads / 32];
+  int most;                     // slots of the largest group
   uint32_t first[kMaxE + 1];    // tiles before each group
 };
 
@@ -68,9 +74,11 @@ struct Params {
   const int32_t* route_ids;
   const float* route_weights;
   int32_t* status;
+  const uint16_t* x;
+  const uint16_t* w;
   uint16_t* y;
   uint16_t* pre;
-  int64_t ldy, ldpre, R;
+  int64_t ldx, ldy, ldpre, R;
   int rows;        // slots of the row buffers
   int E;
   int m;           // M extent of the products (2I for SwiGLU)
@@ -121,6 +129,7 @@ __device__ __forceinline__ void count_tiles(const Params& p, Ctl* ctl) {
   const int e0 = min(static_cast<int>(threadIdx.x) * per, p.E), e1 = min(e0 + per, p.E);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   uint32_t sum = 0;
+  int most = 0;
   bool bad = false;
   for (int e = e0; e < e1; ++e) {
     int s0, n;
@@ -128,6 +137,7 @@ __device__ __forceinline__ void count_tiles(const Params& p, Ctl* ctl) {
     const uint32_t t = tiles_of<kMode>(p, n);
     ctl->first[e] = sum;
     sum += t;
+    most = max(most, n);
   }
   if (bad && blockIdx.x == 0 && p.status) atomicOr(p.status, MOE_DEV_BAD_GROUP);
   uint32_t inc = sum;
@@ -136,12 +146,20 @@ __device__ __forceinline__ void count_tiles(const Params& p, Ctl* ctl) {
     const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += v;
   }
-  if (lane == 31) ctl->warp_sum[warp] = inc;
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 31) {
+    ctl->warp_sum[warp] = inc;
+    ctl->warp_most[warp] = most;
+  }
   __syncthreads();
   uint32_t base = inc - sum;
   for (int w = 0; w < warp; ++w) base += ctl->warp_sum[w];
   for (int e = e0; e < e1; ++e) ctl->first[e] += base;
-  if (threadIdx.x == kThreads - 1) ctl->first[p.E] = base + sum;
+  if (threadIdx.x == kThreads - 1) {
+    ctl->first[p.E] = base + sum;
+    for (int w = 0; w < warp; ++w) most = max(most, ctl->warp_most[w]);
+    ctl->most = most;
+  }
 }
 
 template <Mode kMode>
@@ -172,6 +190,15 @@ __device__ __forceinline__ Tile tile_at(const Params& p, const Ctl* ctl, uint32_
   return t;
 }
 
+// Two values that this lane holds for columns c and c + 1 of its row, against
+// the neighbour's: the even lane returns rows (lane, lane + 1) of column c,
+// the odd lane rows (lane - 1, lane) of column c + 1.
+template <typename T>
+__device__ __forceinline__ uint32_t pair_rows(float v0, float v1, bool odd) {
+  const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+  return odd ? Pack2<T>::store(got, v1) : Pack2<T>::store(v0, got);
+}
+
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   int ok = 0;
   if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag) ? 1 : 0;
@@ -183,13 +210,221 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
   mbar_wait(bar, parity, &dummy);
 }
 
-// Two values that this lane holds for columns c and c + 1 of its row, against
-// the neighbour's: the even lane returns rows (lane, lane + 1) of column c,
-// the odd lane rows (lane - 1, lane) of column c + 1.
+// ---------------------------------------------------------------- few slots
+//
+// A decoding step's groups hold a slot or two, and its few tiles of 256 weight
+// rows would keep few pairs busy.  The weights' bytes bound it, so the
+// contraction is split over the eight warps of every CTA: a unit is 16 weight
+// rows, a warp takes every eighth of its blocks of 64 contraction elements
+// through a ring of its own in shared memory (asynchronous 16-byte copies, 112
+// KB of weights in flight per SM, prefetched across units).  A ninth warp adds
+// the warps' sums, handed over through shared memory, so that no warp waits
+// for another one's copies.  (Loads into registers instead stalled at 17
+// GB/s per SM: beside this kernel's shared memory the L1 has room for few
+// outstanding lines.)  The products are m16n8k16 MMAs with up to 8 slots as
+// columns; as the order of the contraction is free, a lane's 16 contiguous
+// bytes of a weight row serve as its A fragments of two MMAs, and the same 16
+// bytes of a slot's row as the B fragments.
+constexpr int kFewSlots = 8;
+constexpr uint32_t kFewTiles = 4;   // ... and fewer than this many tiles per pair
+
 template <typename T>
-__device__ __forceinline__ uint32_t pair_rows(float v0, float v1, bool odd) {
-  const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
-  return odd ? Pack2<T>::store(got, v1) : Pack2<T>::store(v0, got);
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  if (std::is_same<T, __half>::value)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 16 bytes from global to shared memory, zeros where `bytes` is 0.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ uint4 load_shared16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+
+constexpr int kFewWarps = 8;
+constexpr int kFewStages = 8;
+constexpr int kFewStageBytes = 24 * 128;   // 16 weight rows, up to 8 slots: 64 elements each
+static_assert(kFewWarps * kFewStages * kFewStageBytes <= 6 * (kABytes + kBBytes), "the rings fit the operand stages");
+constexpr int kFewSums = kFewWarps * kFewSlots * 16;   // the warps' sums of a unit
+static_assert(kSumBuffers * kFewSums * 4 <= 16384, "the warps' sums");
+
+// A unit of 16 weight rows: eight gates and their ups, or 16 rows in order.
+template <Mode kMode>
+struct FewUnits {
+  int mt, units;        // tiles and units per group
+  uint32_t total;
+  __device__ __forceinline__ FewUnits(const Params& p, const Ctl* ctl)
+      : mt((p.m + kTileM - 1) / kTileM), units((p.m + 15) / 16), total(ctl->first[p.E] / mt * units) {}
+  __device__ __forceinline__ Tile at(const Params& p, const Ctl* ctl, uint32_t u) const {
+    return u < total ? tile_at<kMode>(p, ctl, u / units * mt) : Tile{};
+  }
+};
+
+// One of the eight streaming warps.
+template <Mode kMode, typename T>
+__device__ __forceinline__ void few_slots_stream(const Params& p, Ctl* ctl, uint8_t* ring, float* sums) {
+  constexpr bool kGlu = kMode == kSwiglu;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  volatile int* abort_flag = &ctl->abort_flag;
+  const FewUnits<kMode> f(p, ctl);
+  const int nkb = (p.z + kTileZ - 1) / kTileZ;
+  const int nst = warp < nkb ? (nkb - warp + kFewWarps - 1) / kFewWarps : 0;   // this warp's blocks of a unit
+  const uint32_t base = smem_u32(ring) + warp * kFewStages * kFewStageBytes;
+
+  // The copies run ahead: unit cu, block cb of it, into stage cs.
+  uint32_t cu = blockIdx.x, cs = 0;
+  int cb = 0;
+  // this lane's 16-byte column of 4 rows, then of 2 slots, of each block
+  const int chunk = lane % 8, sub = lane / 8;
+  const uint16_t* cw[4];   // null: no such row
+  const uint16_t* cx = nullptr;
+  int cslots = 0;
+  // (a unit's group is looked up one unit ahead: the lookup's loads take as long as several blocks)
+  Tile ct = f.at(p, ctl, cu);
+  auto open = [&]() {
+    if (cu >= f.total || nst == 0) return;
+    const Tile t = ct;
+    ct = f.at(p, ctl, cu + gridDim.x);
+    const int unit = static_cast<int>(cu % f.units);
+    const uint16_t* we = p.w + static_cast<int64_t>(t.e) * p.m * p.z;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = 4 * i + sub;
+      const int r = kGlu ? 8 * unit + j % 8 + (j / 8) * (p.m / 2) : 16 * unit + j;
+      cw[i] = r < p.m ? we + static_cast<int64_t>(r) * p.z + 8 * chunk : nullptr;
+    }
+    cx = p.x + (static_cast<int64_t>(t.s0) + sub) * p.ldx + 8 * chunk;
+    cslots = t.slots;
+  };
+  auto copy = [&]() {
+    if (cu < f.total && nst > 0) {
+      const int z = (warp + cb * kFewWarps) * kTileZ;
+      const uint32_t st = base + cs * kFewStageBytes;
+      const bool in = z + 8 * chunk < p.z;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = 4 * i + sub;
+        const uint32_t dst = st + 128 * j + 16 * (chunk ^ (j & 7));
+        copy16_async(dst, in && cw[i] ? cw[i] + z : p.w, in && cw[i] ? 16u : 0u);
+      }
+#pragma unroll
+      for (int i = 0; i < kFewSlots / 4; ++i) {
+        const int j = 4 * i + sub;
+        if (j < cslots)
+          copy16_async(st + 2048 + 128 * j + 16 * (chunk ^ (j & 7)), in ? cx + 4 * i * p.ldx + z : p.x, in ? 16u : 0u);
+      }
+      if (++cb == nst) {
+        cb = 0;
+        cu += gridDim.x;
+        open();
+      }
+    }
+    cs = cs + 1 == kFewStages ? 0 : cs + 1;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  open();
+  for (int i = 0; i < kFewStages - 1; ++i) copy();
+
+  uint32_t s = 0, n = 0;
+  for (uint32_t u = blockIdx.x; u < f.total; u += gridDim.x, ++n) {
+    float d[4] = {};
+    for (int b = 0; b < nst; ++b) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kFewStages - 2) : "memory");
+      __syncwarp();
+      copy();   // into the stage read in the step before
+      const uint32_t st = base + s * kFewStageBytes;
+      const int g = lane / 4;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        // (columns 2 (lane % 4) + h: no two lanes of a quarter-warp share a bank)
+        const uint32_t at = 128 * g + 16 * ((2 * (lane % 4) + h) ^ g);
+        const uint4 a0 = load_shared16(st + at), a1 = load_shared16(st + 1024 + at);
+        const uint4 x0 = load_shared16(st + 2048 + at);
+        mma_16816<T>(d, a0.x, a1.x, a0.y, a1.y, x0.x, x0.y);
+        mma_16816<T>(d, a0.z, a1.z, a0.w, a1.w, x0.z, x0.w);
+      }
+      s = s + 1 == kFewStages ? 0 : s + 1;
+      __syncwarp();
+    }
+    // sums[warp][slot][row]: weight rows lane / 4 and 8 on, slots 2 (lane % 4) and the next
+    const uint32_t buf = n % kSumBuffers;
+    if (!warp_wait(smem_u32(&ctl->sempty[buf]), ((n / kSumBuffers) & 1u) ^ 1u, abort_flag)) break;
+    float* out = sums + buf * kFewSums + warp * kFewSlots * 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[(2 * (lane % 4) + (i & 1)) * 16 + lane / 4 + 8 * (i / 2)] = d[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&ctl->sfull[buf]));
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// The ninth warp: adds the warps' sums in order and writes the results.
+template <Mode kMode, typename T>
+__device__ __forceinline__ void few_slots_finish(const Params& p, Ctl* ctl, const float* sums) {
+  constexpr bool kGlu = kMode == kSwiglu;
+  const int lane = threadIdx.x % 32;
+  volatile int* abort_flag = &ctl->abort_flag;
+  const FewUnits<kMode> f(p, ctl);
+  Tile next = f.at(p, ctl, blockIdx.x);
+  uint32_t n = 0;
+  for (uint32_t u = blockIdx.x; u < f.total; u += gridDim.x, ++n) {
+    const Tile t = next;
+    next = f.at(p, ctl, u + gridDim.x);
+    const int unit = static_cast<int>(u % f.units);
+    const int row = lane % 16;
+    // this lane's slots: lane / 16 + 0, 2, 4, 6
+    float wt[kFewSlots / 2];
+#pragma unroll
+    for (int c = 0; c < kFewSlots / 2; ++c) {
+      const int slot = 2 * c + lane / 16;
+      wt[c] = 1.f;
+      if (kGlu && p.route_weights && slot < t.slots) {
+        int64_t r = static_cast<int64_t>(t.s0) + slot;
+        if (p.route_ids) r = p.route_ids[r];
+        wt[c] = p.route_ids && (r < 0 || r >= p.R) ? 0.f : p.route_weights[r];
+      }
+    }
+    const uint32_t buf = n % kSumBuffers;
+    if (!warp_wait(smem_u32(&ctl->sfull[buf]), (n / kSumBuffers) & 1u, abort_flag)) break;
+    const float* in = sums + buf * kFewSums;
+    float sum[kFewSlots / 2] = {};
+#pragma unroll
+    for (int w = 0; w < kFewWarps; ++w)
+#pragma unroll
+      for (int c = 0; c < kFewSlots / 2; ++c) sum[c] += in[(w * kFewSlots + 2 * c + lane / 16) * 16 + row];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&ctl->sempty[buf]));
+#pragma unroll
+    for (int c = 0; c < kFewSlots / 2; ++c) {
+      const int slot = 2 * c + lane / 16;
+      const int64_t sl = static_cast<int64_t>(t.s0) + slot;
+      const bool live = slot < t.slots;
+      if (kGlu) {
+        const float up = __shfl_down_sync(0xffffffffu, sum[c], 8);   // row + 8 of the same slot
+        const int I = p.m / 2, i = 8 * unit + row % 8;
+        if (live && p.pre)
+          p.pre[sl * p.ldpre + (row < 8 ? i : I + i)] = static_cast<uint16_t>(Pack2<T>::store(sum[c], 0.f));
+        if (live && row < 8)
+          p.y[sl * p.ldy + i] =
+              static_cast<uint16_t>(Pack2<T>::store(sum[c] * sigmoid_f32(sum[c]) * up * wt[c], 0.f));
+      } else if (live && 16 * unit + row < p.m) {
+        p.y[sl * p.ldy + 16 * unit + row] = static_cast<uint16_t>(Pack2<T>::store(sum[c], 0.f));
+      }
+    }
+  }
 }
 
 template <Mode kMode, typename T, typename Out>
@@ -216,6 +451,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctl->tfull[b]), 1);
       mbar_init(smem_u32(&ctl->tempty[b]), 2 * kEpiWarps);
     }
+    for (int b = 0; b < kSumBuffers; ++b) {
+      mbar_init(smem_u32(&ctl->sfull[b]), 8);
+      mbar_init(smem_u32(&ctl->sempty[b]), 1);
+    }
     ctl->abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&maps.a);
@@ -236,7 +475,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t total = ctl->first[p.E];
   const uint32_t tile0 = blockIdx.x / 2, step = gridDim.x / 2;
 
-  if (warp == 0 || warp == 6) {
+  constexpr bool kFew = kMode == kForward || kMode == kSwiglu;
+  if (kFew && ctl->most <= kFewSlots && total < kFewTiles * step) {
+    if (warp < kFewWarps)
+      few_slots_stream<kMode, T>(p, ctl, sA, reinterpret_cast<float*>(sC));
+    else
+      few_slots_finish<kMode, T>(p, ctl, reinterpret_cast<const float*>(sC));
+  } else if (warp == 0 || warp == 6) {
     // ------------------------------------------------------------ producers (A: warp 0, B: warp 6)
     const bool isA = warp == 0;
     const uint32_t lead_full0 = pair::mapa_shared(smem_u32(&ctl->full[0]), 0);
@@ -358,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (it > 0) drain_wait(smem_u32(&ctl->empty[(it - 1) % kStages]), ((it - 1) / kStages) & 1u);
     }
     __syncwarp();
-  } else {
+  } else if (warp < 6) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;   // the lanes of tensor memory that this warp may read
     const uint32_t lanes = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
@@ -623,6 +868,9 @@ moe_status moe_grouped_gemm(const moe_grouped_args* a, moe_stream_t stream) {
   p.route_ids = glu && a->route_weights ? a->route_ids : nullptr;
   p.route_weights = glu ? a->route_weights : nullptr;
   p.status = a->device_status;
+  p.x = a->x;
+  p.w = a->w;
+  p.ldx = a->ldx;
   p.y = a->y;
   p.pre = pre ? a->pre : nullptr;
   p.ldy = a->ldy;
@@ -658,7 +906,10 @@ moe_status moe_grouped_gemm(const moe_grouped_args* a, moe_stream_t stream) {
   if (!ok) return MOE_ERR_CUDA;
   maps.ag = maps.bg = maps.c = maps.a;  // not used
   const int64_t mt = ceil_div(p.m, kTileM);
-  const int64_t most = mt * (ceil_div(a->rows, kTileN) + (a->E < a->rows ? a->E : a->rows));
+  const int64_t groups = a->E < a->rows ? a->E : a->rows;
+  int64_t most = mt * (ceil_div(a->rows, kTileN) + groups);
+  // (the few-slots path has a unit of 16 rows for each CTA)
+  if (fwd && most < ceil_div(p.m, 32) * groups) most = ceil_div(p.m, 32) * groups;
   const bool bf = a->dtype == MOE_TYPE_BF16;
   if (glu)
     return bf ? launch_grouped<kSwiglu, __nv_bfloat16, __nv_bfloat16>(most, dev, stream, maps, p)
