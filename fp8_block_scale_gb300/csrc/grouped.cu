@@ -47,6 +47,8 @@ template <Mode kMode> struct Cfg {
 };
 constexpr int kMaxStages = 6;
 constexpr int kSumBuffers = 4;
+constexpr int kFewGroups = 640;
+
 
 struct Ctl {
   uint64_t full[kMaxStages];    // operands landed (the leader's counts both CTAs)
@@ -60,6 +62,7 @@ struct Ctl {
   int warp_most[kThreads / 32];
   int most;                     // slots of the largest group
   uint32_t first[kMaxE + 1];    // tiles before each group
+  int2 group[kFewGroups];       // few slots: (8 expert + slots - 1, first slot) of the groups that have any
 };
 
 template <Mode kMode>
@@ -154,7 +157,17 @@ __device__ __forceinline__ void count_tiles(const Params& p, Ctl* ctl) {
   __syncthreads();
   uint32_t base = inc - sum;
   for (int w = 0; w < warp; ++w) base += ctl->warp_sum[w];
-  for (int e = e0; e < e1; ++e) ctl->first[e] += base;
+  const uint32_t mt = (p.m + kTileM - 1) / kTileM;
+  for (int e = e0; e < e1; ++e) {
+    const uint32_t at = ctl->first[e] + base;
+    ctl->first[e] = at;
+    if (kMode == kForward || kMode == kSwiglu) {
+      // (each group has mt tiles where this table is used)
+      int s0, n;
+      group_at(p, e, s0, n);
+      if (n > 0 && at / mt < kFewGroups) ctl->group[at / mt] = make_int2(8 * e + min(n, 8) - 1, s0);
+    }
+  }
   if (threadIdx.x == kThreads - 1) {
     ctl->first[p.E] = base + sum;
     for (int w = 0; w < warp; ++w) most = max(most, ctl->warp_most[w]);
@@ -213,7 +226,8 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
 // ---------------------------------------------------------------- few slots
 //
 // A decoding step's groups hold a slot or two, and its few tiles of 256 weight
-// rows would keep few pairs busy.  The weights' bytes bound it, so the
+// rows would keep few pairs busy.  The weights' bytes bound it: where no group
+// has more than 8 slots (and no more than 640 groups have any) the
 // contraction is split over the eight warps of every CTA: a unit is 16 weight
 // rows, a warp takes every eighth of its blocks of 64 contraction elements
 // through a ring of its own in shared memory (asynchronous 16-byte copies, 112
@@ -226,7 +240,6 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
 // bytes of a weight row serve as its A fragments of two MMAs, and the same 16
 // bytes of a slot's row as the B fragments.
 constexpr int kFewSlots = 8;
-constexpr uint32_t kFewTiles = 4;   // ... and fewer than this many tiles per pair
 
 template <typename T>
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -264,13 +277,10 @@ static_assert(kSumBuffers * kFewSums * 4 <= 16384, "the warps' sums");
 // A unit of 16 weight rows: eight gates and their ups, or 16 rows in order.
 template <Mode kMode>
 struct FewUnits {
-  int mt, units;        // tiles and units per group
+  int units;            // per group
   uint32_t total;
   __device__ __forceinline__ FewUnits(const Params& p, const Ctl* ctl)
-      : mt((p.m + kTileM - 1) / kTileM), units((p.m + 15) / 16), total(ctl->first[p.E] / mt * units) {}
-  __device__ __forceinline__ Tile at(const Params& p, const Ctl* ctl, uint32_t u) const {
-    return u < total ? tile_at<kMode>(p, ctl, u / units * mt) : Tile{};
-  }
+      : units((p.m + 15) / 16), total(ctl->first[p.E] / ((p.m + kTileM - 1) / kTileM) * units) {}
 };
 
 // One of the eight streaming warps.
@@ -292,22 +302,19 @@ __device__ __forceinline__ void few_slots_stream(const Params& p, Ctl* ctl, uint
   const uint16_t* cw[4];   // null: no such row
   const uint16_t* cx = nullptr;
   int cslots = 0;
-  // (a unit's group is looked up one unit ahead: the lookup's loads take as long as several blocks)
-  Tile ct = f.at(p, ctl, cu);
   auto open = [&]() {
     if (cu >= f.total || nst == 0) return;
-    const Tile t = ct;
-    ct = f.at(p, ctl, cu + gridDim.x);
+    const int2 t = ctl->group[cu / f.units];
     const int unit = static_cast<int>(cu % f.units);
-    const uint16_t* we = p.w + static_cast<int64_t>(t.e) * p.m * p.z;
+    const uint16_t* we = p.w + static_cast<int64_t>(t.x / 8) * p.m * p.z;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int j = 4 * i + sub;
       const int r = kGlu ? 8 * unit + j % 8 + (j / 8) * (p.m / 2) : 16 * unit + j;
       cw[i] = r < p.m ? we + static_cast<int64_t>(r) * p.z + 8 * chunk : nullptr;
     }
-    cx = p.x + (static_cast<int64_t>(t.s0) + sub) * p.ldx + 8 * chunk;
-    cslots = t.slots;
+    cx = p.x + (static_cast<int64_t>(t.y) + sub) * p.ldx + 8 * chunk;
+    cslots = t.x % 8 + 1;
   };
   auto copy = [&]() {
     if (cu < f.total && nst > 0) {
@@ -378,11 +385,10 @@ __device__ __forceinline__ void few_slots_finish(const Params& p, Ctl* ctl, cons
   const int lane = threadIdx.x % 32;
   volatile int* abort_flag = &ctl->abort_flag;
   const FewUnits<kMode> f(p, ctl);
-  Tile next = f.at(p, ctl, blockIdx.x);
   uint32_t n = 0;
   for (uint32_t u = blockIdx.x; u < f.total; u += gridDim.x, ++n) {
-    const Tile t = next;
-    next = f.at(p, ctl, u + gridDim.x);
+    const int2 group = ctl->group[u / f.units];
+    const int s0 = group.y, slots = group.x % 8 + 1;
     const int unit = static_cast<int>(u % f.units);
     const int row = lane % 16;
     // this lane's slots: lane / 16 + 0, 2, 4, 6
@@ -391,8 +397,8 @@ __device__ __forceinline__ void few_slots_finish(const Params& p, Ctl* ctl, cons
     for (int c = 0; c < kFewSlots / 2; ++c) {
       const int slot = 2 * c + lane / 16;
       wt[c] = 1.f;
-      if (kGlu && p.route_weights && slot < t.slots) {
-        int64_t r = static_cast<int64_t>(t.s0) + slot;
+      if (kGlu && p.route_weights && slot < slots) {
+        int64_t r = static_cast<int64_t>(s0) + slot;
         if (p.route_ids) r = p.route_ids[r];
         wt[c] = p.route_ids && (r < 0 || r >= p.R) ? 0.f : p.route_weights[r];
       }
@@ -410,8 +416,8 @@ __device__ __forceinline__ void few_slots_finish(const Params& p, Ctl* ctl, cons
 #pragma unroll
     for (int c = 0; c < kFewSlots / 2; ++c) {
       const int slot = 2 * c + lane / 16;
-      const int64_t sl = static_cast<int64_t>(t.s0) + slot;
-      const bool live = slot < t.slots;
+      const int64_t sl = static_cast<int64_t>(s0) + slot;
+      const bool live = slot < slots;
       if (kGlu) {
         const float up = __shfl_down_sync(0xffffffffu, sum[c], 8);   // row + 8 of the same slot
         const int I = p.m / 2, i = 8 * unit + row % 8;
@@ -460,28 +466,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&maps.a);
     tma_prefetch_desc(&maps.b[0]);
   }
+  pdl_launch_dependents();
+  pdl_wait();
+  count_tiles<kMode>(p, ctl);
+  __syncthreads();
+  const uint32_t total = ctl->first[p.E];
+  const uint32_t tile0 = blockIdx.x / 2, step = gridDim.x / 2;
+  constexpr bool kFew = kMode == kForward || kMode == kSwiglu;
+  if (kFew && ctl->most <= kFewSlots && total <= kFewGroups * static_cast<uint32_t>((p.m + kTileM - 1) / kTileM)) {
+    if (warp < kFewWarps)
+      few_slots_stream<kMode, T>(p, ctl, sA, reinterpret_cast<float*>(sC));
+    else
+      few_slots_finish<kMode, T>(p, ctl, reinterpret_cast<const float*>(sC));
+    __syncthreads();
+    if (threadIdx.x == 0 && ctl->abort_flag && p.status) atomicOr(p.status, MOE_DEV_TIMEOUT);
+    return;
+  }
   if (warp == 1) {
     pair::tmem_alloc(smem_u32(&ctl->tmem_base), 512);
     pair::tmem_relinquish();
   }
-  pdl_launch_dependents();
-  pdl_wait();
-  count_tiles<kMode>(p, ctl);
   tc_fence_before();
   __syncthreads();
   pair::cluster_sync();  // the peer's copies and arrivals target initialised barriers
   tc_fence_after();
   const uint32_t tmem_base = ctl->tmem_base;
-  const uint32_t total = ctl->first[p.E];
-  const uint32_t tile0 = blockIdx.x / 2, step = gridDim.x / 2;
 
-  constexpr bool kFew = kMode == kForward || kMode == kSwiglu;
-  if (kFew && ctl->most <= kFewSlots && total < kFewTiles * step) {
-    if (warp < kFewWarps)
-      few_slots_stream<kMode, T>(p, ctl, sA, reinterpret_cast<float*>(sC));
-    else
-      few_slots_finish<kMode, T>(p, ctl, reinterpret_cast<const float*>(sC));
-  } else if (warp == 0 || warp == 6) {
+  if (warp == 0 || warp == 6) {
     // ------------------------------------------------------------ producers (A: warp 0, B: warp 6)
     const bool isA = warp == 0;
     const uint32_t lead_full0 = pair::mapa_shared(smem_u32(&ctl->full[0]), 0);
