@@ -209,6 +209,7 @@ class MoeAdamWArgs(ctypes.Structure):
         ("seed", ctypes.c_uint32),
         ("count", ctypes.c_int32),
         ("state_bits", ctypes.c_int32),
+        ("grad_types", ctypes.c_int32),
     ]
 
 
@@ -269,7 +270,7 @@ _SIGS = {
     "moe_adamw_table_bytes": (ctypes.c_size_t, [ctypes.c_int]),
     "moe_adamw_table_init": (ctypes.c_int, [ctypes.POINTER(MoeAdamWTensor), ctypes.c_int, ctypes.c_int,
                                             ctypes.c_void_p, ctypes.c_size_t, ctypes.POINTER(ctypes.c_int64),
-                                            ctypes.c_void_p]),
+                                            ctypes.POINTER(ctypes.c_int32), ctypes.c_void_p]),
     "moe_adamw_step": (ctypes.c_int, [ctypes.POINTER(MoeAdamWArgs), ctypes.c_void_p]),
     "moe_debug_bounds_enabled": (ctypes.c_int, []),
     "moe_debug_bounds_selftest": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_void_p,
@@ -757,11 +758,11 @@ class AdamWTable:
         lib = load()
         self.table = torch.empty(lib.moe_adamw_table_bytes(self.count), dtype=torch.uint8,
                                  device=tensors[0]["param"].device)
-        chunks = ctypes.c_int64()
+        chunks, types = ctypes.c_int64(), ctypes.c_int32()
         _check("moe_adamw_table_init", lib.moe_adamw_table_init(
             host, self.count, self.state_bits, _ptr(self.table), self.table.numel(), ctypes.byref(chunks),
-            _stream(stream)))
-        self.chunks = chunks.value
+            ctypes.byref(types), _stream(stream)))
+        self.chunks, self.grad_types = chunks.value, types.value
 
 
 def make_adamw_args(table, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, seed=0, grad_scale=None, skip=None):
@@ -769,8 +770,8 @@ def make_adamw_args(table, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, seed=0, g
     fields a loop rewrites between steps."""
     args = MoeAdamWArgs()
     args._table_keepalive = (table, grad_scale, skip)
-    args.table, args.chunks, args.count, args.state_bits = (table.table.data_ptr(), table.chunks, table.count,
-                                                            table.state_bits)
+    args.table, args.chunks, args.count = table.table.data_ptr(), table.chunks, table.count
+    args.state_bits, args.grad_types = table.state_bits, table.grad_types
     args.grad_scale = _opt("grad_scale", grad_scale, torch.float32, 1)
     args.skip = _opt("skip", skip, torch.int32, 1)
     args.lr, args.step, args.beta1, args.beta2, args.eps, args.seed = lr, step, beta1, beta2, eps, seed & 0xFFFFFFFF

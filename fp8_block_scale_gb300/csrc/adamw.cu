@@ -1,6 +1,6 @@
 // One AdamW step over many tensors in one launch (moe_adamw_step).
 //
-// A device table lists the tensors; each is cut into chunks of 4096 elements
+// A device table lists the tensors; each is cut into chunks of 2048 elements
 // and the CTAs walk the chunks of all tensors, so that a list of small
 // tensors costs one launch.  Per element the step reads the gradient, the
 // parameter and both states once and writes the parameter, its 16-bit copy
@@ -17,8 +17,8 @@
 namespace moe {
 namespace {
 
-constexpr int kChunk = 4096;   // elements per chunk
-constexpr int kThreads = 256;
+constexpr int kChunk = 2048;   // elements per chunk
+constexpr int kThreads = 128;
 constexpr int kSteps = kChunk / (4 * kThreads);  // four elements per thread and step
 
 struct AdamEntry {
@@ -31,7 +31,7 @@ struct AdamEntry {
   float* v_scale;
   int64_t n;
   int64_t first_chunk;
-  double weight_decay;
+  float weight_decay;
   int32_t grad_dtype;
   int32_t model_dtype;
 };
@@ -41,7 +41,7 @@ struct AdamParams {
   const float* grad_scale;
   const int32_t* skip;
   int64_t chunks;
-  double lr;
+  float lr;
   float beta1, one_minus_beta1, beta2, one_minus_beta2;
   float step_size;   // lr / (1 - beta1^step)
   float root_scale;  // 1 / sqrt(1 - beta2^step)
@@ -51,50 +51,81 @@ struct AdamParams {
 };
 
 // The new m, v, root of v and parameter of one element.  m and v are rounded
-// once per written operation; the root and the quotient of the update come
-// from the hardware's approximations (within 2 units of the last place of the
-// update, which is far below the parameter's own rounding).
-struct Elem {
-  float m, v, r, p;
+// once per written operation; the quotient of the update comes from the
+// hardware's reciprocal (within 2 units of the last place of the update, far
+// below the parameter's own rounding).  A v below 1e-37 loses precision.
+// Two elements at a time: the packed FP32 instructions round each half as the
+// scalar ones do.
+struct Elem2 {
+  float2 m, v, r, p;
 };
-__device__ __forceinline__ float sqrt_fast(float v) {
+__device__ __forceinline__ float rsqrt_fast(float v) {
   float r;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
 __device__ __forceinline__ float rcp_fast(float v) {
   float r;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
-__device__ __forceinline__ Elem adam_elem(const AdamParams& a, float decay, float g, float p, float m, float v) {
-  Elem e;
-  e.m = __fadd_rn(__fmul_rn(m, a.beta1), __fmul_rn(g, a.one_minus_beta1));
-  e.v = __fadd_rn(__fmul_rn(v, a.beta2), __fmul_rn(__fmul_rn(g, g), a.one_minus_beta2));
-  e.r = sqrt_fast(e.v);
-  const float den = fmaf(e.r, a.root_scale, a.eps);
-  e.p = __fsub_rn(__fmul_rn(p, decay), __fmul_rn(__fmul_rn(e.m, a.step_size), rcp_fast(den)));
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+// The sum of two packed products, each rounded on its own: a packed addition
+// would be contracted with them (and a state's last bit decides, now and then,
+// about an 8-bit code).
+__device__ __forceinline__ float2 add_unfused(float2 a, float2 b) {
+  return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
+}
+__device__ __forceinline__ float2 neg(float2 v) { return make_float2(-v.x, -v.y); }
+
+// The states' codes are to be those of the formula, so roots and quotients are
+// rounded correctly: an approximation and its exact residual, corrected once
+// (Markstein's method).
+__device__ __forceinline__ float2 root2(float2 v) {
+  const float2 y = make_float2(rsqrt_fast(fmaxf(v.x, 1e-37f)), rsqrt_fast(fmaxf(v.y, 1e-37f)));
+  const float2 s = __fmul2_rn(v, y);
+  return __ffma2_rn(__ffma2_rn(neg(s), s, v), __fmul2_rn(y, both(0.5f)), s);
+}
+// a / b, `inv` the correctly rounded reciprocal of b.
+__device__ __forceinline__ float2 quotient2(float2 a, float b, float inv) {
+  const float2 q = __fmul2_rn(a, both(inv));
+  return __ffma2_rn(__ffma2_rn(neg(q), both(b), a), both(inv), q);
+}
+__device__ __forceinline__ Elem2 adam_elem2(const AdamParams& a, float decay, float2 g, float2 p, float2 m, float2 v) {
+  Elem2 e;
+  e.m = add_unfused(__fmul2_rn(m, both(a.beta1)), __fmul2_rn(g, both(a.one_minus_beta1)));
+  e.v = add_unfused(__fmul2_rn(v, both(a.beta2)), __fmul2_rn(__fmul2_rn(g, g), both(a.one_minus_beta2)));
+  e.r = root2(e.v);
+  const float2 den = __ffma2_rn(e.r, both(a.root_scale), both(a.eps));
+  const float2 upd = __fmul2_rn(__fmul2_rn(e.m, both(-a.step_size)), make_float2(rcp_fast(den.x), rcp_fast(den.y)));
+  e.p = __fadd2_rn(__fmul2_rn(p, both(decay)), upd);
   return e;
 }
 
-// Four gradients; kGrad = -1: of a type known at run time.
+// Four gradients: their bits first (nothing waits for them yet), then the
+// values.
+// kGrad: the gradients' type, known when a chunk's loop is chosen.
 template <int kGrad>
-__device__ __forceinline__ void load_grad4(const AdamEntry& t, int64_t i, float (&g)[4]) {
-  const int type = kGrad >= 0 ? kGrad : t.grad_dtype;
-  if (type == MOE_TYPE_FP32) {
-    const float4 v = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(t.grad) + i));
-    g[0] = v.x; g[1] = v.y; g[2] = v.z; g[3] = v.w;
+__device__ __forceinline__ uint4 load_grad4(const AdamEntry& t, int64_t i, bool ok) {
+  uint4 raw = make_uint4(0, 0, 0, 0);
+  if (ok && kGrad == MOE_TYPE_FP32)
+    raw = __ldcs(reinterpret_cast<const uint4*>(static_cast<const float*>(t.grad) + i));
+  if (ok && kGrad != MOE_TYPE_FP32) {
+    const uint2 v = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(t.grad) + i));
+    raw.x = v.x;
+    raw.y = v.y;
+  }
+  return raw;
+}
+template <int kGrad>
+__device__ __forceinline__ void grad4(const uint4& raw, float (&g)[4]) {
+  if (kGrad == MOE_TYPE_FP32) {
+    g[0] = __uint_as_float(raw.x); g[1] = __uint_as_float(raw.y);
+    g[2] = __uint_as_float(raw.z); g[3] = __uint_as_float(raw.w);
     return;
   }
-  const uint2 v = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(t.grad) + i));
-  float2 a, b;
-  if (type == MOE_TYPE_BF16) {
-    a = Pack2<__nv_bfloat16>::load(v.x);
-    b = Pack2<__nv_bfloat16>::load(v.y);
-  } else {
-    a = Pack2<__half>::load(v.x);
-    b = Pack2<__half>::load(v.y);
-  }
+  const float2 a = kGrad == MOE_TYPE_BF16 ? Pack2<__nv_bfloat16>::load(raw.x) : Pack2<__half>::load(raw.x);
+  const float2 b = kGrad == MOE_TYPE_BF16 ? Pack2<__nv_bfloat16>::load(raw.y) : Pack2<__half>::load(raw.y);
   g[0] = a.x; g[1] = a.y; g[2] = b.x; g[3] = b.y;
 }
 __device__ __forceinline__ float load_grad1(const AdamEntry& t, int64_t i) {
@@ -125,36 +156,38 @@ __device__ __forceinline__ int find_entry(const AdamParams& a, int64_t c) {
 
 // ---------------------------------------------------------------- 32-bit states
 
+// A chunk, four elements a thread and step; steps that pass the tensor's end
+// are left out.
 template <int kGrad>
 __device__ __forceinline__ void adamw32_chunk(const AdamParams& a, const AdamEntry& t, float decay, float gs,
                                               int64_t i0) {
   // every load of the chunk goes out before the first result is needed
-  float g[kSteps][4];
+  uint4 raw[kSteps];
   float4 p4[kSteps], m4[kSteps], v4[kSteps];
   float* m = static_cast<float*>(t.m);
   float* v = static_cast<float*>(t.v);
 #pragma unroll
   for (int u = 0; u < kSteps; ++u) {
     const int64_t i = i0 + 4 * (threadIdx.x + u * kThreads);
-    load_grad4<kGrad>(t, i, g[u]);
-    p4[u] = __ldcs(reinterpret_cast<const float4*>(t.param + i));
-    m4[u] = __ldcs(reinterpret_cast<const float4*>(m + i));
-    v4[u] = __ldcs(reinterpret_cast<const float4*>(v + i));
+    const bool ok = i + 4 <= t.n;
+    raw[u] = load_grad4<kGrad>(t, i, ok);
+    if (ok) p4[u] = __ldcs(reinterpret_cast<const float4*>(t.param + i));
+    if (ok) m4[u] = __ldcs(reinterpret_cast<const float4*>(m + i));
+    if (ok) v4[u] = __ldcs(reinterpret_cast<const float4*>(v + i));
   }
 #pragma unroll
   for (int u = 0; u < kSteps; ++u) {
     const int64_t i = i0 + 4 * (threadIdx.x + u * kThreads);
-    float p[4];
-    const float po[4] = {p4[u].x, p4[u].y, p4[u].z, p4[u].w};
-    float* mp = &m4[u].x;
-    float* vp = &v4[u].x;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const Elem e = adam_elem(a, decay, __fmul_rn(g[u][j], gs), po[j], mp[j], vp[j]);
-      p[j] = e.p;
-      mp[j] = e.m;
-      vp[j] = e.v;
-    }
+    if (i + 4 > t.n) continue;
+    float g[4], p[4];
+    grad4<kGrad>(raw[u], g);
+    const Elem2 lo = adam_elem2(a, decay, __fmul2_rn(make_float2(g[0], g[1]), both(gs)), make_float2(p4[u].x, p4[u].y),
+                                make_float2(m4[u].x, m4[u].y), make_float2(v4[u].x, v4[u].y));
+    const Elem2 hi = adam_elem2(a, decay, __fmul2_rn(make_float2(g[2], g[3]), both(gs)), make_float2(p4[u].z, p4[u].w),
+                                make_float2(m4[u].z, m4[u].w), make_float2(v4[u].z, v4[u].w));
+    p[0] = lo.p.x; p[1] = lo.p.y; p[2] = hi.p.x; p[3] = hi.p.y;
+    m4[u] = make_float4(lo.m.x, lo.m.y, hi.m.x, hi.m.y);
+    v4[u] = make_float4(lo.v.x, lo.v.y, hi.v.x, hi.v.y);
     __stcs(reinterpret_cast<float4*>(t.param + i), make_float4(p[0], p[1], p[2], p[3]));
     __stcs(reinterpret_cast<float4*>(m + i), m4[u]);
     __stcs(reinterpret_cast<float4*>(v + i), v4[u]);
@@ -162,29 +195,27 @@ __device__ __forceinline__ void adamw32_chunk(const AdamParams& a, const AdamEnt
   }
 }
 
-__global__ void __launch_bounds__(kThreads) adamw32_kernel(const AdamParams a) {
+template <int kGrad>
+__global__ void __launch_bounds__(kThreads) adamw32_kernel(const __grid_constant__ AdamParams a) {
   pdl_wait();
   if (a.skip && *a.skip) return;
   const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
   for (int64_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
     const AdamEntry t = a.table[find_entry(a, c)];
-    const float decay = static_cast<float>(1.0 - a.lr * t.weight_decay);
+    if (t.grad_dtype != kGrad) continue;
+    const float decay = fmaf(-a.lr, t.weight_decay, 1.0f);
     const int64_t i0 = (c - t.first_chunk) * kChunk;
-    if (i0 + kChunk <= t.n) {
-      if (t.grad_dtype == MOE_TYPE_FP32) adamw32_chunk<MOE_TYPE_FP32>(a, t, decay, gs, i0);
-      else if (t.grad_dtype == MOE_TYPE_BF16) adamw32_chunk<MOE_TYPE_BF16>(a, t, decay, gs, i0);
-      else adamw32_chunk<MOE_TYPE_FP16>(a, t, decay, gs, i0);
-      continue;
-    }
-    // a tensor's last chunk, one element a thread and step
-    float* m = static_cast<float*>(t.m);
-    float* v = static_cast<float*>(t.v);
-    for (int64_t k = i0 + threadIdx.x; k < t.n; k += kThreads) {
-      const Elem e = adam_elem(a, decay, __fmul_rn(load_grad1(t, k), gs), t.param[k], m[k], v[k]);
-      t.param[k] = e.p;
-      m[k] = e.m;
-      v[k] = e.v;
-      const float p[4] = {e.p, 0.f, 0.f, 0.f};
+    adamw32_chunk<kGrad>(a, t, decay, gs, i0);
+    // the last one to three elements
+    const int64_t k = (t.n & ~int64_t(3)) + threadIdx.x;
+    if (i0 + kChunk > t.n && k < t.n) {
+      float* m = static_cast<float*>(t.m);
+      float* v = static_cast<float*>(t.v);
+      const Elem2 e = adam_elem2(a, decay, both(__fmul_rn(load_grad1(t, k), gs)), both(t.param[k]), both(m[k]), both(v[k]));
+      t.param[k] = e.p.x;
+      m[k] = e.m.x;
+      v[k] = e.v.x;
+      const float p[4] = {e.p.x, 0.f, 0.f, 0.f};
       if (t.model) t.model[k] = static_cast<uint16_t>(model4(t, p).x & 0xFFFFu);
     }
   }
@@ -209,61 +240,68 @@ __device__ __forceinline__ uint32_t random20(uint32_t key, uint32_t i) {
 // (three mantissa bits stay), so the random bits are added below it and cut
 // off; the exponent's bias goes from 127 to 7.  Below, codes are multiples of
 // 2^-9.  A positive y stays at least at the smallest code.
+__device__ __forceinline__ uint32_t encode_random_high(float y, uint32_t u20) {
+  return min(((__float_as_uint(y) + u20) >> 20) - ((127u - 7u) << 3), 0x7Eu);
+}
 __device__ __forceinline__ uint32_t encode_random(float y, uint32_t u20) {
-  const uint32_t high = min(((__float_as_uint(y) + u20) >> 20) - ((127u - 7u) << 3), 0x7Eu);
-  const uint32_t low = static_cast<uint32_t>(
+  if (y >= 0x1p-6f) return encode_random_high(y, u20);
+  return static_cast<uint32_t>(
       __fadd_rn(__fmul_rn(fmaxf(y, 0x1p-9f), 512.f), __fmul_rn(static_cast<float>(u20), 0x1p-20f)));
-  return y >= 0x1p-6f ? high : low;
 }
 
-// A warp's groups of 128 elements (four a lane), kGroups at once.
+// What a lane holds of its warp's group of 128 elements: four of them.
 struct Group8 {
-  float g[4], p[4];
+  uint4 graw;
+  float p[4];
   uint32_t mw, vw;
   float ms, vs;
 };
 template <bool kWhole>
 __device__ __forceinline__ void adamw8_group(const AdamParams& a, const AdamEntry& t, float decay, float gs,
-                                             uint32_t tensor, int64_t group, Group8& x, int have) {
+                                             uint32_t tensor, int64_t group, Group8& x, const float (&g)[4], int have) {
   const int lane = threadIdx.x % 32;
   const int64_t i = group * 128 + 4 * lane;
   uint8_t* mc = static_cast<uint8_t*>(t.m);
   uint8_t* vc = static_cast<uint8_t*>(t.v);
   float m[4], r[4];
-  const float2 ma = e4m3x2_to_f32(x.mw & 0xFFFFu), mb = e4m3x2_to_f32(x.mw >> 16);
-  const float2 va = e4m3x2_to_f32(x.vw & 0xFFFFu), vb = e4m3x2_to_f32(x.vw >> 16);
-  m[0] = ma.x; m[1] = ma.y; m[2] = mb.x; m[3] = mb.y;
-  r[0] = va.x; r[1] = va.y; r[2] = vb.x; r[3] = vb.y;
   float mmax = 0.f, rmax = 0.f;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float ro = __fmul_rn(r[j], x.vs);
-    const Elem e = adam_elem(a, decay, __fmul_rn(x.g[j], gs), x.p[j], __fmul_rn(m[j], x.ms), __fmul_rn(ro, ro));
-    const bool in = kWhole || j < have;
-    m[j] = in ? e.m : 0.f;
-    r[j] = in ? e.r : 0.f;
-    x.p[j] = e.p;
-    mmax = fmaxf(mmax, fabsf(m[j]));
-    rmax = fmaxf(rmax, r[j]);
+  for (int h = 0; h < 2; ++h) {
+    const float2 mo = __fmul2_rn(e4m3x2_to_f32(x.mw >> (16 * h) & 0xFFFFu), both(x.ms));
+    const float2 ro = __fmul2_rn(e4m3x2_to_f32(x.vw >> (16 * h) & 0xFFFFu), both(x.vs));
+    const Elem2 e = adam_elem2(a, decay, __fmul2_rn(make_float2(g[2 * h], g[2 * h + 1]), both(gs)),
+                               make_float2(x.p[2 * h], x.p[2 * h + 1]), mo, __fmul2_rn(ro, ro));
+    const bool in0 = kWhole || 2 * h < have, in1 = kWhole || 2 * h + 1 < have;
+    m[2 * h] = in0 ? e.m.x : 0.f;
+    m[2 * h + 1] = in1 ? e.m.y : 0.f;
+    r[2 * h] = in0 ? e.r.x : 0.f;
+    r[2 * h + 1] = in1 ? e.r.y : 0.f;
+    x.p[2 * h] = e.p.x;
+    x.p[2 * h + 1] = e.p.y;
+    mmax = fmaxf(mmax, fmaxf(fabsf(m[2 * h]), fabsf(m[2 * h + 1])));
+    rmax = fmaxf(rmax, fmaxf(r[2 * h], r[2 * h + 1]));
   }
   // (nonnegative floats order as their patterns do)
   mmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mmax)));
   rmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(rmax)));
-  const float mns = __fdiv_rn(mmax, 448.f), vns = __fdiv_rn(rmax, 448.f);
+  const float mns = __fmul_rn(mmax, 1.f / 448.f), vns = __fmul_rn(rmax, 1.f / 448.f);
   if (lane == 0) {
     t.m_scale[group] = mns;
     t.v_scale[group] = vns;
   }
   float mq[4], y[4];
-  if (fminf(mmax, rmax) > 1e-30f) {
-    // one reciprocal per group: the quotients are within two units of the last place
-    const float mi = __fdiv_rn(448.f, mmax), vi = __fdiv_rn(448.f, rmax);
+  if (fminf(mmax, rmax) > 1e-25f) {
+    const float mi = __frcp_rn(mns), vi = __frcp_rn(vns);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      mq[j] = __fmul_rn(m[j], mi);
-      y[j] = __fmul_rn(r[j], vi);
+    for (int h = 0; h < 2; ++h) {
+      const float2 q = quotient2(make_float2(m[2 * h], m[2 * h + 1]), mns, mi);
+      const float2 z = quotient2(make_float2(r[2 * h], r[2 * h + 1]), vns, vi);
+      mq[2 * h] = q.x;
+      mq[2 * h + 1] = q.y;
+      y[2 * h] = z.x;
+      y[2 * h + 1] = z.y;
     }
-  } else {   // zeros, or values whose reciprocal could overflow
+  } else {   // zeros, or so small that a residual could underflow
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       mq[j] = mns > 0.f ? __fdiv_rn(m[j], mns) : 0.f;
@@ -272,10 +310,17 @@ __device__ __forceinline__ void adamw8_group(const AdamParams& a, const AdamEntr
   }
   const uint32_t key = random_key(a.seed, tensor, i);
   uint32_t vo = 0;
+  if (__all_sync(0xffffffffu, fminf(fminf(y[0], y[1]), fminf(y[2], y[3])) >= 0x1p-6f)) {
+    // (roots within a factor of 28672 of the group's largest: the usual case)
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t code = encode_random(y[j], random20(key, static_cast<uint32_t>(i) + j));
-    vo |= (r[j] > 0.f && vns > 0.f ? code : 0u) << (8 * j);
+    for (int j = 0; j < 4; ++j)
+      vo |= encode_random_high(y[j], random20(key, static_cast<uint32_t>(i) + j)) << (8 * j);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t code = encode_random(y[j], random20(key, static_cast<uint32_t>(i) + j));
+      vo |= (r[j] > 0.f && vns > 0.f ? code : 0u) << (8 * j);
+    }
   }
   const uint32_t mo = cvt_e4m3x2(mq[0], mq[1]) | (static_cast<uint32_t>(cvt_e4m3x2(mq[2], mq[3])) << 16);
   if (kWhole) {
@@ -284,7 +329,9 @@ __device__ __forceinline__ void adamw8_group(const AdamParams& a, const AdamEntr
     __stcs(reinterpret_cast<uint32_t*>(vc + i), vo);
     if (t.model) *reinterpret_cast<uint2*>(t.model + i) = model4(t, x.p);
   } else {
-    for (int j = 0; j < have; ++j) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j >= have) continue;
       t.param[i + j] = x.p[j];
       mc[i + j] = static_cast<uint8_t>(mo >> (8 * j));
       vc[i + j] = static_cast<uint8_t>(vo >> (8 * j));
@@ -295,58 +342,85 @@ __device__ __forceinline__ void adamw8_group(const AdamParams& a, const AdamEntr
 }
 
 template <int kGrad>
-__device__ __forceinline__ void adamw8_chunk(const AdamParams& a, const AdamEntry& t, float decay, float gs,
-                                             uint32_t tensor, int64_t group0) {
-  const int lane = threadIdx.x % 32;
-  Group8 x[kSteps];
-#pragma unroll
-  for (int u = 0; u < kSteps; ++u) {
-    const int64_t group = group0 + u * (kThreads / 32), i = group * 128 + 4 * lane;
-    load_grad4<kGrad>(t, i, x[u].g);
-    const float4 p4 = __ldcs(reinterpret_cast<const float4*>(t.param + i));
-    x[u].p[0] = p4.x; x[u].p[1] = p4.y; x[u].p[2] = p4.z; x[u].p[3] = p4.w;
-    x[u].mw = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.m) + i));
-    x[u].vw = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.v) + i));
-    x[u].ms = t.m_scale[group];
-    x[u].vs = t.v_scale[group];
-  }
-#pragma unroll
-  for (int u = 0; u < kSteps; ++u)
-    adamw8_group<true>(a, t, decay, gs, tensor, group0 + u * (kThreads / 32), x[u], 4);
+__device__ __forceinline__ void load_group8(const AdamEntry& t, int64_t group, Group8& x) {
+  const int64_t i = group * 128 + 4 * (threadIdx.x % 32);
+  const bool ok = (group + 1) * 128 <= t.n;
+  x.graw = load_grad4<kGrad>(t, i, ok);
+  float4 p4 = {};
+  if (ok) p4 = __ldcs(reinterpret_cast<const float4*>(t.param + i));
+  x.p[0] = p4.x; x.p[1] = p4.y; x.p[2] = p4.z; x.p[3] = p4.w;
+  if (ok) x.mw = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.m) + i));
+  if (ok) x.vw = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.v) + i));
+  if (ok) x.ms = t.m_scale[group];
+  if (ok) x.vs = t.v_scale[group];
 }
 
-__global__ void __launch_bounds__(kThreads) adamw8_kernel(const AdamParams a) {
+// (apart, so that its registers are not the loop's)
+__device__ __noinline__ void adamw8_last(const AdamParams& a, float decay, float gs, uint32_t tensor) {
+  const AdamEntry t = a.table[tensor];
+  const int lane = threadIdx.x % 32;
+  const int64_t group = t.n / 128, i = group * 128 + 4 * lane;
+  const int have = t.n - i >= 4 ? 4 : t.n > i ? static_cast<int>(t.n - i) : 0;
+  Group8 x = {};
+  float g[4] = {};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (j >= have) continue;
+    g[j] = load_grad1(t, i + j);
+    x.p[j] = t.param[i + j];
+    x.mw |= static_cast<uint32_t>(static_cast<const uint8_t*>(t.m)[i + j]) << (8 * j);
+    x.vw |= static_cast<uint32_t>(static_cast<const uint8_t*>(t.v)[i + j]) << (8 * j);
+  }
+  x.ms = t.m_scale[group];
+  x.vs = t.v_scale[group];
+  __syncwarp();   // (lane 0 rewrites the scales that every lane has read)
+  adamw8_group<false>(a, t, decay, gs, tensor, group, x, g, have);
+}
+
+// While a CTA computes a chunk, its next chunk's loads are in flight (where
+// that is of the same tensor): with loads and arithmetic in turn the warps
+// mostly waited.  The CTAs walk the chunks side by side, not each a stretch of
+// its own: a thousand separate streams cost the translation of as many pages.
+template <int kGrad>
+__global__ void __launch_bounds__(kThreads, 4) adamw8_kernel(const __grid_constant__ AdamParams a) {
   pdl_wait();
   if (a.skip && *a.skip) return;
   const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  for (int64_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
+  const int warp = threadIdx.x / 32;
+  constexpr int kWarps = kThreads / 32;
+  int64_t c = blockIdx.x;
+  while (c < a.chunks) {
     const int index = find_entry(a, c);
     const AdamEntry t = a.table[index];
-    const float decay = static_cast<float>(1.0 - a.lr * t.weight_decay);
-    const int64_t group0 = (c - t.first_chunk) * (kChunk / 128) + warp;
-    if ((c - t.first_chunk + 1) * kChunk <= t.n) {
-      if (t.grad_dtype == MOE_TYPE_FP32) adamw8_chunk<MOE_TYPE_FP32>(a, t, decay, gs, index, group0);
-      else if (t.grad_dtype == MOE_TYPE_BF16) adamw8_chunk<MOE_TYPE_BF16>(a, t, decay, gs, index, group0);
-      else adamw8_chunk<MOE_TYPE_FP16>(a, t, decay, gs, index, group0);
-      continue;
+    const int64_t past = t.first_chunk + (t.n + kChunk - 1) / kChunk;   // the tensor's chunks end here
+    const float decay = fmaf(-a.lr, t.weight_decay, 1.0f);
+    const uint32_t id = static_cast<uint32_t>(index);
+    Group8 next[kSteps];
+    int64_t group = (c - t.first_chunk) * (kChunk / 128) + warp;
+    if (t.grad_dtype == kGrad) {
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u) load_group8<kGrad>(t, group + u * kWarps, next[u]);
     }
-    // a tensor's last chunk: a group at a time, the last one partly filled
-    for (int64_t group = group0; group * 128 < t.n && group < (c - t.first_chunk + 1) * (kChunk / 128);
-         group += kThreads / 32) {
-      const int64_t i = group * 128 + 4 * lane;
-      const int have = t.n - i >= 4 ? 4 : t.n > i ? static_cast<int>(t.n - i) : 0;
-      Group8 x = {};
-      for (int j = 0; j < have; ++j) {
-        x.g[j] = load_grad1(t, i + j);
-        x.p[j] = t.param[i + j];
-        x.mw |= static_cast<uint32_t>(static_cast<const uint8_t*>(t.m)[i + j]) << (8 * j);
-        x.vw |= static_cast<uint32_t>(static_cast<const uint8_t*>(t.v)[i + j]) << (8 * j);
+    for (; c < past; c += gridDim.x) {
+      if (t.grad_dtype != kGrad) continue;
+      Group8 x[kSteps];
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u) x[u] = next[u];
+      const int64_t ahead = group + static_cast<int64_t>(gridDim.x) * (kChunk / 128);
+      if (c + gridDim.x < past) {
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) load_group8<kGrad>(t, ahead + u * kWarps, next[u]);
       }
-      x.ms = t.m_scale[group];
-      x.vs = t.v_scale[group];
-      __syncwarp();   // (lane 0 rewrites the scales that every lane has read)
-      adamw8_group<false>(a, t, decay, gs, static_cast<uint32_t>(index), group, x, have);
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u) {
+        if ((group + u * kWarps + 1) * 128 > t.n) continue;
+        float g[4];
+        grad4<kGrad>(x[u].graw, g);
+        adamw8_group<true>(a, t, decay, gs, id, group + u * kWarps, x[u], g, 4);
+      }
+      // a partly filled last group
+      if (c + 1 == past && t.n % 128 && warp == 0) adamw8_last(a, decay, gs, id);
+      group = ahead;
     }
   }
 }
@@ -362,14 +436,15 @@ size_t moe_adamw_table_bytes(int count) {
 }
 
 moe_status moe_adamw_table_init(const moe_adamw_tensor* tensors, int count, int state_bits, void* table,
-                                size_t table_bytes, int64_t* chunks, moe_stream_t stream) {
+                                size_t table_bytes, int64_t* chunks, int32_t* grad_types, moe_stream_t stream) {
   using namespace moe;
   if (state_bits != 32 && state_bits != 8) return MOE_ERR_DTYPE;
   if (count < 1 || count > 65536) return MOE_ERR_SHAPE;
-  if (!tensors || !table || !chunks) return MOE_ERR_NULL;
+  if (!tensors || !table || !chunks || !grad_types) return MOE_ERR_NULL;
   if (!aligned16(table)) return MOE_ERR_ALIGN;
   if (table_bytes < moe_adamw_table_bytes(count)) return MOE_ERR_CAPACITY;
   int64_t total = 0;
+  int32_t types = 0;
   std::vector<AdamEntry> host;
   try {
     host.resize(static_cast<size_t>(count));
@@ -398,10 +473,11 @@ moe_status moe_adamw_table_init(const moe_adamw_tensor* tensors, int count, int 
     e.v_scale = t.exp_avg_sq_scale;
     e.n = t.n;
     e.first_chunk = total;
-    e.weight_decay = t.weight_decay;
+    e.weight_decay = static_cast<float>(t.weight_decay);
     e.grad_dtype = t.grad_dtype;
     e.model_dtype = t.model ? t.model_dtype : MOE_TYPE_BF16;
     total += ceil_div(t.n, kChunk);
+    if (t.n > 0) types |= 1 << t.grad_dtype;
   }
   DeviceInfo dev;
   if (current_device(&dev) != MOE_OK) return MOE_ERR_CUDA;
@@ -418,6 +494,7 @@ moe_status moe_adamw_table_init(const moe_adamw_tensor* tensors, int count, int 
   MOE_CUDA_TRY(cudaMemcpyAsync(table, host.data(), host.size() * sizeof(AdamEntry), cudaMemcpyHostToDevice, stream));
   MOE_CUDA_TRY(cudaStreamSynchronize(stream));
   *chunks = total;
+  *grad_types = types;
   return MOE_OK;
 }
 
@@ -425,7 +502,7 @@ moe_status moe_adamw_step(const moe_adamw_args* g, moe_stream_t stream) {
   using namespace moe;
   if (!g) return MOE_ERR_NULL;
   if (g->state_bits != 32 && g->state_bits != 8) return MOE_ERR_DTYPE;
-  if (g->count < 1 || g->count > 65536 || g->chunks < 0 || g->step < 1 || !(g->lr >= 0) || !std::isfinite(g->lr) ||
+  if (g->count < 1 || g->count > 65536 || g->chunks < 0 || g->grad_types < 0 || g->grad_types > 7 || g->step < 1 || !(g->lr >= 0) || !std::isfinite(g->lr) ||
       !(g->eps >= 0) || !std::isfinite(g->eps) || !(g->beta1 >= 0 && g->beta1 < 1) ||
       !(g->beta2 >= 0 && g->beta2 < 1))
     return MOE_ERR_SHAPE;
@@ -441,7 +518,7 @@ moe_status moe_adamw_step(const moe_adamw_args* g, moe_stream_t stream) {
   p.grad_scale = g->grad_scale;
   p.skip = g->skip;
   p.chunks = g->chunks;
-  p.lr = g->lr;
+  p.lr = static_cast<float>(g->lr);
   p.beta1 = static_cast<float>(g->beta1);
   p.one_minus_beta1 = static_cast<float>(1.0 - g->beta1);
   p.beta2 = static_cast<float>(g->beta2);
@@ -452,10 +529,21 @@ moe_status moe_adamw_step(const moe_adamw_args* g, moe_stream_t stream) {
   p.eps = static_cast<float>(g->eps);
   p.seed = g->seed;
   p.count = g->count;
-  const int64_t most = static_cast<int64_t>(dev.sms) * 8;
+  // as many CTAs as are resident at once
+  const int64_t most = static_cast<int64_t>(dev.sms) * (g->state_bits == 32 ? 16 : 4);
   const unsigned grid = static_cast<unsigned>(g->chunks < most ? g->chunks : most);
-  MOE_CUDA_TRY(launch_pdl(g->state_bits == 32 ? adamw32_kernel : adamw8_kernel, dim3(grid), dim3(kThreads), 0, stream,
-                          1, p));
+  // a kernel for each type of gradient that the table holds
+  for (int type = 0; type < 3; ++type) {
+    if (!(g->grad_types >> type & 1)) continue;
+    const auto kernel = g->state_bits == 32
+                            ? (type == MOE_TYPE_BF16   ? adamw32_kernel<MOE_TYPE_BF16>
+                               : type == MOE_TYPE_FP16 ? adamw32_kernel<MOE_TYPE_FP16>
+                                                       : adamw32_kernel<MOE_TYPE_FP32>)
+                            : (type == MOE_TYPE_BF16   ? adamw8_kernel<MOE_TYPE_BF16>
+                               : type == MOE_TYPE_FP16 ? adamw8_kernel<MOE_TYPE_FP16>
+                                                       : adamw8_kernel<MOE_TYPE_FP32>);
+    MOE_CUDA_TRY(launch_pdl(kernel, dim3(grid), dim3(kThreads), 0, stream, 1, p));
+  }
   return MOE_OK;
 }
 

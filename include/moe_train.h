@@ -175,7 +175,7 @@ typedef struct moe_swiglu_backward_args {
 moe_status moe_swiglu_backward(const moe_swiglu_backward_args* args, moe_stream_t stream);
 
 /* ------------------------------------------------------------------------
- * AdamW over many tensors in one launch.  Per element, in FP32:
+ * AdamW over many tensors in one launch (one for each type of gradient).  Per element, in FP32:
  *   g = grad * *grad_scale                      (1 without grad_scale)
  *   m = beta1 m + (1 - beta1) g
  *   v = beta2 v + (1 - beta2) g^2
@@ -212,10 +212,10 @@ size_t moe_adamw_table_bytes(int count);
 /* Check `tensors` (HOST array) and copy their table to the device.  Pointers
  * 16-byte aligned (scales: 4-byte), no two tensors overlapping; the array may
  * be reused when the call returns, the device buffers it names have to live
- * as long as the table.  Writes the table's number of work chunks through the
- * host pointer `chunks`.  1 <= count <= 65536; state_bits 32 or 8. */
+ * as long as the table.  Writes, through the host pointers, the table's number
+ * of work chunks and which gradient types it has (bit MOE_TYPE_*).  1 <= count <= 65536; state_bits 32 or 8. */
 moe_status moe_adamw_table_init(const moe_adamw_tensor* tensors, int count, int state_bits, void* table,
-                                size_t table_bytes, int64_t* chunks, moe_stream_t stream);
+                                size_t table_bytes, int64_t* chunks, int32_t* grad_types, moe_stream_t stream);
 
 typedef struct moe_adamw_args {
   const void* table;           /* written by moe_adamw_table_init                         */
@@ -227,6 +227,7 @@ typedef struct moe_adamw_args {
   uint32_t seed;               /* state bits 8                                            */
   int32_t count;
   int32_t state_bits;          /* as given to moe_adamw_table_init                        */
+  int32_t grad_types;          /* from moe_adamw_table_init                               */
 } moe_adamw_args;
 
 /* lr, eps >= 0 and finite; 0 <= beta1, beta2 < 1; step >= 1. */

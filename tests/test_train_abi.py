@@ -136,14 +136,14 @@ def test_adamw_refusals(L):
     t = (L.MoeAdamWTensor * 1)()
     e = t[0]
     e.param, e.grad, e.exp_avg, e.exp_avg_sq, e.n, e.grad_dtype = 1 << 20, 2 << 20, 3 << 20, 4 << 20, 100, 2
-    chunks = ctypes.c_int64()
+    chunks, types = ctypes.c_int64(), ctypes.c_int32()
     table = ctypes.c_void_p(8 << 20)
 
     def init(want, bits=32, count=1, tab=table, nbytes=size, **fields):
         old = {k: getattr(e, k) for k in fields}
         for k, v in fields.items():
             setattr(e, k, v)
-        got = lib.moe_adamw_table_init(t, count, bits, tab, nbytes, ctypes.byref(chunks), None)
+        got = lib.moe_adamw_table_init(t, count, bits, tab, nbytes, ctypes.byref(chunks), ctypes.byref(types), None)
         for k, v in old.items():
             setattr(e, k, v)
         assert got == want, (fields, got)
@@ -163,7 +163,7 @@ def test_adamw_refusals(L):
     assert f(None, None) == NULL
     _refused(f, a, DTYPE, state_bits=4)
     nan = float("nan")
-    for bad in ({"count": 0}, {"chunks": -1}, {"step": 0}, {"lr": -1.0}, {"lr": nan}, {"lr": float("inf")}, {"eps": -1.0},
+    for bad in ({"count": 0}, {"chunks": -1}, {"grad_types": 8}, {"grad_types": -1}, {"step": 0}, {"lr": -1.0}, {"lr": nan}, {"lr": float("inf")}, {"eps": -1.0},
                 {"beta1": 1.0}, {"beta1": nan}, {"beta2": -0.1}):
         _refused(f, a, SHAPE, **bad)
     _refused(f, a, NULL, table=None)
