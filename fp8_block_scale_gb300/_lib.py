@@ -575,6 +575,14 @@ def _rows2d(name, t, dtype=None):
     return t.data_ptr(), t.stride(0)
 
 
+def _row_buffer(name, t):
+    """(rows, width, row stride) of a 2D row buffer."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or stride[1] != 1:
+        raise ValueError(f"{name}: a 2D tensor with contiguous rows is expected")
+    return shape[0], shape[1], stride[0]
+
+
 def _dense(name, t, dtype=None, numel=None):
     if not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous tensor is expected")
@@ -610,27 +618,30 @@ def moe_plan_groups(sorted_token_ids, expert_ids, num_tokens_post_padded, block_
 
 def moe_gather_rows(x, xs, route_ids, top_k, num_rows=None, stream=None):
     """xs[s] = x[route_ids[s] // top_k]; zero rows where the id is none of the len(x) * top_k routes."""
-    xp, ldx = _rows2d("x", x)
-    xsp, ldxs = _rows2d("xs", xs, x.dtype)
-    if xs.shape[1] != x.shape[1]:
-        raise ValueError("x and xs differ in width")
-    _dense("route_ids", route_ids, torch.int32, xs.shape[0])
-    _opt("num_rows", num_rows, torch.int32, 1)
-    _check("moe_gather_rows", load().moe_gather_rows(
-        xp, x.shape[0], x.shape[1], ldx, xsp, xs.shape[0], ldxs, _ptr(route_ids), top_k, _ptr(num_rows),
-        TYPE_CODES[x.dtype], _stream(stream)))
+    M, width, ldx = _row_buffer("x", x)
+    rows, w2, ldxs = _row_buffer("xs", xs)
+    if width != w2 or x.dtype != xs.dtype:
+        raise ValueError("x and xs differ in width or type")
+    status = load().moe_gather_rows(
+        x.data_ptr(), M, width, ldx, xs.data_ptr(), rows, ldxs, _dense("route_ids", route_ids, torch.int32, rows), top_k,
+        None if num_rows is None else _dense("num_rows", num_rows, torch.int32, 1), TYPE_CODES[x.dtype],
+        _stream(stream))
+    if status:
+        raise MoeError("moe_gather_rows", status)
 
 
 def moe_sum_routes(y, out, route_slot, top_k, accumulate=False, stream=None):
     """out[t] = sum of y[route_slot[t * top_k + j]] over j (on top of out[t] with accumulate)."""
-    yp, ldy = _rows2d("y", y)
-    op, ldo = _rows2d("out", out, y.dtype)
-    if out.shape[1] != y.shape[1]:
-        raise ValueError("y and out differ in width")
-    _dense("route_slot", route_slot, torch.int32, out.shape[0] * top_k)
-    _check("moe_sum_routes", load().moe_sum_routes(
-        yp, y.shape[0], y.shape[1], ldy, op, out.shape[0], ldo, _ptr(route_slot), top_k, 1 if accumulate else 0,
-        TYPE_CODES[y.dtype], _stream(stream)))
+    rows, width, ldy = _row_buffer("y", y)
+    M, w2, ldo = _row_buffer("out", out)
+    if width != w2 or y.dtype != out.dtype:
+        raise ValueError("y and out differ in width or type")
+    status = load().moe_sum_routes(
+        y.data_ptr(), rows, width, ldy, out.data_ptr(), M, ldo,
+        _dense("route_slot", route_slot, torch.int32, M * top_k), top_k, 1 if accumulate else 0, TYPE_CODES[y.dtype],
+        _stream(stream))
+    if status:
+        raise MoeError("moe_sum_routes", status)
 
 
 def make_grouped_args(x, w, y, group_start, group_rows, input_gradient=False, epilogue=GROUPED_PLAIN, pre=None,

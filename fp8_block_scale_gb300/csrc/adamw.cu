@@ -382,7 +382,7 @@ __device__ __noinline__ void adamw8_last(const AdamParams& a, float decay, float
 // mostly waited.  The CTAs walk the chunks side by side, not each a stretch of
 // its own: a thousand separate streams cost the translation of as many pages.
 template <int kGrad>
-__global__ void __launch_bounds__(kThreads, 4) adamw8_kernel(const __grid_constant__ AdamParams a) {
+__global__ void __launch_bounds__(kThreads, 3) adamw8_kernel(const __grid_constant__ AdamParams a) {
   pdl_wait();
   if (a.skip && *a.skip) return;
   const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
@@ -530,7 +530,7 @@ moe_status moe_adamw_step(const moe_adamw_args* g, moe_stream_t stream) {
   p.seed = g->seed;
   p.count = g->count;
   // as many CTAs as are resident at once
-  const int64_t most = static_cast<int64_t>(dev.sms) * (g->state_bits == 32 ? 16 : 4);
+  const int64_t most = static_cast<int64_t>(dev.sms) * (g->state_bits == 32 ? 16 : 3);
   const unsigned grid = static_cast<unsigned>(g->chunks < most ? g->chunks : most);
   // a kernel for each type of gradient that the table holds
   for (int type = 0; type < 3; ++type) {
