@@ -33,8 +33,8 @@ namespace {
 
 enum Mode { kForward, kSwiglu, kDgrad, kWgrad };
 
-constexpr int kThreads = 288;
-constexpr int kEpiWarps = 4;
+constexpr int kThreads = 352;
+
 constexpr int kTileM = 256, kTileN = 256, kTileZ = 64;   // per pair; contraction elements per stage
 constexpr int kABytes = 128 * kTileZ * 2;                // per CTA and stage
 constexpr int kBBytes = 128 * kTileZ * 2;
@@ -42,8 +42,10 @@ constexpr int kMaxE = 2048;
 
 template <Mode kMode> struct Cfg {
   static constexpr int kStages = kMode == kWgrad ? 5 : 6;
-  // tensor-store staging; the few-slots path's sums
-  static constexpr int kStoreBytes = kMode == kWgrad ? kEpiWarps * 2 * 4096 : kMode == kDgrad ? 0 : 16384;
+  // the epilogue's transposition; the few-slots path's sums
+  static constexpr int kStoreBytes = kMode == kWgrad ? 8 * 4096 : kMode == kDgrad ? 0 : 16384;
+  // epilogue warps: 2-5, and 7-10 (each lane quarter's second warp takes the columns' second half)
+  static constexpr int kEpiWarps = kMode == kWgrad ? 8 : 4;
 };
 constexpr int kMaxStages = 6;
 constexpr int kSumBuffers = 4;
@@ -81,6 +83,7 @@ struct Params {
   const uint16_t* w;
   uint16_t* y;
   uint16_t* pre;
+  void* dw;        // wgrad
   int64_t ldx, ldy, ldpre, R;
   int rows;        // slots of the row buffers
   int E;
@@ -97,7 +100,6 @@ struct Maps {
   CUtensorMap a;
   CUtensorMap b[3];    // K-major B: boxes of 32, 64 and 128 slots; wgrad: [0]
   CUtensorMap ag, bg;  // wgrad: single rows, for gather4
-  CUtensorMap c;       // wgrad: dw
 };
 
 struct Tile {
@@ -175,33 +177,70 @@ __device__ __forceinline__ void count_tiles(const Params& p, Ctl* ctl) {
   }
 }
 
+// Walks a CTA pair's tiles in ascending order (whole warps).  The group's
+// search goes on from the last tile's, 32 groups at a step, and its table
+// entries are fetched a tile ahead: a lookup from the start, of 0.7 us, held
+// up tiles that are only a few blocks long.
 template <Mode kMode>
-__device__ __forceinline__ Tile tile_at(const Params& p, const Ctl* ctl, uint32_t tile) {
-  int lo = 0, hi = p.E;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (ctl->first[mid] <= tile) lo = mid; else hi = mid;
+struct Tiles {
+  const Params& p;
+  const Ctl* ctl;
+  uint32_t tile, step, total;
+  int e = 0;             // group of `tile`
+  int s0 = 0, n = 0;
+
+  __device__ __forceinline__ Tiles(const Params& p_, const Ctl* ctl_, uint32_t first, uint32_t step_)
+      : p(p_), ctl(ctl_), tile(first), step(step_), total(ctl_->first[p_.E]) {
+    find();
   }
-  Tile t;
-  t.e = lo;
-  group_at(p, lo, t.s0, t.slots);
-  const int local = static_cast<int>(tile - ctl->first[lo]);
-  if (kMode == kWgrad) {
-    const int nts = (p.n + kTileN - 1) / kTileN;
-    t.m0 = local / nts * kTileM;
-    t.n0 = local % nts * kTileN;
-    t.nt = min(kTileN, p.n - t.n0);
-    t.nkb = (t.slots + kTileZ - 1) / kTileZ;
-  } else {
-    const int nts = (t.slots + kTileN - 1) / kTileN;
-    const int width = ((t.slots + nts - 1) / nts + 31) / 32 * 32;
-    t.m0 = local / nts * kTileM;
-    t.n0 = local % nts * width;
-    t.nt = min(width, t.slots - t.n0);
-    t.nkb = (p.z + kTileZ - 1) / kTileZ;
+  __device__ __forceinline__ bool done() const { return tile >= total; }
+  __device__ __forceinline__ void find() {
+    if (done()) return;
+    // the last group whose first tile is not past this one
+    for (;;) {
+      const int i = e + 1 + static_cast<int>(threadIdx.x % 32);
+      const uint32_t past = __ballot_sync(0xffffffffu, i >= p.E || ctl->first[i] > tile);
+      if (past) {
+        e += __ffs(past) - 1;
+        break;
+      }
+      e += 32;
+    }
+    group_at(p, e, s0, n);
   }
-  return t;
-}
+  __device__ __forceinline__ void next() {
+    tile += step;
+    find();
+  }
+  __device__ __forceinline__ Tile get() const {
+    Tile t;
+    t.e = e;
+    t.s0 = s0;
+    t.slots = n;
+    const uint32_t local = tile - ctl->first[e];
+    if (kMode == kWgrad) {
+      const uint32_t nts = (p.n + kTileN - 1) / kTileN, m = local / nts;
+      t.m0 = static_cast<int>(m * kTileM);
+      t.n0 = static_cast<int>((local - m * nts) * kTileN);
+      t.nt = min(kTileN, p.n - t.n0);
+      t.nkb = (n + kTileZ - 1) / kTileZ;
+    } else {
+      t.nkb = (p.z + kTileZ - 1) / kTileZ;
+      if (n <= kTileN) {
+        t.m0 = static_cast<int>(local * kTileM);
+        t.n0 = 0;
+        t.nt = n;
+        return t;
+      }
+      const uint32_t nts = (n + kTileN - 1) / kTileN, m = local / nts;
+      const int width = static_cast<int>((n + nts - 1) / nts + 31) / 32 * 32;
+      t.m0 = static_cast<int>(m * kTileM);
+      t.n0 = static_cast<int>(local - m * nts) * width;
+      t.nt = min(width, n - t.n0);
+    }
+    return t;
+  }
+};
 
 // Two values that this lane holds for columns c and c + 1 of its row, against
 // the neighbour's: the even lane returns rows (lane, lane + 1) of column c,
@@ -455,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&ctl->tfull[b]), 1);
-      mbar_init(smem_u32(&ctl->tempty[b]), 2 * kEpiWarps);
+      mbar_init(smem_u32(&ctl->tempty[b]), 2 * Cfg<kMode>::kEpiWarps);
     }
     for (int b = 0; b < kSumBuffers; ++b) {
       mbar_init(smem_u32(&ctl->sfull[b]), 8);
@@ -476,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (kFew && ctl->most <= kFewSlots && total <= kFewGroups * static_cast<uint32_t>((p.m + kTileM - 1) / kTileM)) {
     if (warp < kFewWarps)
       few_slots_stream<kMode, T>(p, ctl, sA, reinterpret_cast<float*>(sC));
-    else
+    else if (warp == kFewWarps)
       few_slots_finish<kMode, T>(p, ctl, reinterpret_cast<const float*>(sC));
     __syncthreads();
     if (threadIdx.x == 0 && ctl->abort_flag && p.status) atomicOr(p.status, MOE_DEV_TIMEOUT);
@@ -498,9 +537,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lead_full0 = pair::mapa_shared(smem_u32(&ctl->full[0]), 0);
     uint32_t it = 0;
     bool ok = true;
-    // lane 0 issues; wgrad's other lanes come along for the row-by-row copies
-    for (uint32_t tile = tile0; tile < total && ok && (kMode == kWgrad || lane == 0); tile += step) {
-      const Tile t = tile_at<kMode>(p, ctl, tile);
+    // lane 0 issues (wgrad's row-by-row copies: all lanes)
+    Tiles<kMode> tiles(p, ctl, tile0, step);
+    while (!tiles.done() && ok) {
+      const Tile t = tiles.get();
+      tiles.next();
       const int half = (t.nt + 31) / 32 * 16;               // N columns of each CTA
       const int chunks = (half + 63) / 64;                  // N-major B: 64-column boxes
       const int bsel = half <= 32 ? 0 : half <= 64 ? 1 : 2; // K-major B: box of 32, 64 or 128 slots
@@ -546,10 +587,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (kMode == kWgrad) {
-        it = __shfl_sync(0xffffffffu, it, 0);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-      }
+      it = __shfl_sync(0xffffffffu, it, 0);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
       if (kMode == kWgrad && last < t.nkb) {
         // row by row instead; row -1 reads as zeros
         const int s = it % kStages, z = last * kTileZ;
@@ -580,49 +619,54 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader)
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       uint32_t it = 0, done = 0;
       bool ok = true;
-      for (uint32_t tile = tile0; tile < total && ok; tile += step) {
-        const Tile t = tile_at<kMode>(p, ctl, tile);
+      Tiles<kMode> tiles(p, ctl, tile0, step);
+      while (!tiles.done() && ok) {
+        const Tile t = tiles.get();
+        tiles.next();
         if (t.nkb == 0) continue;
-        const uint32_t idesc = pair::idesc_f16(p.format, kAmn, kBmn, (t.nt + 31) / 32 * 32);
-        const uint32_t tb = done & 1u, d = tmem_base + tb * kTileN;
-        if (!mbar_wait(smem_u32(&ctl->tempty[tb]), ((done >> 1) & 1u) ^ 1u, abort_flag)) break;
-        tc_fence_after();
-        for (int kb = 0; kb < t.nkb; ++kb, ++it) {
-          const int s = it % kStages;
-          if (!mbar_wait(smem_u32(&ctl->full[s]), (it / kStages) & 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
+        if (lane == 0) {
+          const uint32_t idesc = pair::idesc_f16(p.format, kAmn, kBmn, (t.nt + 31) / 32 * 32);
+          const uint32_t tb = done & 1u, d = tmem_base + tb * kTileN;
+          ok = mbar_wait(smem_u32(&ctl->tempty[tb]), ((done >> 1) & 1u) ^ 1u, abort_flag);
           tc_fence_after();
-          const uint32_t a = smem_u32(sA + s * kABytes), b = smem_u32(sB + s * kBBytes);
+          for (int kb = 0; kb < t.nkb && ok; ++kb, ++it) {
+            const int s = it % kStages;
+            if (!mbar_wait(smem_u32(&ctl->full[s]), (it / kStages) & 1u, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a = smem_u32(sA + s * kABytes), b = smem_u32(sB + s * kBBytes);
 #pragma unroll
-          for (int kk = 0; kk < kTileZ / 16; ++kk)
-            pair::umma_f16(d, kAmn ? pair::sw128_mnmajor_desc(a + 2048u * kk, 8192u) : sw128_kmajor_desc(a + 32u * kk),
-                           kBmn ? pair::sw128_mnmajor_desc(b + 2048u * kk, 8192u) : sw128_kmajor_desc(b + 32u * kk),
-                           idesc, kb > 0 || kk > 0 ? 1u : 0u);
-          pair::umma_commit(smem_u32(&ctl->empty[s]));
+            for (int kk = 0; kk < kTileZ / 16; ++kk)
+              pair::umma_f16(d, kAmn ? pair::sw128_mnmajor_desc(a + 2048u * kk, 8192u) : sw128_kmajor_desc(a + 32u * kk),
+                             kBmn ? pair::sw128_mnmajor_desc(b + 2048u * kk, 8192u) : sw128_kmajor_desc(b + 32u * kk),
+                             idesc, kb > 0 || kk > 0 ? 1u : 0u);
+            pair::umma_commit(smem_u32(&ctl->empty[s]));
+          }
+          if (ok) pair::umma_commit(smem_u32(&ctl->tfull[tb]));
         }
-        if (ok) {
-          pair::umma_commit(smem_u32(&ctl->tfull[tb]));
-          ++done;
-        }
+        ++done;
+        ok = __shfl_sync(0xffffffffu, ok, 0);
       }
       // no MMA may still be writing TMEM when it is released
-      if (it > 0) drain_wait(smem_u32(&ctl->empty[(it - 1) % kStages]), ((it - 1) / kStages) & 1u);
+      if (lane == 0 && it > 0) drain_wait(smem_u32(&ctl->empty[(it - 1) % kStages]), ((it - 1) / kStages) & 1u);
     }
     __syncwarp();
-  } else if (warp < 6) {
+  } else if (warp < 6 || Cfg<kMode>::kEpiWarps == 8) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;   // the lanes of tensor memory that this warp may read
     const uint32_t lanes = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
     const bool odd = lane & 1;
     uint32_t done = 0;
     bool ok = true;
-    for (uint32_t tile = tile0; tile < total && ok; tile += step) {
-      const Tile t = tile_at<kMode>(p, ctl, tile);
+    Tiles<kMode> tiles(p, ctl, tile0, step);
+    while (!tiles.done() && ok) {
+      const Tile t = tiles.get();
+      tiles.next();
       const uint32_t tb = done & 1u;
       if (t.nkb > 0) {
         ok = warp_wait(smem_u32(&ctl->tfull[tb]), (done >> 1) & 1u, abort_flag);
@@ -685,13 +729,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } else {
-        // rows of dw through shared memory (128-byte swizzle) and tensor stores
-        constexpr int kCols = 128 / sizeof(Out);   // columns of one 128-byte box row
+        // rows of dw, transposed through the warp's 4 KB of shared memory
+        // (128-byte swizzle) into stores of whole 128-byte lines
+        constexpr int kCols = 128 / sizeof(Out);   // columns of a line
         const int row0 = t.m0 + 128 * static_cast<int>(rank) + 32 * q;
-        for (int c = 0; c < t.nt; c += kCols) {
-          uint8_t* box = sC + ((warp - 2) * 2 + ((c / kCols) & 1)) * 4096;
-          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-          __syncwarp();
+        uint8_t* box = sC + (warp < 6 ? warp - 2 : warp - 3) * 4096;
+        const int half = warp < 6 ? 0 : kTileN / 2;
+        for (int c = half; c < min(t.nt, half + kTileN / 2); c += kCols) {
 #pragma unroll
           for (int h = 0; h < kCols / 32; ++h) {
             uint32_t v[32];
@@ -717,17 +761,27 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
-            if (row0 < p.m) {
-              if (p.accumulate)
-                pair::reduce_add_3d(&maps.c, smem_u32(box), t.n0 + c, row0, t.e);
-              else
-                pair::store_3d(&maps.c, smem_u32(box), t.n0 + c, row0, t.e);
+          // eight lanes a row, four rows at a time
+          const int chunk = lane % 8, col = t.n0 + c + chunk * static_cast<int>(16 / sizeof(Out));
+          Out* out = static_cast<Out*>(p.dw) + (static_cast<int64_t>(t.e) * p.m + row0) * p.n + col;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + lane / 8;
+            if (row0 + r < p.m && col < p.n) {
+              uint4 v = *reinterpret_cast<const uint4*>(box + 128 * r + 16 * (chunk ^ (r & 7)));
+              uint4* dst = reinterpret_cast<uint4*>(out + static_cast<int64_t>(r) * p.n);
+              if (sizeof(Out) == 4 && p.accumulate) {
+                const uint4 old = *dst;
+                v.x = __float_as_uint(__uint_as_float(old.x) + __uint_as_float(v.x));
+                v.y = __float_as_uint(__uint_as_float(old.y) + __uint_as_float(v.y));
+                v.z = __float_as_uint(__uint_as_float(old.z) + __uint_as_float(v.z));
+                v.w = __float_as_uint(__uint_as_float(old.w) + __uint_as_float(v.w));
+              }
+              *dst = v;
             }
-            bulk_commit();
           }
+          __syncwarp();
         }
       }
       if (t.nkb > 0) {
@@ -742,7 +796,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++done;
       }
     }
-    if (kMode == kWgrad && lane == 0) bulk_wait_all();
   }
 
   tc_fence_before();
@@ -915,7 +968,7 @@ moe_status moe_grouped_gemm(const moe_grouped_args* a, moe_stream_t stream) {
     ok = ok && weight_map(&maps.a, a->dtype, a->w, a->E, a->N, a->K, 64, fwd ? 128 : 64);
   }
   if (!ok) return MOE_ERR_CUDA;
-  maps.ag = maps.bg = maps.c = maps.a;  // not used
+  maps.ag = maps.bg = maps.a;  // not used
   const int64_t mt = ceil_div(p.m, kTileM);
   const int64_t groups = a->E < a->rows ? a->E : a->rows;
   int64_t most = mt * (ceil_div(a->rows, kTileN) + groups);
@@ -961,6 +1014,7 @@ moe_status moe_grouped_wgrad(const moe_grouped_wgrad_args* a, moe_stream_t strea
   p.n = a->K;
   p.format = a->dtype == MOE_TYPE_BF16 ? 1u : 0u;
   p.accumulate = a->accumulate ? 1 : 0;
+  p.dw = a->dw;
   // without slots every group is empty and nothing is read: any address will do
   const void* dy = a->rows > 0 ? a->dy : static_cast<const uint16_t*>(a->dw);
   const void* x = a->rows > 0 ? a->x : static_cast<const uint16_t*>(a->dw);
@@ -971,8 +1025,7 @@ moe_status moe_grouped_wgrad(const moe_grouped_wgrad_args* a, moe_stream_t strea
   if (!window_map(&maps.a, a->dtype, dy, a->N, rows, a->lddy, p.a_one) ||
       !window_map(&maps.b[0], a->dtype, x, a->K, rows, a->ldx, p.b_one) ||
       !rows_map(&maps.ag, a->dtype, dy, a->N, rows, a->lddy, 1) ||
-      !rows_map(&maps.bg, a->dtype, x, a->K, rows, a->ldx, 1) ||
-      !weight_map(&maps.c, a->dw_dtype, a->dw, a->E, a->N, a->K, a->dw_dtype == MOE_TYPE_FP32 ? 32 : 64, 32))
+      !rows_map(&maps.bg, a->dtype, x, a->K, rows, a->ldx, 1))
     return MOE_ERR_CUDA;
   maps.b[1] = maps.b[2] = maps.b[0];  // not used
   const int64_t most = static_cast<int64_t>(a->E) * ceil_div(p.m, kTileM) * ceil_div(p.n, kTileN);

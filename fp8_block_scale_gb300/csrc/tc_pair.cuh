@@ -95,18 +95,6 @@ __device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap* map, ui
       "l"(map), "r"(bar), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3)
       : "memory");
 }
-// Tensor store, and FP32 add into memory, of a 3D box as a bulk group of the issuing thread.
-__device__ __forceinline__ void store_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map), "r"(src),
-               "r"(x), "r"(y), "r"(z)
-               : "memory");
-}
-__device__ __forceinline__ void reduce_add_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
-  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
-               "r"(src), "r"(x), "r"(y), "r"(z)
-               : "memory");
-}
-
 // Shared-memory descriptor of an operand stored along its M (or N) dimension:
 // boxes of 64 elements (128 bytes, 128-byte swizzle) by 64 contraction rows,
 // the next 64 elements `box_bytes` further on, 8 contraction rows 1024 bytes.
