@@ -33,7 +33,7 @@ namespace {
 
 enum Mode { kForward, kSwiglu, kDgrad, kWgrad };
 
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;
 
 constexpr int kTileM = 256, kTileN = 256, kTileZ = 64;   // per pair; contraction elements per stage
 constexpr int kABytes = 128 * kTileZ * 2;                // per CTA and stage
@@ -49,6 +49,7 @@ template <Mode kMode> struct Cfg {
 };
 constexpr int kMaxStages = 6;
 constexpr int kSumBuffers = 4;
+constexpr int kQueue = 4;
 constexpr int kFewGroups = 640;
 
 
@@ -58,6 +59,8 @@ struct Ctl {
   uint64_t tfull[2];            // accumulator complete
   uint64_t sfull[kSumBuffers], sempty[kSumBuffers];   // few slots: a unit's sums
   uint64_t tempty[2];           // (leader) accumulator drained by every epilogue warp of the pair
+  uint64_t qfull[kQueue], qempty[kQueue];             // tile queue
+  int4 queue[kQueue][2];
   uint32_t tmem_base;
   int abort_flag;
   uint32_t warp_sum[kThreads / 32];
@@ -177,10 +180,8 @@ __device__ __forceinline__ void count_tiles(const Params& p, Ctl* ctl) {
   }
 }
 
-// Walks a CTA pair's tiles in ascending order (whole warps).  The group's
-// search goes on from the last tile's, 32 groups at a step, and its table
-// entries are fetched a tile ahead: a lookup from the start, of 0.7 us, held
-// up tiles that are only a few blocks long.
+// Walks a CTA pair's tiles in ascending order (a whole warp).  The group's
+// search goes on from the last tile's, 32 groups at a step.
 template <Mode kMode>
 struct Tiles {
   const Params& p;
@@ -242,15 +243,6 @@ struct Tiles {
   }
 };
 
-// Two values that this lane holds for columns c and c + 1 of its row, against
-// the neighbour's: the even lane returns rows (lane, lane + 1) of column c,
-// the odd lane rows (lane - 1, lane) of column c + 1.
-template <typename T>
-__device__ __forceinline__ uint32_t pair_rows(float v0, float v1, bool odd) {
-  const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
-  return odd ? Pack2<T>::store(got, v1) : Pack2<T>::store(v0, got);
-}
-
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   int ok = 0;
   if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag) ? 1 : 0;
@@ -260,6 +252,53 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
   int dummy = 0;
   mbar_wait(bar, parity, &dummy);
+}
+
+// The queue's two sides.  A tile with nkb < 0 ends it.
+template <Mode kMode>
+__device__ __forceinline__ void publish_tiles(const Params& p, Ctl* ctl, uint32_t tile0, uint32_t step) {
+  volatile int* abort_flag = &ctl->abort_flag;
+  Tiles<kMode> tiles(p, ctl, tile0, step);
+  for (uint32_t i = 0;; ++i) {
+    const bool end = tiles.done();
+    Tile t = {};
+    t.nkb = -1;
+    if (!end) t = tiles.get();
+    const uint32_t q = i % kQueue;
+    if (!warp_wait(smem_u32(&ctl->qempty[q]), ((i / kQueue) & 1u) ^ 1u, abort_flag)) return;
+    if (threadIdx.x % 32 == 0) {
+      ctl->queue[q][0] = make_int4(t.e, t.m0, t.n0, t.nt);
+      ctl->queue[q][1] = make_int4(t.s0, t.slots, t.nkb, 0);
+      mbar_arrive(smem_u32(&ctl->qfull[q]));
+    }
+    if (end) return;
+    tiles.next();
+  }
+}
+// The next tile; false at the end (or once a wait has run out).  kWarp: taken
+// by a whole warp, else by one thread.
+template <bool kWarp>
+__device__ __forceinline__ bool take_tile(Ctl* ctl, uint32_t& i, Tile& t) {
+  volatile int* abort_flag = &ctl->abort_flag;
+  const uint32_t q = i % kQueue, parity = (i / kQueue) & 1u;
+  ++i;
+  const bool ok = kWarp ? warp_wait(smem_u32(&ctl->qfull[q]), parity, abort_flag)
+                        : mbar_wait(smem_u32(&ctl->qfull[q]), parity, abort_flag);
+  if (!ok) return false;
+  const int4 a = ctl->queue[q][0], b = ctl->queue[q][1];
+  t = {a.x, a.y, a.z, a.w, b.x, b.y, b.z};
+  if (kWarp) __syncwarp();
+  if (!kWarp || threadIdx.x % 32 == 0) mbar_arrive(smem_u32(&ctl->qempty[q]));
+  return t.nkb >= 0;
+}
+
+// Two values that this lane holds for columns c and c + 1 of its row, against
+// the neighbour's: the even lane returns rows (lane, lane + 1) of column c,
+// the odd lane rows (lane - 1, lane) of column c + 1.
+template <typename T>
+__device__ __forceinline__ uint32_t pair_rows(float v0, float v1, bool odd) {
+  const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+  return odd ? Pack2<T>::store(got, v1) : Pack2<T>::store(v0, got);
 }
 
 // ---------------------------------------------------------------- few slots
@@ -500,6 +539,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctl->sfull[b]), 8);
       mbar_init(smem_u32(&ctl->sempty[b]), 1);
     }
+    for (int q = 0; q < kQueue; ++q) {
+      mbar_init(smem_u32(&ctl->qfull[q]), 1);
+      // the producers, the leader's MMA issuer, the epilogue warps
+      mbar_init(smem_u32(&ctl->qempty[q]), 2 + (rank == 0 ? 1 : 0) + Cfg<kMode>::kEpiWarps);
+    }
     ctl->abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&maps.a);
@@ -538,10 +582,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = 0;
     bool ok = true;
     // lane 0 issues (wgrad's row-by-row copies: all lanes)
-    Tiles<kMode> tiles(p, ctl, tile0, step);
-    while (!tiles.done() && ok) {
-      const Tile t = tiles.get();
-      tiles.next();
+    constexpr bool kWarp = kMode == kWgrad;
+    uint32_t next = 0;
+    Tile t;
+    while ((kWarp || lane == 0) && ok && take_tile<kWarp>(ctl, next, t)) {
       const int half = (t.nt + 31) / 32 * 16;               // N columns of each CTA
       const int chunks = (half + 63) / 64;                  // N-major B: 64-column boxes
       const int bsel = half <= 32 ? 0 : half <= 64 ? 1 : 2; // K-major B: box of 32, 64 or 128 slots
@@ -587,8 +631,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      it = __shfl_sync(0xffffffffu, it, 0);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (kWarp) {
+        it = __shfl_sync(0xffffffffu, it, 0);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+      }
       if (kMode == kWgrad && last < t.nkb) {
         // row by row instead; row -1 reads as zeros
         const int s = it % kStages, z = last * kTileZ;
@@ -619,54 +665,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader)
-    if (rank == 0) {
-      uint32_t it = 0, done = 0;
+    if (rank == 0 && lane == 0) {
+      uint32_t it = 0, done = 0, next = 0;
       bool ok = true;
-      Tiles<kMode> tiles(p, ctl, tile0, step);
-      while (!tiles.done() && ok) {
-        const Tile t = tiles.get();
-        tiles.next();
+      Tile t;
+      while (ok && take_tile<false>(ctl, next, t)) {
         if (t.nkb == 0) continue;
-        if (lane == 0) {
-          const uint32_t idesc = pair::idesc_f16(p.format, kAmn, kBmn, (t.nt + 31) / 32 * 32);
-          const uint32_t tb = done & 1u, d = tmem_base + tb * kTileN;
-          ok = mbar_wait(smem_u32(&ctl->tempty[tb]), ((done >> 1) & 1u) ^ 1u, abort_flag);
-          tc_fence_after();
-          for (int kb = 0; kb < t.nkb && ok; ++kb, ++it) {
-            const int s = it % kStages;
-            if (!mbar_wait(smem_u32(&ctl->full[s]), (it / kStages) & 1u, abort_flag)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t a = smem_u32(sA + s * kABytes), b = smem_u32(sB + s * kBBytes);
-#pragma unroll
-            for (int kk = 0; kk < kTileZ / 16; ++kk)
-              pair::umma_f16(d, kAmn ? pair::sw128_mnmajor_desc(a + 2048u * kk, 8192u) : sw128_kmajor_desc(a + 32u * kk),
-                             kBmn ? pair::sw128_mnmajor_desc(b + 2048u * kk, 8192u) : sw128_kmajor_desc(b + 32u * kk),
-                             idesc, kb > 0 || kk > 0 ? 1u : 0u);
-            pair::umma_commit(smem_u32(&ctl->empty[s]));
+        const uint32_t idesc = pair::idesc_f16(p.format, kAmn, kBmn, (t.nt + 31) / 32 * 32);
+        const uint32_t tb = done & 1u, d = tmem_base + tb * kTileN;
+        if (!mbar_wait(smem_u32(&ctl->tempty[tb]), ((done >> 1) & 1u) ^ 1u, abort_flag)) break;
+        tc_fence_after();
+        for (int kb = 0; kb < t.nkb; ++kb, ++it) {
+          const int s = it % kStages;
+          if (!mbar_wait(smem_u32(&ctl->full[s]), (it / kStages) & 1u, abort_flag)) {
+            ok = false;
+            break;
           }
-          if (ok) pair::umma_commit(smem_u32(&ctl->tfull[tb]));
+          tc_fence_after();
+          const uint32_t a = smem_u32(sA + s * kABytes), b = smem_u32(sB + s * kBBytes);
+#pragma unroll
+          for (int kk = 0; kk < kTileZ / 16; ++kk)
+            pair::umma_f16(d, kAmn ? pair::sw128_mnmajor_desc(a + 2048u * kk, 8192u) : sw128_kmajor_desc(a + 32u * kk),
+                           kBmn ? pair::sw128_mnmajor_desc(b + 2048u * kk, 8192u) : sw128_kmajor_desc(b + 32u * kk),
+                           idesc, kb > 0 || kk > 0 ? 1u : 0u);
+          pair::umma_commit(smem_u32(&ctl->empty[s]));
         }
-        ++done;
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (ok) {
+          pair::umma_commit(smem_u32(&ctl->tfull[tb]));
+          ++done;
+        }
       }
       // no MMA may still be writing TMEM when it is released
-      if (lane == 0 && it > 0) drain_wait(smem_u32(&ctl->empty[(it - 1) % kStages]), ((it - 1) / kStages) & 1u);
+      if (it > 0) drain_wait(smem_u32(&ctl->empty[(it - 1) % kStages]), ((it - 1) / kStages) & 1u);
     }
     __syncwarp();
+  } else if (warp == 11) {
+    publish_tiles<kMode>(p, ctl, tile0, step);
   } else if (warp < 6 || Cfg<kMode>::kEpiWarps == 8) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;   // the lanes of tensor memory that this warp may read
     const uint32_t lanes = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
     const bool odd = lane & 1;
-    uint32_t done = 0;
+    uint32_t done = 0, next = 0;
     bool ok = true;
-    Tiles<kMode> tiles(p, ctl, tile0, step);
-    while (!tiles.done() && ok) {
-      const Tile t = tiles.get();
-      tiles.next();
+    Tile t;
+    while (ok && take_tile<true>(ctl, next, t)) {
       const uint32_t tb = done & 1u;
       if (t.nkb > 0) {
         ok = warp_wait(smem_u32(&ctl->tfull[tb]), (done >> 1) & 1u, abort_flag);
