@@ -44,7 +44,7 @@ template <Mode kMode> struct Cfg {
   static constexpr int kStages = kMode == kWgrad ? 5 : 6;
   // the epilogue's transposition; the few-slots path's sums
   static constexpr int kStoreBytes = kMode == kWgrad ? 8 * 4096 : kMode == kDgrad ? 0 : 16384;
-  // epilogue warps: 2-5, and 7-10 (each lane quarter's second warp takes the columns' second half)
+  // epilogue warps: 2-5, and 7-10 (each lane quarter's second warp takes every other 128 bytes of columns)
   static constexpr int kEpiWarps = kMode == kWgrad ? 8 : 4;
 };
 constexpr int kMaxStages = 6;
@@ -180,34 +180,39 @@ __device__ __forceinline__ void count_tiles(const Params& p, Ctl* ctl) {
   }
 }
 
-// Walks a CTA pair's tiles in ascending order (a whole warp).  The group's
-// search goes on from the last tile's, 32 groups at a step.
+// Walks a CTA pair's tiles in ascending order (a whole warp).  Each lane holds
+// the table entries of one of 32 groups, so that most steps touch no memory.
 template <Mode kMode>
 struct Tiles {
   const Params& p;
   const Ctl* ctl;
   uint32_t tile, step, total;
+  int base = 0;          // lane l holds group base + l
+  uint32_t my_first = 0, my_past = 0;   // its tiles: [my_first, my_past)
+  int my_s0 = 0, my_n = 0;
   int e = 0;             // group of `tile`
-  int s0 = 0, n = 0;
 
   __device__ __forceinline__ Tiles(const Params& p_, const Ctl* ctl_, uint32_t first, uint32_t step_)
       : p(p_), ctl(ctl_), tile(first), step(step_), total(ctl_->first[p_.E]) {
+    load();
     find();
   }
   __device__ __forceinline__ bool done() const { return tile >= total; }
+  __device__ __forceinline__ void load() {
+    const int g = min(base + static_cast<int>(threadIdx.x % 32), p.E - 1);
+    my_first = ctl->first[g];
+    my_past = ctl->first[g + 1];
+    group_at(p, g, my_s0, my_n);
+  }
   __device__ __forceinline__ void find() {
     if (done()) return;
-    // the last group whose first tile is not past this one
-    for (;;) {
-      const int i = e + 1 + static_cast<int>(threadIdx.x % 32);
-      const uint32_t past = __ballot_sync(0xffffffffu, i >= p.E || ctl->first[i] > tile);
-      if (past) {
-        e += __ffs(past) - 1;
-        break;
-      }
-      e += 32;
+    // the first group whose tiles are not all before this one
+    uint32_t past;
+    while ((past = __ballot_sync(0xffffffffu, my_past > tile)) == 0) {
+      base += 32;
+      load();
     }
-    group_at(p, e, s0, n);
+    e = base + __ffs(past) - 1;
   }
   __device__ __forceinline__ void next() {
     tile += step;
@@ -215,10 +220,11 @@ struct Tiles {
   }
   __device__ __forceinline__ Tile get() const {
     Tile t;
+    const int n = __shfl_sync(0xffffffffu, my_n, e - base);
     t.e = e;
-    t.s0 = s0;
+    t.s0 = __shfl_sync(0xffffffffu, my_s0, e - base);
     t.slots = n;
-    const uint32_t local = tile - ctl->first[e];
+    const uint32_t local = tile - __shfl_sync(0xffffffffu, my_first, e - base);
     if (kMode == kWgrad) {
       const uint32_t nts = (p.n + kTileN - 1) / kTileN, m = local / nts;
       t.m0 = static_cast<int>(m * kTileM);
@@ -777,8 +783,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kCols = 128 / sizeof(Out);   // columns of a line
         const int row0 = t.m0 + 128 * static_cast<int>(rank) + 32 * q;
         uint8_t* box = sC + (warp < 6 ? warp - 2 : warp - 3) * 4096;
-        const int half = warp < 6 ? 0 : kTileN / 2;
-        for (int c = half; c < min(t.nt, half + kTileN / 2); c += kCols) {
+        const int half = warp < 6 ? 0 : kCols;
+        for (int c = half; c < t.nt; c += 2 * kCols) {
 #pragma unroll
           for (int h = 0; h < kCols / 32; ++h) {
             uint32_t v[32];
