@@ -19,7 +19,10 @@
 //
 // Warps of each CTA: 0 issues A's tensor copies, 6 those of B (one thread
 // issues a copy every ~0.1-0.2 us whatever its size, so a stage is one 16 KB
-// copy of each), 1 (of the leader) the MMAs, 2-5 drain the accumulators.  Two 256-column accumulators let the drain of
+// copy of each), 1 (of the leader) the MMAs, 2-5 (and 7-10 in some modes)
+// drain the accumulators, and 11 works out which tile comes next, up to four
+// tiles ahead of the others (each role doing that for itself held up tiles that
+// are only a few blocks long).  Two 256-column accumulators let the drain of
 // one tile overlap the products of the next.  The CTAs are persistent: the
 // tiles of all groups form one sequence, dealt round-robin to the pairs.
 #include <mutex>
@@ -39,13 +42,19 @@ constexpr int kTileM = 256, kTileN = 256, kTileZ = 64;   // per pair; contractio
 constexpr int kABytes = 128 * kTileZ * 2;                // per CTA and stage
 constexpr int kBBytes = 128 * kTileZ * 2;
 constexpr int kMaxE = 2048;
+// A warp's transposition of 16 columns (slots): 32 FP32 rows of one column in
+// 128 bytes, padded so that the reads' 16-byte pieces meet different banks.
+constexpr int kRowsPitch = 144, kRowsBytes = 16 * kRowsPitch;
 
 template <Mode kMode> struct Cfg {
   static constexpr int kStages = kMode == kWgrad ? 5 : 6;
   // the epilogue's transposition; the few-slots path's sums
-  static constexpr int kStoreBytes = kMode == kWgrad ? 8 * 4096 : kMode == kDgrad ? 0 : 16384;
-  // epilogue warps: 2-5, and 7-10 (each lane quarter's second warp takes every other 128 bytes of columns)
-  static constexpr int kEpiWarps = kMode == kWgrad ? 8 : 4;
+  static constexpr int kStoreBytes = kMode == kWgrad ? 8 * 4096 : 8 * kRowsBytes;
+  // Epilogue warps 2-5, and 7-10 where the drain has more to do than store: a
+  // lane quarter's two warps take turns over the columns.  (In the plain
+  // products eight warps beside the issuing ones cost 2.7% where the tensor
+  // cores bound.)
+  static constexpr int kEpiWarps = kMode == kWgrad || kMode == kSwiglu ? 8 : 4;
 };
 constexpr int kMaxStages = 6;
 constexpr int kSumBuffers = 4;
@@ -67,7 +76,10 @@ struct Ctl {
   int warp_most[kThreads / 32];
   int most;                     // slots of the largest group
   uint32_t first[kMaxE + 1];    // tiles before each group
-  int2 group[kFewGroups];       // few slots: (8 expert + slots - 1, first slot) of the groups that have any
+  union {
+    int2 group[kFewGroups];       // few slots: (8 expert + slots - 1, first slot) of the groups that have any
+    float weight[8][kTileN / 2];   // SwiGLU: route weights of the columns that a warp takes
+  };
 };
 
 template <Mode kMode>
@@ -356,7 +368,7 @@ constexpr int kFewStages = 8;
 constexpr int kFewStageBytes = 24 * 128;   // 16 weight rows, up to 8 slots: 64 elements each
 static_assert(kFewWarps * kFewStages * kFewStageBytes <= 6 * (kABytes + kBBytes), "the rings fit the operand stages");
 constexpr int kFewSums = kFewWarps * kFewSlots * 16;   // the warps' sums of a unit
-static_assert(kSumBuffers * kFewSums * 4 <= 16384, "the warps' sums");
+static_assert(kSumBuffers * kFewSums * 4 <= 8 * kRowsBytes, "the warps' sums");
 
 // A unit of 16 weight rows: eight gates and their ups, or 16 rows in order.
 template <Mode kMode>
@@ -515,6 +527,24 @@ __device__ __forceinline__ void few_slots_finish(const Params& p, Ctl* ctl, cons
       }
     }
   }
+}
+
+// The route weights of the columns that a warp drains: 16 of every 32.
+__device__ __forceinline__ void slot_weights(const Params& p, const Tile& t, int turn, float* out) {
+  const int lane = threadIdx.x % 32;
+  int64_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int k = 32 * i + lane, col = k / 16 * 32 + 16 * turn + k % 16;
+    r[i] = col < t.nt ? static_cast<int64_t>(t.s0) + t.n0 + col : -1;
+    if (r[i] >= 0 && p.route_ids) {
+      r[i] = p.route_ids[r[i]];
+      if (r[i] >= p.R) r[i] = -1;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) out[32 * i + lane] = r[i] >= 0 ? p.route_weights[r[i]] : 0.f;
+  __syncwarp();
 }
 
 template <Mode kMode, typename T, typename Out>
@@ -711,12 +741,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;   // the lanes of tensor memory that this warp may read
     const uint32_t lanes = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
-    const bool odd = lane & 1;
+    const int epi = warp < 6 ? warp - 2 : warp - 3, turn = warp < 6 ? 0 : 1;
     uint32_t done = 0, next = 0;
     bool ok = true;
     Tile t;
     while (ok && take_tile<true>(ctl, next, t)) {
       const uint32_t tb = done & 1u;
+      // (fetched while the products still run)
+      if (kMode == kSwiglu && p.route_weights) slot_weights(p, t, turn, ctl->weight[epi]);
       if (t.nkb > 0) {
         ok = warp_wait(smem_u32(&ctl->tfull[tb]), (done >> 1) & 1u, abort_flag);
         if (!ok) break;
@@ -724,6 +756,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const uint32_t acc = lanes + tb * kTileN;
       if (kMode == kForward || kMode == kDgrad) {
+        // 32 columns (slots) at a time, neighbouring lanes' rows paired into
+        // 4-byte stores (a transposition through shared memory, with 16-byte
+        // stores, took 1.7% from products that the tensor cores bound)
+        const bool odd = lane & 1;
         const int row = t.m0 + 128 * static_cast<int>(rank) + 32 * q + (lane & ~1);
         uint16_t* out = p.y + (static_cast<int64_t>(t.s0) + t.n0) * p.ldy + row;
         for (int c = 0; c < t.nt; c += 32) {
@@ -738,53 +774,44 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } else if (kMode == kSwiglu) {
-        const int I = p.m / 2;
-        const bool up = lane & 8;
-        // even row of the lane's pair
-        const int i = t.m0 / 2 + 64 * static_cast<int>(rank) + 16 * q + (lane & 16) / 2 + (lane & 6);
+        // 16 columns (slots) at a time through the warp's shared memory, then
+        // 16-byte stores by two lanes a slot: eight gates and their ups each
+        uint8_t* rows = sC + epi * kRowsBytes;
+        const int I = p.m / 2, i = t.m0 / 2 + 64 * static_cast<int>(rank) + 16 * q + 8 * (lane & 1);
         const int64_t s0 = static_cast<int64_t>(t.s0) + t.n0;
-        for (int c = 0; c < t.nt; c += 32) {
-          float wt = 1.f;   // of this lane's slot
-          if (p.route_weights && c + lane < t.nt) {
-            int64_t r = s0 + c + lane;
-            if (p.route_ids) r = p.route_ids[r];
-            wt = p.route_ids && (r < 0 || r >= p.R) ? 0.f : p.route_weights[r];
-          }
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(acc + c, v);
+        for (int c = 16 * turn; c < t.nt; c += 32) {
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(acc + c, v);
           tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            float h[2];
+          for (int j = 0; j < 16; ++j) *reinterpret_cast<uint32_t*>(rows + j * kRowsPitch + 4 * lane) = v[j];
+          __syncwarp();
+          const int col = c + lane / 2;
+          if (col < t.nt && i < I) {
+            const float4* in = reinterpret_cast<const float4*>(rows + lane / 2 * kRowsPitch + 64 * (lane & 1));
+            const float4 ga = in[0], gb = in[1], ua = in[2], ub = in[3];
+            const float g[8] = {ga.x, ga.y, ga.z, ga.w, gb.x, gb.y, gb.z, gb.w};
+            const float u[8] = {ua.x, ua.y, ua.z, ua.w, ub.x, ub.y, ub.z, ub.w};
+            const float wt = p.route_weights ? ctl->weight[epi][c / 32 * 16 + lane / 2] : 1.f;
+            float h[8];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              // gate lanes finish the even slot, up lanes the odd one
-              const float v0 = __uint_as_float(v[j + 2 * k]), v1 = __uint_as_float(v[j + 2 * k + 1]);
-              const float got = __shfl_xor_sync(0xffffffffu, up ? v0 : v1, 8);
-              const float g = up ? got : v0, u = up ? v1 : got;
-              const float ws = __shfl_sync(0xffffffffu, wt, j + 2 * k + (up ? 1 : 0));
-              h[k] = g * sigmoid_f32(g) * u * ws;
-              if (p.pre) {
-                const uint32_t w = pair_rows<T>(v0, v1, odd);
-                const int col = c + j + 2 * k + (odd ? 1 : 0);
-                if (col < t.nt && i < I)
-                  *reinterpret_cast<uint32_t*>(p.pre + (s0 + col) * p.ldpre + (up ? I : 0) + i) = w;
-              }
+            for (int j = 0; j < 8; ++j) h[j] = g[j] * sigmoid_f32(g[j]) * u[j] * wt;
+            *reinterpret_cast<uint4*>(p.y + (s0 + col) * p.ldy + i) = pack8<T>(h);
+            if (p.pre) {
+              uint16_t* pre = p.pre + (s0 + col) * p.ldpre + i;
+              *reinterpret_cast<uint4*>(pre) = pack8<T>(g);
+              *reinterpret_cast<uint4*>(pre + I) = pack8<T>(u);
             }
-            // h[0], h[1]: slots j, j + 2 (gate lanes) or j + 1, j + 3 (up lanes)
-            const uint32_t w = pair_rows<T>(h[0], h[1], odd);
-            const int col = c + j + (odd ? 2 : 0) + (up ? 1 : 0);
-            if (col < t.nt && i < I) *reinterpret_cast<uint32_t*>(p.y + (s0 + col) * p.ldy + i) = w;
           }
+          __syncwarp();
         }
       } else {
         // rows of dw, transposed through the warp's 4 KB of shared memory
         // (128-byte swizzle) into stores of whole 128-byte lines
         constexpr int kCols = 128 / sizeof(Out);   // columns of a line
         const int row0 = t.m0 + 128 * static_cast<int>(rank) + 32 * q;
-        uint8_t* box = sC + (warp < 6 ? warp - 2 : warp - 3) * 4096;
-        const int half = warp < 6 ? 0 : kCols;
-        for (int c = half; c < t.nt; c += 2 * kCols) {
+        uint8_t* box = sC + epi * 4096;
+        for (int c = kCols * turn; c < t.nt; c += 2 * kCols) {
 #pragma unroll
           for (int h = 0; h < kCols / 32; ++h) {
             uint32_t v[32];
