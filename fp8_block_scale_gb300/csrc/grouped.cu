@@ -60,6 +60,7 @@ constexpr int kMaxStages = 6;
 constexpr int kSumBuffers = 4;
 constexpr int kQueue = 4;
 constexpr int kFewGroups = 640;
+constexpr int kFewWarps = 8, kFinishWarps = kThreads / 32 - kFewWarps;
 
 
 struct Ctl {
@@ -77,7 +78,7 @@ struct Ctl {
   int most;                     // slots of the largest group
   uint32_t first[kMaxE + 1];    // tiles before each group
   union {
-    int2 group[kFewGroups];       // few slots: (8 expert + slots - 1, first slot) of the groups that have any
+    int2 group[kFewGroups];       // few slots: (16 expert + slots - 1, first slot) of the groups that have any
     float weight[8][kTileN / 2];   // SwiGLU: route weights of the columns that a warp takes
   };
 };
@@ -182,7 +183,7 @@ __device__ __forceinline__ void count_tiles(const Params& p, Ctl* ctl) {
       // (each group has mt tiles where this table is used)
       int s0, n;
       group_at(p, e, s0, n);
-      if (n > 0 && at / mt < kFewGroups) ctl->group[at / mt] = make_int2(8 * e + min(n, 8) - 1, s0);
+      if (n > 0 && at / mt < kFewGroups) ctl->group[at / mt] = make_int2(16 * e + min(n, 16) - 1, s0);
     }
   }
   if (threadIdx.x == kThreads - 1) {
@@ -323,19 +324,20 @@ __device__ __forceinline__ uint32_t pair_rows(float v0, float v1, bool odd) {
 //
 // A decoding step's groups hold a slot or two, and its few tiles of 256 weight
 // rows would keep few pairs busy.  The weights' bytes bound it: where no group
-// has more than 8 slots (and no more than 640 groups have any) the
-// contraction is split over the eight warps of every CTA: a unit is 16 weight
-// rows, a warp takes every eighth of its blocks of 64 contraction elements
-// through a ring of its own in shared memory (asynchronous 16-byte copies, 112
-// KB of weights in flight per SM, prefetched across units).  A ninth warp adds
-// the warps' sums, handed over through shared memory, so that no warp waits
-// for another one's copies.  (Loads into registers instead stalled at 17
-// GB/s per SM: beside this kernel's shared memory the L1 has room for few
-// outstanding lines.)  The products are m16n8k16 MMAs with up to 8 slots as
-// columns; as the order of the contraction is free, a lane's 16 contiguous
-// bytes of a weight row serve as its A fragments of two MMAs, and the same 16
-// bytes of a slot's row as the B fragments.
-constexpr int kFewSlots = 8;
+// has more than 16 slots (and no more than 640 groups have any), a unit is 16
+// weight rows, whose contraction is split over 8, 4, 2 or 1 of a CTA's eight
+// streaming warps (as many units run side by side as that leaves warps for).  A
+// warp takes its blocks of 64 contraction elements through a ring of its own in
+// shared memory (asynchronous 16-byte copies, 80-112 KB of weights in flight
+// per SM, prefetched across units).  The other four warps add the sums, handed
+// over through shared memory, so that no warp waits for another one's copies.
+// (Loads into registers instead stalled at 17 GB/s per SM: beside this kernel's
+// shared memory the L1 has room for few outstanding lines.)  The products are
+// m16n8k16 MMAs with 8 or 16 slots as columns; as the order of the contraction
+// is free, a lane's 16 contiguous bytes of a weight row serve as its A
+// fragments of two MMAs, and the same 16 bytes of a slot's row as the B
+// fragments.
+constexpr int kFewSlots = 16;
 
 template <typename T>
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -363,32 +365,48 @@ __device__ __forceinline__ uint4 load_shared16(uint32_t a) {
   return v;
 }
 
-constexpr int kFewWarps = 8;
-constexpr int kFewStages = 8;
-constexpr int kFewStageBytes = 24 * 128;   // 16 weight rows, up to 8 slots: 64 elements each
-static_assert(kFewWarps * kFewStages * kFewStageBytes <= 6 * (kABytes + kBBytes), "the rings fit the operand stages");
-constexpr int kFewSums = kFewWarps * kFewSlots * 16;   // the warps' sums of a unit
-static_assert(kSumBuffers * kFewSums * 4 <= 8 * kRowsBytes, "the warps' sums");
+// kSlots: slots that a group has at most, 8 or 16.
+template <int kSlots>
+struct Few {
+  static constexpr int kStages = kSlots == 8 ? 8 : 6;
+  static constexpr int kStageBytes = (16 + kSlots) * 128;   // 16 weight rows and the slots: 64 elements each
+  static constexpr int kSums = kFewWarps * kSlots * 16;     // the warps' sums
+  static constexpr int kBuffers = kSlots == 8 ? kSumBuffers : kSumBuffers / 2;
+  static_assert(kFewWarps * kStages * kStageBytes <= 6 * (kABytes + kBBytes), "the rings fit the operand stages");
+  static_assert(kBuffers * kSums * 4 <= 8 * kRowsBytes, "the warps' sums");
+};
 
-// A unit of 16 weight rows: eight gates and their ups, or 16 rows in order.
+// How the units are dealt: a unit of 16 weight rows is eight gates and their
+// ups, or 16 rows in order; `side` units run side by side in a CTA, each on
+// `split` warps.  The split is as wide as leaves a warp four blocks, or wider
+// where the CTAs would not all have work.
 template <Mode kMode>
 struct FewUnits {
-  int units;            // per group
-  uint32_t total;
-  __device__ __forceinline__ FewUnits(const Params& p, const Ctl* ctl)
-      : units((p.m + 15) / 16), total(ctl->first[p.E] / ((p.m + kTileM - 1) / kTileM) * units) {}
+  int split, side, steps;   // steps: of `side` units, per group
+  uint32_t total;           // steps of all groups
+  __device__ __forceinline__ FewUnits(const Params& p, const Ctl* ctl) {
+    const uint32_t groups = ctl->first[p.E] / ((p.m + kTileM - 1) / kTileM);
+    const int units = (p.m + 15) / 16, nkb = (p.z + kTileZ - 1) / kTileZ;
+    split = kFewWarps;
+    while (split > 1 && nkb < 4 * split && groups * ((units * split + 15) / 16) >= gridDim.x) split /= 2;
+    side = kFewWarps / split;
+    steps = (units + side - 1) / side;
+    total = groups * steps;
+  }
 };
 
 // One of the eight streaming warps.
-template <Mode kMode, typename T>
+template <Mode kMode, typename T, int kSlots>
 __device__ __forceinline__ void few_slots_stream(const Params& p, Ctl* ctl, uint8_t* ring, float* sums) {
+  using F = Few<kSlots>;
   constexpr bool kGlu = kMode == kSwiglu;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   volatile int* abort_flag = &ctl->abort_flag;
   const FewUnits<kMode> f(p, ctl);
   const int nkb = (p.z + kTileZ - 1) / kTileZ;
-  const int nst = warp < nkb ? (nkb - warp + kFewWarps - 1) / kFewWarps : 0;   // this warp's blocks of a unit
-  const uint32_t base = smem_u32(ring) + warp * kFewStages * kFewStageBytes;
+  const int part = warp % f.split, side = warp / f.split;
+  const int nst = part < nkb ? (nkb - part + f.split - 1) / f.split : 0;   // this warp's blocks of a unit
+  const uint32_t base = smem_u32(ring) + warp * F::kStages * F::kStageBytes;
 
   // The copies run ahead: unit cu, block cb of it, into stage cs.
   uint32_t cu = blockIdx.x, cs = 0;
@@ -400,22 +418,22 @@ __device__ __forceinline__ void few_slots_stream(const Params& p, Ctl* ctl, uint
   int cslots = 0;
   auto open = [&]() {
     if (cu >= f.total || nst == 0) return;
-    const int2 t = ctl->group[cu / f.units];
-    const int unit = static_cast<int>(cu % f.units);
-    const uint16_t* we = p.w + static_cast<int64_t>(t.x / 8) * p.m * p.z;
+    const int2 t = ctl->group[cu / f.steps];
+    const int unit = static_cast<int>(cu % f.steps) * f.side + side;
+    const uint16_t* we = p.w + static_cast<int64_t>(t.x / kFewSlots) * p.m * p.z;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int j = 4 * i + sub;
-      const int r = kGlu ? 8 * unit + j % 8 + (j / 8) * (p.m / 2) : 16 * unit + j;
-      cw[i] = r < p.m ? we + static_cast<int64_t>(r) * p.z + 8 * chunk : nullptr;
+      const int r = kGlu ? 8 * unit + j % 8 : 16 * unit + j, top = kGlu ? p.m / 2 : p.m;
+      cw[i] = r < top ? we + (static_cast<int64_t>(r) + (kGlu ? j / 8 * top : 0)) * p.z + 8 * chunk : nullptr;
     }
     cx = p.x + (static_cast<int64_t>(t.y) + sub) * p.ldx + 8 * chunk;
-    cslots = t.x % 8 + 1;
+    cslots = t.x % kFewSlots + 1;
   };
   auto copy = [&]() {
     if (cu < f.total && nst > 0) {
-      const int z = (warp + cb * kFewWarps) * kTileZ;
-      const uint32_t st = base + cs * kFewStageBytes;
+      const int z = (part + cb * f.split) * kTileZ;
+      const uint32_t st = base + cs * F::kStageBytes;
       const bool in = z + 8 * chunk < p.z;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -424,7 +442,7 @@ __device__ __forceinline__ void few_slots_stream(const Params& p, Ctl* ctl, uint
         copy16_async(dst, in && cw[i] ? cw[i] + z : p.w, in && cw[i] ? 16u : 0u);
       }
 #pragma unroll
-      for (int i = 0; i < kFewSlots / 4; ++i) {
+      for (int i = 0; i < kSlots / 4; ++i) {
         const int j = 4 * i + sub;
         if (j < cslots)
           copy16_async(st + 2048 + 128 * j + 16 * (chunk ^ (j & 7)), in ? cx + 4 * i * p.ldx + z : p.x, in ? 16u : 0u);
@@ -435,99 +453,136 @@ __device__ __forceinline__ void few_slots_stream(const Params& p, Ctl* ctl, uint
         open();
       }
     }
-    cs = cs + 1 == kFewStages ? 0 : cs + 1;
+    cs = cs + 1 == F::kStages ? 0 : cs + 1;
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   open();
-  for (int i = 0; i < kFewStages - 1; ++i) copy();
+  for (int i = 0; i < F::kStages - 1; ++i) copy();
 
   uint32_t s = 0, n = 0;
   for (uint32_t u = blockIdx.x; u < f.total; u += gridDim.x, ++n) {
-    float d[4] = {};
+    float d[kSlots / 8][4] = {};
     for (int b = 0; b < nst; ++b) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kFewStages - 2) : "memory");
+      asm volatile("cp.async.wait_group %0;" ::"n"(F::kStages - 2) : "memory");
       __syncwarp();
       copy();   // into the stage read in the step before
-      const uint32_t st = base + s * kFewStageBytes;
+      const uint32_t st = base + s * F::kStageBytes;
       const int g = lane / 4;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         // (columns 2 (lane % 4) + h: no two lanes of a quarter-warp share a bank)
         const uint32_t at = 128 * g + 16 * ((2 * (lane % 4) + h) ^ g);
         const uint4 a0 = load_shared16(st + at), a1 = load_shared16(st + 1024 + at);
-        const uint4 x0 = load_shared16(st + 2048 + at);
-        mma_16816<T>(d, a0.x, a1.x, a0.y, a1.y, x0.x, x0.y);
-        mma_16816<T>(d, a0.z, a1.z, a0.w, a1.w, x0.z, x0.w);
+#pragma unroll
+        for (int c = 0; c < kSlots / 8; ++c) {
+          const uint4 x = load_shared16(st + 2048 + 1024 * c + at);
+          mma_16816<T>(d[c], a0.x, a1.x, a0.y, a1.y, x.x, x.y);
+          mma_16816<T>(d[c], a0.z, a1.z, a0.w, a1.w, x.z, x.w);
+        }
       }
-      s = s + 1 == kFewStages ? 0 : s + 1;
+      s = s + 1 == F::kStages ? 0 : s + 1;
       __syncwarp();
     }
     // sums[warp][slot][row]: weight rows lane / 4 and 8 on, slots 2 (lane % 4) and the next
-    const uint32_t buf = n % kSumBuffers;
-    if (!warp_wait(smem_u32(&ctl->sempty[buf]), ((n / kSumBuffers) & 1u) ^ 1u, abort_flag)) break;
-    float* out = sums + buf * kFewSums + warp * kFewSlots * 16;
+    const uint32_t buf = n % F::kBuffers;
+    if (!warp_wait(smem_u32(&ctl->sempty[buf]), ((n / F::kBuffers) & 1u) ^ 1u, abort_flag)) break;
+    float* out = sums + buf * F::kSums + warp * kSlots * 16;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) out[(2 * (lane % 4) + (i & 1)) * 16 + lane / 4 + 8 * (i / 2)] = d[i];
+    for (int c = 0; c < kSlots / 8; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        out[(8 * c + 2 * (lane % 4) + (i & 1)) * 16 + lane / 4 + 8 * (i / 2)] = d[c][i];
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&ctl->sfull[buf]));
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// The ninth warp: adds the warps' sums in order and writes the results.
-template <Mode kMode, typename T>
+// The finishing warps add the streaming warps' sums in order and write the
+// results, each for every fourth of the units side by side.
+template <Mode kMode, typename T, int kSlots>
 __device__ __forceinline__ void few_slots_finish(const Params& p, Ctl* ctl, const float* sums) {
+  using F = Few<kSlots>;
   constexpr bool kGlu = kMode == kSwiglu;
-  const int lane = threadIdx.x % 32;
+  constexpr int kMine = kSlots / 2;   // this lane's slots: lane / 16 + 0, 2, 4, ...
+  const int lane = threadIdx.x % 32, row = lane % 16, turn = threadIdx.x / 32 - kFewWarps;
   volatile int* abort_flag = &ctl->abort_flag;
   const FewUnits<kMode> f(p, ctl);
+  // route weights: ids two steps ahead, weights one (their loads follow one another)
+  const bool weighted = kGlu && p.route_weights;
+  int64_t id[kMine];
+  float wt[kMine], next_wt[kMine];
+  auto fetch_ids = [&](uint32_t u) {
+#pragma unroll
+    for (int c = 0; c < kMine; ++c) {
+      id[c] = -1;
+      if (!weighted || u >= f.total) continue;
+      const int2 group = ctl->group[u / f.steps];
+      const int slot = 2 * c + lane / 16;
+      if (slot > group.x % kFewSlots) continue;
+      id[c] = static_cast<int64_t>(group.y) + slot;
+      if (p.route_ids) id[c] = p.route_ids[id[c]];
+    }
+  };
+  auto fetch_weights = [&](float (&w)[kMine]) {
+#pragma unroll
+    for (int c = 0; c < kMine; ++c) {
+      w[c] = weighted ? 0.f : 1.f;
+      if (id[c] >= 0 && (!p.route_ids || id[c] < p.R)) w[c] = p.route_weights[id[c]];
+    }
+  };
+  fetch_ids(blockIdx.x);
+  fetch_weights(wt);
+  fetch_ids(blockIdx.x + gridDim.x);
   uint32_t n = 0;
   for (uint32_t u = blockIdx.x; u < f.total; u += gridDim.x, ++n) {
-    const int2 group = ctl->group[u / f.units];
-    const int s0 = group.y, slots = group.x % 8 + 1;
-    const int unit = static_cast<int>(u % f.units);
-    const int row = lane % 16;
-    // this lane's slots: lane / 16 + 0, 2, 4, 6
-    float wt[kFewSlots / 2];
+    const int2 group = ctl->group[u / f.steps];
+    const int s0 = group.y, slots = group.x % kFewSlots + 1;
+    fetch_weights(next_wt);
+    fetch_ids(u + 2 * gridDim.x);
+    const uint32_t buf = n % F::kBuffers;
+    if (!warp_wait(smem_u32(&ctl->sfull[buf]), (n / F::kBuffers) & 1u, abort_flag)) break;
+    for (int side = turn; side < f.side; side += kFinishWarps) {
+      const int unit = static_cast<int>(u % f.steps) * f.side + side;
+      const float* in = sums + buf * F::kSums + side * f.split * kSlots * 16;
+      float sum[kMine] = {};
+      for (int w = 0; w < f.split; ++w)
 #pragma unroll
-    for (int c = 0; c < kFewSlots / 2; ++c) {
-      const int slot = 2 * c + lane / 16;
-      wt[c] = 1.f;
-      if (kGlu && p.route_weights && slot < slots) {
-        int64_t r = static_cast<int64_t>(s0) + slot;
-        if (p.route_ids) r = p.route_ids[r];
-        wt[c] = p.route_ids && (r < 0 || r >= p.R) ? 0.f : p.route_weights[r];
+        for (int c = 0; c < kMine; ++c) sum[c] += in[(w * kSlots + 2 * c + lane / 16) * 16 + row];
+#pragma unroll
+      for (int c = 0; c < kMine; ++c) {
+        const int slot = 2 * c + lane / 16;
+        const int64_t sl = static_cast<int64_t>(s0) + slot;
+        const bool live = slot < slots;
+        if (kGlu) {
+          const float up = __shfl_down_sync(0xffffffffu, sum[c], 8);   // row + 8 of the same slot
+          const int I = p.m / 2, i = 8 * unit + row % 8;
+          if (live && i < I && p.pre)
+            p.pre[sl * p.ldpre + (row < 8 ? i : I + i)] = static_cast<uint16_t>(Pack2<T>::store(sum[c], 0.f));
+          if (live && i < I && row < 8)
+            p.y[sl * p.ldy + i] =
+                static_cast<uint16_t>(Pack2<T>::store(sum[c] * sigmoid_f32(sum[c]) * up * wt[c], 0.f));
+        } else if (live && 16 * unit + row < p.m) {
+          p.y[sl * p.ldy + 16 * unit + row] = static_cast<uint16_t>(Pack2<T>::store(sum[c], 0.f));
+        }
       }
     }
-    const uint32_t buf = n % kSumBuffers;
-    if (!warp_wait(smem_u32(&ctl->sfull[buf]), (n / kSumBuffers) & 1u, abort_flag)) break;
-    const float* in = sums + buf * kFewSums;
-    float sum[kFewSlots / 2] = {};
-#pragma unroll
-    for (int w = 0; w < kFewWarps; ++w)
-#pragma unroll
-      for (int c = 0; c < kFewSlots / 2; ++c) sum[c] += in[(w * kFewSlots + 2 * c + lane / 16) * 16 + row];
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&ctl->sempty[buf]));
 #pragma unroll
-    for (int c = 0; c < kFewSlots / 2; ++c) {
-      const int slot = 2 * c + lane / 16;
-      const int64_t sl = static_cast<int64_t>(s0) + slot;
-      const bool live = slot < slots;
-      if (kGlu) {
-        const float up = __shfl_down_sync(0xffffffffu, sum[c], 8);   // row + 8 of the same slot
-        const int I = p.m / 2, i = 8 * unit + row % 8;
-        if (live && p.pre)
-          p.pre[sl * p.ldpre + (row < 8 ? i : I + i)] = static_cast<uint16_t>(Pack2<T>::store(sum[c], 0.f));
-        if (live && row < 8)
-          p.y[sl * p.ldy + i] =
-              static_cast<uint16_t>(Pack2<T>::store(sum[c] * sigmoid_f32(sum[c]) * up * wt[c], 0.f));
-      } else if (live && 16 * unit + row < p.m) {
-        p.y[sl * p.ldy + 16 * unit + row] = static_cast<uint16_t>(Pack2<T>::store(sum[c], 0.f));
-      }
-    }
+    for (int c = 0; c < kMine; ++c) wt[c] = next_wt[c];
   }
 }
+
+template <Mode kMode, typename T, int kSlots>
+__device__ __forceinline__ void few_slots(const Params& p, Ctl* ctl, uint8_t* ring, float* sums) {
+  if (threadIdx.x / 32 < kFewWarps)
+    few_slots_stream<kMode, T, kSlots>(p, ctl, ring, sums);
+  else
+    few_slots_finish<kMode, T, kSlots>(p, ctl, sums);
+}
+
+// ---------------------------------------------------------------- tiles
 
 // The route weights of the columns that a warp drains: 16 of every 32.
 __device__ __forceinline__ void slot_weights(const Params& p, const Tile& t, int turn, float* out) {
@@ -572,8 +627,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctl->tempty[b]), 2 * Cfg<kMode>::kEpiWarps);
     }
     for (int b = 0; b < kSumBuffers; ++b) {
-      mbar_init(smem_u32(&ctl->sfull[b]), 8);
-      mbar_init(smem_u32(&ctl->sempty[b]), 1);
+      mbar_init(smem_u32(&ctl->sfull[b]), kFewWarps);
+      mbar_init(smem_u32(&ctl->sempty[b]), kFinishWarps);
     }
     for (int q = 0; q < kQueue; ++q) {
       mbar_init(smem_u32(&ctl->qfull[q]), 1);
@@ -592,11 +647,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t total = ctl->first[p.E];
   const uint32_t tile0 = blockIdx.x / 2, step = gridDim.x / 2;
   constexpr bool kFew = kMode == kForward || kMode == kSwiglu;
-  if (kFew && ctl->most <= kFewSlots && total <= kFewGroups * static_cast<uint32_t>((p.m + kTileM - 1) / kTileM)) {
-    if (warp < kFewWarps)
-      few_slots_stream<kMode, T>(p, ctl, sA, reinterpret_cast<float*>(sC));
-    else if (warp == kFewWarps)
-      few_slots_finish<kMode, T>(p, ctl, reinterpret_cast<const float*>(sC));
+  // With more than 8 slots in a group the tiles are faster once every pair has
+  // one (64 groups of up to 14 slots, K 4096, N 2048: 175 us against 211; 14 of
+  // up to 9, K 5936, N 320: 35 against 16).
+  if (kFew && ctl->most <= (total < step ? kFewSlots : 8) &&
+      total <= kFewGroups * static_cast<uint32_t>((p.m + kTileM - 1) / kTileM)) {
+    if (ctl->most <= 8)
+      few_slots<kMode, T, 8>(p, ctl, sA, reinterpret_cast<float*>(sC));
+    else
+      few_slots<kMode, T, 16>(p, ctl, sA, reinterpret_cast<float*>(sC));
     __syncthreads();
     if (threadIdx.x == 0 && ctl->abort_flag && p.status) atomicOr(p.status, MOE_DEV_TIMEOUT);
     return;
