@@ -282,7 +282,17 @@ __device__ __forceinline__ void publish_tiles(const Params& p, Ctl* ctl, uint32_
     const bool end = tiles.done();
     Tile t = {};
     t.nkb = -1;
-    if (!end) t = tiles.get();
+    if (!end) {
+      t = tiles.get();
+      // every box, row and store of the tile follows from these
+      if (!MOE_IN_BOUNDS(t.e >= 0 && t.e < p.E && t.m0 >= 0 && t.m0 < p.m && t.slots >= 0 && t.n0 >= 0 && t.nt > 0 &&
+                         (t.slots == 0 || (t.s0 >= 0 && t.s0 <= p.rows - t.slots)) &&
+                         t.n0 + t.nt <= (kMode == kWgrad ? p.n : t.slots))) {
+        t = {};
+        t.nt = 32;   // computes and stores nothing (wgrad: keeps clear of dw)
+        t.m0 = p.m;
+      }
+    }
     const uint32_t q = i % kQueue;
     if (!warp_wait(smem_u32(&ctl->qempty[q]), ((i / kQueue) & 1u) ^ 1u, abort_flag)) return;
     if (threadIdx.x % 32 == 0) {
@@ -418,7 +428,8 @@ __device__ __forceinline__ void few_slots_stream(const Params& p, Ctl* ctl, uint
   int cslots = 0;
   auto open = [&]() {
     if (cu >= f.total || nst == 0) return;
-    const int2 t = ctl->group[cu / f.steps];
+    int2 t = ctl->group[cu / f.steps];
+    if (!MOE_IN_BOUNDS(t.x >= 0 && t.x / kFewSlots < p.E && t.y >= 0 && t.y <= p.rows - 1 - t.x % kFewSlots)) t = {0, 0};
     const int unit = static_cast<int>(cu % f.steps) * f.side + side;
     const uint16_t* we = p.w + static_cast<int64_t>(t.x / kFewSlots) * p.m * p.z;
 #pragma unroll
