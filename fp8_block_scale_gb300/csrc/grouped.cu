@@ -47,7 +47,7 @@ constexpr int kMaxE = 2048;
 constexpr int kRowsPitch = 144, kRowsBytes = 16 * kRowsPitch;
 
 template <Mode kMode> struct Cfg {
-  static constexpr int kStages = kMode == kWgrad ? 5 : 6;
+  static constexpr int kStages = kMode == kWgrad ? 5 : 6;   // of full size
   // the epilogue's transposition; the few-slots path's sums
   static constexpr int kStoreBytes = kMode == kWgrad ? 8 * 4096 : 8 * kRowsBytes;
   // Epilogue warps 2-5, and 7-10 where the drain has more to do than store: a
@@ -56,7 +56,7 @@ template <Mode kMode> struct Cfg {
   // cores bound.)
   static constexpr int kEpiWarps = kMode == kWgrad || kMode == kSwiglu ? 8 : 4;
 };
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 9;
 constexpr int kSumBuffers = 4;
 constexpr int kQueue = 4;
 constexpr int kFewGroups = 640;
@@ -272,6 +272,18 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
   int dummy = 0;
   mbar_wait(bar, parity, &dummy);
 }
+
+// A place in the ring of stages.
+struct Ring {
+  int s = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1u;
+    }
+  }
+};
 
 // The queue's two sides.  A tile with nkb < 0 ends it.
 template <Mode kMode>
@@ -616,20 +628,18 @@ __device__ __forceinline__ void slot_weights(const Params& p, const Tile& t, int
 template <Mode kMode, typename T, typename Out>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_kernel(const __grid_constant__ Maps maps, const Params p) {
-  constexpr int kStages = Cfg<kMode>::kStages;
   constexpr bool kAmn = kMode == kDgrad || kMode == kWgrad;   // A stored along M
   constexpr bool kBmn = kMode == kWgrad;                      // B stored along N
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sA = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sB = sA + kStages * kABytes;
-  uint8_t* sC = sB + kStages * kBBytes;
+  uint8_t* sC = sA + Cfg<kMode>::kStages * (kABytes + kBBytes);
   Ctl* ctl = reinterpret_cast<Ctl*>(sC + Cfg<kMode>::kStoreBytes);
   volatile int* abort_flag = &ctl->abort_flag;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = pair::cluster_rank();
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(smem_u32(&ctl->full[s]), 1);
       mbar_init(smem_u32(&ctl->empty[s]), 1);
     }
@@ -658,10 +668,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t total = ctl->first[p.E];
   const uint32_t tile0 = blockIdx.x / 2, step = gridDim.x / 2;
   constexpr bool kFew = kMode == kForward || kMode == kSwiglu;
-  // With more than 8 slots in a group the tiles are faster once every pair has
-  // one (64 groups of up to 14 slots, K 4096, N 2048: 175 us against 211; 14 of
-  // up to 9, K 5936, N 320: 35 against 16).
-  if (kFew && ctl->most <= (total < step ? kFewSlots : 8) &&
+  // With more than 8 slots in a group the tiles are faster unless half of the
+  // pairs would have none (24 groups of 9 slots, K 1160, N 712, 72 tiles: 11.9
+  // us against 15.0; 14 of up to 9, K 5936, N 320, 28 tiles: 35 against 16).
+  if (kFew && ctl->most <= (2 * total <= step ? kFewSlots : 8) &&
       total <= kFewGroups * static_cast<uint32_t>((p.m + kTileM - 1) / kTileM)) {
     if (ctl->most <= 8)
       few_slots<kMode, T, 8>(p, ctl, sA, reinterpret_cast<float*>(sC));
@@ -671,6 +681,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0 && ctl->abort_flag && p.status) atomicOr(p.status, MOE_DEV_TIMEOUT);
     return;
   }
+  // Where no tile is wide, B's share of a stage is smaller and the ring longer:
+  // few columns are soon multiplied, and it is the copies' latency that bounds
+  // (24 groups of 65 slots, K 1160, N 712: a block every 0.33 us with 6 stages).
+  const int bstage = kMode == kWgrad || ctl->most > 128 ? kBBytes : ctl->most > 64 ? kBBytes / 2 : kBBytes / 4;
+  const int stages = kMode == kWgrad ? Cfg<kMode>::kStages : bstage == kBBytes ? 6 : bstage == kBBytes / 2 ? 8 : 9;
+  uint8_t* sB = sA + stages * kABytes;
   if (warp == 1) {
     pair::tmem_alloc(smem_u32(&ctl->tmem_base), 512);
     pair::tmem_relinquish();
@@ -685,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ producers (A: warp 0, B: warp 6)
     const bool isA = warp == 0;
     const uint32_t lead_full0 = pair::mapa_shared(smem_u32(&ctl->full[0]), 0);
-    uint32_t it = 0;
+    Ring ring;
     bool ok = true;
     // lane 0 issues (wgrad's row-by-row copies: all lanes)
     constexpr bool kWarp = kMode == kWgrad;
@@ -700,14 +716,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // wgrad: a last block inside the buffer's first 64 slots cannot be a window that ends with the group
       const int last = kMode == kWgrad && t.slots % kTileZ && t.s0 + t.slots < kTileZ ? t.nkb - 1 : t.nkb;
       if (lane == 0) {
-        for (int kb = 0; kb < last; ++kb, ++it) {
-          const int s = it % kStages;
-          if (!mbar_wait(smem_u32(&ctl->empty[s]), ((it / kStages) & 1u) ^ 1u, abort_flag)) {
+        for (int kb = 0; kb < last; ++kb, ring.next(stages)) {
+          const int s = ring.s;
+          if (!mbar_wait(smem_u32(&ctl->empty[s]), ring.phase ^ 1u, abort_flag)) {
             ok = false;
             break;
           }
           const uint32_t full = lead_full0 + 8u * s;
-          const uint32_t dst = smem_u32((isA ? sA : sB) + s * (isA ? kABytes : kBBytes));
+          const uint32_t dst = smem_u32((isA ? sA : sB) + s * (isA ? kABytes : bstage));
           const int z = kb * kTileZ;
           if (isA && rank == 0) mbar_arrive_expect_tx(smem_u32(&ctl->full[s]), 2u * (kABytes + bbytes));
           if (kMode == kWgrad) {
@@ -738,13 +754,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (kWarp) {
-        it = __shfl_sync(0xffffffffu, it, 0);
+        ring.s = __shfl_sync(0xffffffffu, ring.s, 0);
+        ring.phase = __shfl_sync(0xffffffffu, ring.phase, 0);
         ok = __shfl_sync(0xffffffffu, ok, 0);
       }
       if (kMode == kWgrad && last < t.nkb) {
         // row by row instead; row -1 reads as zeros
-        const int s = it % kStages, z = last * kTileZ;
-        if (!ok || !warp_wait(smem_u32(&ctl->empty[s]), ((it / kStages) & 1u) ^ 1u, abort_flag)) {
+        const int s = ring.s, z = last * kTileZ;
+        if (!ok || !warp_wait(smem_u32(&ctl->empty[s]), ring.phase ^ 1u, abort_flag)) {
           ok = false;
           break;
         }
@@ -761,18 +778,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         else if (8192u * j < bbytes)
           pair::gather4(dst + 8192u * j, &maps.bg, full, bcol + 64 * j, r[0], r[1], r[2], r[3]);
         __syncwarp();
-        ++it;
+        ring.next(stages);
       }
     }
-    // wind down: let the copies already issued land before the CTA exits
+    // wind down: let the copies already issued (at most a ring's) land before
+    // the CTA exits; a stage that has none under way has completed this phase
     if (!ok && lane == 0 && rank == 0)
-      for (uint32_t j = (it > kStages ? it - kStages : 0); j < it; ++j)
-        drain_wait(smem_u32(&ctl->full[j % kStages]), (j / kStages) & 1u);
+      for (int j = 0; j < stages; ++j) {
+        drain_wait(smem_u32(&ctl->full[ring.s]), ring.phase ^ 1u);
+        ring.next(stages);
+      }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader)
     if (rank == 0 && lane == 0) {
-      uint32_t it = 0, done = 0, next = 0;
+      uint32_t done = 0, next = 0;
+      Ring ring;
+      int last = -1;   // the last stage used, and its phase
+      uint32_t last_phase = 0;
       bool ok = true;
       Tile t;
       while (ok && take_tile<false>(ctl, next, t)) {
@@ -781,20 +804,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tb = done & 1u, d = tmem_base + tb * kTileN;
         if (!mbar_wait(smem_u32(&ctl->tempty[tb]), ((done >> 1) & 1u) ^ 1u, abort_flag)) break;
         tc_fence_after();
-        for (int kb = 0; kb < t.nkb; ++kb, ++it) {
-          const int s = it % kStages;
-          if (!mbar_wait(smem_u32(&ctl->full[s]), (it / kStages) & 1u, abort_flag)) {
+        for (int kb = 0; kb < t.nkb; ++kb, ring.next(stages)) {
+          const int s = ring.s;
+          if (!mbar_wait(smem_u32(&ctl->full[s]), ring.phase, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a = smem_u32(sA + s * kABytes), b = smem_u32(sB + s * kBBytes);
+          const uint32_t a = smem_u32(sA + s * kABytes), b = smem_u32(sB + s * bstage);
 #pragma unroll
           for (int kk = 0; kk < kTileZ / 16; ++kk)
             pair::umma_f16(d, kAmn ? pair::sw128_mnmajor_desc(a + 2048u * kk, 8192u) : sw128_kmajor_desc(a + 32u * kk),
                            kBmn ? pair::sw128_mnmajor_desc(b + 2048u * kk, 8192u) : sw128_kmajor_desc(b + 32u * kk),
                            idesc, kb > 0 || kk > 0 ? 1u : 0u);
           pair::umma_commit(smem_u32(&ctl->empty[s]));
+          last = s;
+          last_phase = ring.phase;
         }
         if (ok) {
           pair::umma_commit(smem_u32(&ctl->tfull[tb]));
@@ -802,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // no MMA may still be writing TMEM when it is released
-      if (it > 0) drain_wait(smem_u32(&ctl->empty[(it - 1) % kStages]), ((it - 1) / kStages) & 1u);
+      if (last >= 0) drain_wait(smem_u32(&ctl->empty[last]), last_phase);
     }
     __syncwarp();
   } else if (warp == 11) {
