@@ -794,6 +794,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (rank == 0 && lane == 0) {
       uint32_t done = 0, next = 0;
       Ring ring;
+      // Descriptors of the first stage's first 16 contraction elements; the others'
+      // differ in the address alone (its field is 14 bits of 16-byte units, which
+      // no address of shared memory exceeds).  One thread issues everything, so
+      // its few instructions per block are what narrow tiles cost.
+      const uint64_t da = kAmn ? pair::sw128_mnmajor_desc(smem_u32(sA), 8192u) : sw128_kmajor_desc(smem_u32(sA));
+      const uint64_t db = kBmn ? pair::sw128_mnmajor_desc(smem_u32(sB), 8192u) : sw128_kmajor_desc(smem_u32(sB));
+      const uint32_t a_lo = static_cast<uint32_t>(da), a_hi = static_cast<uint32_t>(da >> 32);
+      const uint32_t b_lo = static_cast<uint32_t>(db), b_hi = static_cast<uint32_t>(db >> 32);
       int last = -1;   // the last stage used, and its phase
       uint32_t last_phase = 0;
       bool ok = true;
@@ -811,12 +819,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t a = smem_u32(sA + s * kABytes), b = smem_u32(sB + s * bstage);
+          const uint32_t a = a_lo + s * (kABytes >> 4), b = b_lo + s * (bstage >> 4);
 #pragma unroll
           for (int kk = 0; kk < kTileZ / 16; ++kk)
-            pair::umma_f16(d, kAmn ? pair::sw128_mnmajor_desc(a + 2048u * kk, 8192u) : sw128_kmajor_desc(a + 32u * kk),
-                           kBmn ? pair::sw128_mnmajor_desc(b + 2048u * kk, 8192u) : sw128_kmajor_desc(b + 32u * kk),
-                           idesc, kb > 0 || kk > 0 ? 1u : 0u);
+            pair::umma_f16(d, a + kk * (kAmn ? 128 : 2), a_hi, b + kk * (kBmn ? 128 : 2), b_hi, idesc,
+                           kb > 0 || kk > 0 ? 1u : 0u);
           pair::umma_commit(smem_u32(&ctl->empty[s]));
           last = s;
           last_phase = ring.phase;

@@ -544,3 +544,65 @@ def test_adamw_in_a_graph_and_with_other_tensors_strides():
     torch.cuda.synchronize()
     for t, o in zip(ts, ref):
         assert all(torch.equal(t[k], o[k]) for k in o)
+
+
+@pytest.mark.parametrize("E,per", [(700, 1), (2048, 2), (650, 20), (2048, 0)])
+def test_many_groups(E, per):
+    """More groups than the few-slots path takes, and the largest table."""
+    rng = np.random.default_rng(E + per)
+    counts = list(rng.integers(0, 2 * per + 1, E)) if per > 1 else [per] * E
+    K, N = 72, 144
+    start, s, r, slots, used = groups(counts, gap=1)
+    g = gen(E)
+    w = (torch.randn(E, N, K, generator=g, device="cuda") * 0.2).to(BF16)
+    x, y = buffer(slots, K, BF16, g), torch.zeros(slots, N, dtype=BF16, device="cuda")
+    dy, dw = buffer(slots, N, BF16, g), torch.full((E, N, K), 9.0, dtype=BF16, device="cuda")
+    L.moe_grouped_gemm(L.make_grouped_args(x, w, y, s, r))
+    L.moe_grouped_wgrad(L.make_grouped_wgrad_args(dy, x, dw, s, r))
+    want, mag = T.grouped_forward(f64(x), f64(w), start, counts)
+    close(y[used], want[used], gamma(K) * mag[used], BF16)
+    assert (y[~torch.from_numpy(used)] == 0).all()
+    want, mag = T.grouped_wgrad(f64(dy), f64(x), start, counts)
+    close(dw, want, gamma(max(counts)) * mag, BF16)
+
+
+@pytest.mark.parametrize("slots,K,N", [(9, 5000, 320), (16, 1096, 64), (13, 136, 72), (1, 7168, 512), (8, 40, 3088)])
+def test_few_slots_with_long_and_short_contractions(slots, K, N):
+    """The paths for at most 8 and 16 slots, one and several units side by side."""
+    counts = [slots, 0, 1, max(1, slots - 1)]
+    start, s, r, rows, used = groups(counts, gap=2)
+    g = gen(K)
+    w = (torch.randn(4, N, K, generator=g, device="cuda") * K ** -0.5).to(FP16)
+    x = buffer(rows, K, FP16, g, pad=8)
+    x[~torch.from_numpy(used).cuda()] = float("nan")
+    y = torch.zeros(rows, N, dtype=FP16, device="cuda")
+    L.moe_grouped_gemm(L.make_grouped_args(x, w, y, s, r))
+    want, mag = T.grouped_forward(f64(x), f64(w), start, counts)
+    close(y[used], want[used], gamma(K) * mag[used], FP16)
+    if N % 16 == 0:
+        wt = torch.rand(rows, generator=g, device="cuda")
+        h, pre = torch.zeros(rows, N // 2, dtype=FP16, device="cuda"), torch.zeros(rows, N, dtype=FP16, device="cuda")
+        L.moe_grouped_gemm(L.make_grouped_args(x, w, h, s, r, epilogue=L.GROUPED_SWIGLU, pre=pre, route_weights=wt))
+        assert torch.equal(pre, y)
+        hw = T.swiglu(want[used], f64(wt)[used])
+        m = gamma(K) * mag[used]
+        I = N // 2
+        gate, up = np.abs(want[used][:, :I]), np.abs(want[used][:, I:])
+        err = 1.1 * m[:, :I] * (up + m[:, I:]) + (gate + m[:, :I]) * m[:, I:] + (10 + 1.2 * gate) * 2.0 ** -23 * np.abs(hw)
+        close(h[used], hw, err, FP16)
+
+
+def test_adamw_with_gradients_of_several_types():
+    g = gen(21)
+    for bits in (32, 8):
+        ts = []
+        for grad in (BF16, F32, FP16, BF16):
+            ts += _tensors([5000, 77], bits, grad, BF16, g)
+        one = [{k: v.clone() for k, v in t.items()} for t in ts]
+        L.moe_adamw_step(L.make_adamw_args(L.AdamWTable(ts), seed=5, **HYPER))
+        for i, t in enumerate(one):
+            # alone, at the same place of its table
+            dummy = [dict(t, **{k: v[:0].clone() for k, v in t.items()}) for _ in range(i)]
+            L.moe_adamw_step(L.make_adamw_args(L.AdamWTable(dummy + [t]), seed=5, **HYPER))
+            for k in t:
+                assert torch.equal(t[k].view(torch.uint8), ts[i][k].view(torch.uint8)), (bits, i, k)
