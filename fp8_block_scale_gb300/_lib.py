@@ -346,7 +346,7 @@ def _ptr(t):
 def _stream(stream=None):
     # (the raw handle: building a torch.cuda.Stream costs 3 us a call on the Grace host)
     if stream is None:
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
     return ctypes.c_void_p(stream.cuda_stream)
 
 

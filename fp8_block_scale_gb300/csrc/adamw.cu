@@ -139,17 +139,22 @@ __device__ __forceinline__ uint2 model4(const AdamEntry& t, const float (&p)[4])
   return make_uint2(Pack2<__half>::store(p[0], p[1]), Pack2<__half>::store(p[2], p[3]));
 }
 
-// The table entry that holds chunk c (whole warps): 32 entries are compared at
-// a time, so a list of 1024 tensors takes two dependent loads.
+// The table entry that holds chunk c (whole warps): 128 entries are compared
+// at a time, four a lane, so a list of 128 tensors takes one load's latency and
+// one of 16384 two.
 __device__ __forceinline__ int find_entry(const AdamParams& a, int64_t c) {
   int lo = 0, n = a.count;   // table[lo].first_chunk <= c; the entry is in [lo, lo + n)
   while (n > 1) {
-    const int stride = (n + 31) / 32, i = lo + static_cast<int>(threadIdx.x % 32) * stride;
-    const unsigned le = __ballot_sync(0xffffffffu, i < lo + n && a.table[min(i, a.count - 1)].first_chunk <= c);
-    const int k = 31 - __clz(le | 1u);
-    const int end = min(lo + n, lo + (k + 1) * stride);
+    const int stride = (n + 127) / 128;
+    unsigned le = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = (4 * static_cast<int>(threadIdx.x % 32) + j) * stride;
+      if (i < n && a.table[lo + i].first_chunk <= c) ++le;
+    }
+    const int k = static_cast<int>(__reduce_add_sync(0xffffffffu, le)) - 1;
     lo += k * stride;
-    n = end - lo;
+    n = min(stride, n - k * stride);
   }
   return lo;
 }

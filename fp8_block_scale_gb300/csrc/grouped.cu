@@ -108,6 +108,7 @@ struct Params {
   int n;           // wgrad: N extent
   uint32_t format; // 0 FP16, 1 BF16
   int accumulate;  // wgrad: add to dw, leave the dw of empty groups
+  int late_tmem;    // take tensor memory only once the tiles are known to run
   int a_one, b_one; // an MN-major stage of A, B is one copy (its width a multiple of 64), else one per 64 columns
 };
 
@@ -661,10 +662,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&maps.a);
     tma_prefetch_desc(&maps.b[0]);
   }
+  // Tensor memory is taken while the group tables are still to be read, unless
+  // the few-slots path, which has no use for it, is likely to run.
+  if (!p.late_tmem && warp == 1) {
+    pair::tmem_alloc(smem_u32(&ctl->tmem_base), 512);
+    pair::tmem_relinquish();
+  }
+  __syncwarp();
+  pair::cluster_arrive();   // (waited for below: the peer's latency passes meanwhile)
   pdl_launch_dependents();
   pdl_wait();
   count_tiles<kMode>(p, ctl);
+  tc_fence_before();
   __syncthreads();
+  pair::cluster_wait();  // the peer's copies and arrivals target initialised barriers
+  tc_fence_after();
   const uint32_t total = ctl->first[p.E];
   const uint32_t tile0 = blockIdx.x / 2, step = gridDim.x / 2;
   constexpr bool kFew = kMode == kForward || kMode == kSwiglu;
@@ -679,24 +691,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       few_slots<kMode, T, 16>(p, ctl, sA, reinterpret_cast<float*>(sC));
     __syncthreads();
     if (threadIdx.x == 0 && ctl->abort_flag && p.status) atomicOr(p.status, MOE_DEV_TIMEOUT);
+    if (!p.late_tmem) {
+      pair::cluster_sync();  // (tensor memory is given back by both CTAs together)
+      if (warp == 1) pair::tmem_dealloc(ctl->tmem_base, 512);
+    }
     return;
   }
+  if (p.late_tmem) {
+    if (warp == 1) {
+      pair::tmem_alloc(smem_u32(&ctl->tmem_base), 512);
+      pair::tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    pair::cluster_sync();
+    tc_fence_after();
+  }
+  const uint32_t tmem_base = ctl->tmem_base;
   // Where no tile is wide, B's share of a stage is smaller and the ring longer:
   // few columns are soon multiplied, and it is the copies' latency that bounds
   // (24 groups of 65 slots, K 1160, N 712: a block every 0.33 us with 6 stages).
   const int bstage = kMode == kWgrad || ctl->most > 128 ? kBBytes : ctl->most > 64 ? kBBytes / 2 : kBBytes / 4;
   const int stages = kMode == kWgrad ? Cfg<kMode>::kStages : bstage == kBBytes ? 6 : bstage == kBBytes / 2 ? 8 : 9;
   uint8_t* sB = sA + stages * kABytes;
-  if (warp == 1) {
-    pair::tmem_alloc(smem_u32(&ctl->tmem_base), 512);
-    pair::tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  pair::cluster_sync();  // the peer's copies and arrivals target initialised barriers
-  tc_fence_after();
-  const uint32_t tmem_base = ctl->tmem_base;
-
   if (warp == 0 || warp == 6) {
     // ------------------------------------------------------------ producers (A: warp 0, B: warp 6)
     const bool isA = warp == 0;
@@ -1150,6 +1167,8 @@ moe_status moe_grouped_gemm(const moe_grouped_args* a, moe_stream_t stream) {
   const int64_t mt = ceil_div(p.m, kTileM);
   const int64_t groups = a->E < a->rows ? a->E : a->rows;
   int64_t most = mt * (ceil_div(a->rows, kTileN) + groups);
+  // (0.6 us either way: at 144 slots for 9 groups of one, at 1560 for 24 of 65)
+  p.late_tmem = fwd && a->rows <= 2 * kFewSlots * groups ? 1 : 0;
   // (the few-slots path has a unit of 16 rows for each CTA)
   if (fwd && most < ceil_div(p.m, 32) * groups) most = ceil_div(p.m, 32) * groups;
   const bool bf = a->dtype == MOE_TYPE_BF16;
