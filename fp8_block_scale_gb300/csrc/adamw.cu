@@ -6,9 +6,11 @@
 // parameter and both states once and writes the parameter, its 16-bit copy
 // and the states once: HBM bounds it.
 //
-// The arithmetic is FP32.
+// The arithmetic is FP32.  268 million elements, BF16 gradients and copy: 32-bit
+// states 1145 us (28 bytes an element, 6.6 TB/s, the measured copy rate), 8-bit
+// states 711 us (16.1 bytes, 6.1 TB/s; some 50 instructions an element keep the
+// schedulers busy enough that the loads have to run a chunk ahead).
 #include <cmath>
-#include <mutex>
 #include <new>
 #include <vector>
 

@@ -25,6 +25,16 @@
 // are only a few blocks long).  Two 256-column accumulators let the drain of
 // one tile overlap the products of the next.  The CTAs are persistent: the
 // tiles of all groups form one sequence, dealt round-robin to the pairs.
+//
+// What bounds it, and what it measures on one GB300 (BF16, bursts):
+//  - many rows (8 experts of 8192, K 4096, N 2048): a block of 64 contraction
+//    elements takes 0.30 us, of which 0.27 the MMAs and 0.24 the 32 KB that each
+//    SM receives (about 135 GB/s at most); 1777 TFLOP/s forward, 1860 input
+//    gradient, 1740 weight gradient;
+//  - a training batch (288 experts of 228 rows): the weights' bytes; forward 854
+//    us (6.6 TB/s), with SwiGLU and its inputs kept 885 us, input gradient 848
+//    us; the weight gradient, 4.8 GB written, 1065 us (5.3 TB/s);
+//  - few rows: the weights' bytes, see the few-slots path below.
 #include <mutex>
 #include <type_traits>
 
@@ -359,7 +369,9 @@ __device__ __forceinline__ uint32_t pair_rows(float v0, float v1, bool odd) {
 // m16n8k16 MMAs with 8 or 16 slots as columns; as the order of the contraction
 // is free, a lane's 16 contiguous bytes of a weight row serve as its A
 // fragments of two MMAs, and the same 16 bytes of a slot's row as the B
-// fragments.
+// fragments.  One token through 9 of 257 experts (K 7168, N 512, SwiGLU): 16 us
+// for 66 MB, of which about 3 are launch, tables and the first loads; 8 tokens
+// 74 us (6.4 TB/s), 32 tokens 193 us (6.8 TB/s).
 constexpr int kFewSlots = 16;
 
 template <typename T>

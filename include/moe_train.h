@@ -184,8 +184,8 @@ moe_status moe_swiglu_backward(const moe_swiglu_backward_args* args, moe_stream_
  *
  * State bits 32: exp_avg and exp_avg_sq hold m and v in FP32.
  * State bits 8: they hold E4M3 codes of m and of r = sqrt(v), with one FP32
- * scale per 128 consecutive elements (the largest magnitude / 448; a group of
- * zeros has scale 0), each rewritten after the step's own update has used the
+ * scale per 128 consecutive elements (the largest magnitude times 1/448; a
+ * group of zeros has scale 0), each rewritten after the step's own update has used the
  * unrounded values.  m is rounded to nearest even.  r moves by less than half
  * a code per step when beta2 is near 1, and would stand still under rounding
  * to nearest; it is rounded up with the probability of the part cut off, from
