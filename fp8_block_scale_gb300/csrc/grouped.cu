@@ -33,7 +33,7 @@
 //    gradient, 1740 weight gradient;
 //  - a training batch (288 experts of 228 rows): the weights' bytes; forward 854
 //    us (6.6 TB/s), with SwiGLU and its inputs kept 885 us, input gradient 848
-//    us; the weight gradient, 4.8 GB written, 1065 us (5.3 TB/s);
+//    us; the weight gradient, 4.8 GB written, 1050 us (5.4 TB/s);
 //  - few rows: the weights' bytes, see the few-slots path below.
 #include <mutex>
 #include <type_traits>
