@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(256)
     const int32_t r = route_ids[s];
     const int64_t t = r >= 0 ? r / top_k : M;
     const bool live = t < M;
-    const uint4* src = x + (live ? t : 0) * ldx;
+    const uint4* src = live ? x + t * ldx : x;
     uint4* dst = xs + s * ldxs;
     for (int v = lane; v < vecs; v += 32) __stcs(dst + v, live ? src[v] : make_uint4(0, 0, 0, 0));
   }
@@ -251,7 +251,7 @@ moe_status moe_gather_rows(const void* x, int64_t M, int width, int64_t ldx, voi
       width % vec || ldx % vec || ldxs % vec || ldx < width || ldxs < width)
     return MOE_ERR_SHAPE;
   if (rows == 0) return MOE_OK;
-  if (!x || !xs || !route_ids) return MOE_ERR_NULL;
+  if ((M > 0 && !x) || !xs || !route_ids) return MOE_ERR_NULL;   // (without tokens every row becomes zero)
   if (!aligned16(x) || !aligned16(xs)) return MOE_ERR_ALIGN;
   if (overlap(x, extent_bytes(M, ldx, width, eb), xs, extent_bytes(rows, ldxs, width, eb))) return MOE_ERR_SHAPE;
   DeviceInfo dev;
@@ -274,13 +274,14 @@ moe_status moe_sum_routes(const void* y, int64_t rows, int width, int64_t ldy, v
       width % vec || ldy % vec || ldout % vec || ldy < width || ldout < width)
     return MOE_ERR_SHAPE;
   if (M == 0) return MOE_OK;
-  if (!y || !out || !route_slot) return MOE_ERR_NULL;
+  if ((rows > 0 && !y) || !out || !route_slot) return MOE_ERR_NULL;   // (without rows every sum is empty)
   if (!aligned16(y) || !aligned16(out)) return MOE_ERR_ALIGN;
   if (overlap(y, extent_bytes(rows, ldy, width, eb), out, extent_bytes(M, ldout, width, eb))) return MOE_ERR_SHAPE;
   DeviceInfo dev;
   if (current_device(&dev) != MOE_OK) return MOE_ERR_CUDA;
-  if (!on_device(y, dev.device) || !on_device(out, dev.device) || !on_device(route_slot, dev.device))
-    return MOE_ERR_DEVICE;
+  const void* ptrs[] = {y, out, route_slot};
+  for (const void* p : ptrs)
+    if (p && !on_device(p, dev.device)) return MOE_ERR_DEVICE;
   auto kernel = dtype == MOE_TYPE_BF16   ? sum_routes_kernel<__nv_bfloat16>
                 : dtype == MOE_TYPE_FP16 ? sum_routes_kernel<__half>
                                          : sum_routes_kernel<float>;

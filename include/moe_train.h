@@ -63,7 +63,8 @@ moe_status moe_plan_groups(const int32_t* sorted_token_ids, int64_t sorted_cap, 
  *  route_ids  [rows] (sorted_token_ids of a plan)
  *  num_rows   nullable [1] device scalar (num_tokens_post_padded); NULL: rows
  * dtype BF16, FP16 or FP32; width, ldx and ldxs multiples of 16 bytes' worth
- * of elements, x and xs 16-byte aligned; x and xs do not overlap. */
+ * of elements, x and xs 16-byte aligned; x and xs do not overlap.  x may be
+ * NULL where M is 0. */
 moe_status moe_gather_rows(const void* x, int64_t M, int width, int64_t ldx, void* xs, int64_t rows, int64_t ldxs,
                            const int32_t* route_ids, int top_k, const int32_t* num_rows, int dtype,
                            moe_stream_t stream);
@@ -72,7 +73,8 @@ moe_status moe_gather_rows(const void* x, int64_t M, int width, int64_t ldx, voi
  * order of j (first out[t] itself if accumulate != 0) and rounded once.
  * Slots outside [0, rows) add nothing; a token without any gives zero.
  *  y [rows, ldy], out [M, ldout], route_slot [M, top_k]
- * Types, widths and alignment as above; y and out do not overlap. */
+ * Types, widths and alignment as above; y and out do not overlap.  y may be
+ * NULL where rows is 0. */
 moe_status moe_sum_routes(const void* y, int64_t rows, int width, int64_t ldy, void* out, int64_t M, int64_t ldout,
                           const int32_t* route_slot, int top_k, int accumulate, int dtype, moe_stream_t stream);
 

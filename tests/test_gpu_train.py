@@ -331,6 +331,21 @@ def test_gather_and_sum(M, k, width, dtype):
     assert (out._base[:, width:] == 2.0).all()
 
 
+def test_gather_without_tokens_and_sum_without_rows():
+    ids = torch.full((16,), 0, dtype=torch.int32, device="cuda")
+    xs = torch.full((16, 64), float("nan"), dtype=BF16, device="cuda")
+    L.moe_gather_rows(torch.empty(0, 64, dtype=BF16, device="cuda"), xs, ids, 2)
+    assert torch.equal(xs, torch.zeros_like(xs))
+    out = torch.full((8, 64), float("nan"), dtype=BF16, device="cuda")
+    none = torch.empty(0, 64, dtype=BF16, device="cuda")
+    L.moe_sum_routes(none, out, ids, 2)
+    assert torch.equal(out, torch.zeros_like(out))
+    kept = torch.randn(8, 64, device="cuda").to(BF16)
+    out.copy_(kept)
+    L.moe_sum_routes(none, out, ids, 2, accumulate=True)
+    assert torch.equal(out, kept)
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP16])
 @pytest.mark.parametrize("rows,I", [(1, 8), (3, 24), (77, 256), (50, 1032), (2000, 128)])
 @pytest.mark.parametrize("kind", ["routes", "slots", "bare", "in place"])
