@@ -111,9 +111,13 @@ __device__ __forceinline__ uint4 to_vec<float>(const float (&acc)[8]) {
                     __float_as_uint(acc[3]));
 }
 
-// One thread per 16-byte vector of the output.  8192 tokens of 8 routes, rows of
-// 8 KB: 91 us, 6.6 TB/s (the measured copy rate); 1000 of 9, 14 KB: 24 us.
-template <typename T>
+// One thread per 16-byte vector of the output, kBatch routes' rows in flight at
+// a time, added in order.  Rounds without idle places count: every load and
+// addition is predicated, and few registers keep many threads resident.  1000
+// tokens of 9 routes, rows of 14 KB: 19.3 us in rounds of 5, 24.2 in rounds of 8;
+// 4096 of 4, 8 KB: 23.0 against 30.2; 8192 of 8, 8 KB: 89.1 in rounds of 4 (6.8
+// TB/s, a little of it from L2), 90.3 in one of 8.
+template <typename T, int kBatch>
 __global__ void __launch_bounds__(256)
     sum_routes_kernel(const uint4* __restrict__ y, int64_t rows, int vecs, int64_t ldy, uint4* __restrict__ out,
                       int64_t M, int64_t ldout, const int32_t* __restrict__ route_slot, int top_k, int accumulate) {
@@ -125,23 +129,31 @@ __global__ void __launch_bounds__(256)
     const int v = static_cast<int>(i - t * vecs);
     float acc[8] = {};
     if (accumulate) add_vec<T>(out[t * ldout + v], acc);
-    // eight routes' rows in flight at a time, added in order
-    for (int j0 = 0; j0 < top_k; j0 += 8) {
-      int32_t slot[8];
-      uint4 row[8];
+    for (int j0 = 0; j0 < top_k; j0 += kBatch) {
+      int32_t slot[kBatch];
+      uint4 row[kBatch];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) slot[j] = j0 + j < top_k ? __ldg(route_slot + t * top_k + j0 + j) : -1;
+      for (int j = 0; j < kBatch; ++j) slot[j] = j0 + j < top_k ? __ldg(route_slot + t * top_k + j0 + j) : -1;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < kBatch; ++j) {
         row[j] = make_uint4(0, 0, 0, 0);
         if (slot[j] >= 0 && slot[j] < rows) row[j] = __ldcs(y + slot[j] * ldy + v);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < kBatch; ++j)
         if (slot[j] >= 0 && slot[j] < rows) add_vec<T>(row[j], acc);
     }
-    out[t * ldout + v] = to_vec<T>(acc);
+    __stcs(out + t * ldout + v, to_vec<T>(acc));
   }
+}
+
+template <typename T>
+auto sum_routes_of(int batch) {
+  return batch == 1   ? sum_routes_kernel<T, 1>
+         : batch == 2 ? sum_routes_kernel<T, 2>
+         : batch == 3 ? sum_routes_kernel<T, 3>
+         : batch == 4 ? sum_routes_kernel<T, 4>
+                      : sum_routes_kernel<T, 5>;
 }
 
 // ---------------------------------------------------------------- SwiGLU gradient
@@ -282,9 +294,12 @@ moe_status moe_sum_routes(const void* y, int64_t rows, int width, int64_t ldy, v
   const void* ptrs[] = {y, out, route_slot};
   for (const void* p : ptrs)
     if (p && !on_device(p, dev.device)) return MOE_ERR_DEVICE;
-  auto kernel = dtype == MOE_TYPE_BF16   ? sum_routes_kernel<__nv_bfloat16>
-                : dtype == MOE_TYPE_FP16 ? sum_routes_kernel<__half>
-                                         : sum_routes_kernel<float>;
+  // rounds of at most five routes, as equal as they can be (rounds of 10, 12 and
+  // 16 were slower for every top_k)
+  const int batch = static_cast<int>(ceil_div(top_k, ceil_div(top_k, 5)));
+  auto kernel = dtype == MOE_TYPE_BF16   ? sum_routes_of<__nv_bfloat16>(batch)
+                : dtype == MOE_TYPE_FP16 ? sum_routes_of<__half>(batch)
+                                         : sum_routes_of<float>(batch);
   MOE_CUDA_TRY(launch_pdl(kernel, dim3(grid_of(M * (width / vec), 256, dev.sms)), dim3(256), 0, stream, 1,
                           static_cast<const uint4*>(y), rows, width / vec, ldy / vec, static_cast<uint4*>(out), M,
                           ldout / vec, route_slot, top_k, accumulate));

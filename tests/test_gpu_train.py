@@ -331,6 +331,12 @@ def test_gather_and_sum(M, k, width, dtype):
     assert (out._base[:, width:] == 2.0).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16, F32])
+@pytest.mark.parametrize("k", [4, 5, 6, 7, 8, 11, 16, 64])
+def test_sum_of_any_number_of_routes(k, dtype):
+    test_gather_and_sum(29, k, 136, dtype)
+
+
 def test_gather_without_tokens_and_sum_without_rows():
     ids = torch.full((16,), 0, dtype=torch.int32, device="cuda")
     xs = torch.full((16, 64), float("nan"), dtype=BF16, device="cuda")
