@@ -10,6 +10,7 @@
 // states 1145 us (28 bytes an element, 6.6 TB/s, the measured copy rate), 8-bit
 // states 711 us (16.1 bytes, 6.1 TB/s; some 50 instructions an element keep the
 // schedulers busy enough that the loads have to run a chunk ahead).
+#include <cfloat>
 #include <cmath>
 #include <new>
 #include <vector>
@@ -86,7 +87,9 @@ __device__ __forceinline__ float2 neg(float2 v) { return make_float2(-v.x, -v.y)
 __device__ __forceinline__ float2 root2(float2 v) {
   const float2 y = make_float2(rsqrt_fast(fmaxf(v.x, 1e-37f)), rsqrt_fast(fmaxf(v.y, 1e-37f)));
   const float2 s = __fmul2_rn(v, y);
-  return __ffma2_rn(__ffma2_rn(neg(s), s, v), __fmul2_rn(y, both(0.5f)), s);
+  const float2 r = __ffma2_rn(__ffma2_rn(neg(s), s, v), __fmul2_rn(y, both(0.5f)), s);
+  // (infinity is its own root; the steps above would make it a NaN)
+  return make_float2(v.x > FLT_MAX ? v.x : r.x, v.y > FLT_MAX ? v.y : r.y);
 }
 // a / b, `inv` the correctly rounded reciprocal of b.
 __device__ __forceinline__ float2 quotient2(float2 a, float b, float inv) {

@@ -495,6 +495,17 @@ def test_adamw_step(bits, grad, model):
             assert ((got >= lo) & (got <= hi)).all(), (i, name, int(((got < lo) | (got > hi)).sum()))
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_second_moment_beyond_fp32(bits):
+    # v overflows to infinity, m does not: the update is m / inf = 0
+    ts = _tensors([300], bits, F32, None, gen(5))
+    ts[0]["grad"][7:200:3] = 1e25
+    before = ts[0]["param"].clone()
+    L.moe_adamw_step(L.make_adamw_args(L.AdamWTable(ts), seed=1, **HYPER))
+    assert torch.equal(ts[0]["param"][7:200:3], before[7:200:3])
+    assert bool(torch.isfinite(ts[0]["param"]).all())
+
+
 def test_adamw_skip_leaves_everything():
     for bits in (32, 8):
         g = gen(9)
