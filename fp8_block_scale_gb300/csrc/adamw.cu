@@ -8,7 +8,7 @@
 //
 // The arithmetic is FP32.  268 million elements, BF16 gradients and copy: 32-bit
 // states 1145 us (28 bytes an element, 6.6 TB/s, the measured copy rate), 8-bit
-// states 711 us (16.1 bytes, 6.1 TB/s; some 50 instructions an element keep the
+// states 714 us (16.1 bytes, 6.05 TB/s; some 50 instructions an element keep the
 // schedulers busy enough that the loads have to run a chunk ahead).
 #include <cfloat>
 #include <cmath>
