@@ -113,6 +113,7 @@ class ExpertLayer:
         [tokens, top_k]); fills grads.  Uses the last forward's buffers up."""
         L.moe_gather_rows(dout, self.dys, self.sorted_ids, self.top_k, self.num_padded)
         L.moe_grouped_gemm(self._dh)
+        self.dweights.zero_()                             # (the kernel leaves routes that the plan does not hold)
         L.moe_swiglu_backward(self._swiglu)
         L.moe_grouped_wgrad(self._dw2)
         L.moe_grouped_wgrad(self._dw13)
