@@ -429,6 +429,9 @@ def moe_quantize_act_1x128_ue8m0(x_bf16, q, scale, stream=None):
 
 
 def moe_quantize_weight_128x128(w_bf16, q, scale, stream=None):
+    # (BF16, or its bit patterns: another type's bits would be read as BF16)
+    if w_bf16.dtype not in (torch.bfloat16, torch.uint16, torch.int16):
+        raise ValueError(f"w_bf16: dtype {w_bf16.dtype}, expected {torch.bfloat16}")
     E, rows, cols = w_bf16.shape
     _check("moe_quantize_weight_128x128", load().moe_quantize_weight_128x128(
         _ptr(w_bf16), E, rows, cols, _ptr(q), _ptr(scale), _stream(stream)))

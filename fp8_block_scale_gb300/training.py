@@ -129,7 +129,7 @@ class ExpertLayer:
 
     def quantized(self):
         """The trained weights as the FP8 forward takes them: (w13 interleaved,
-        w13_scale, w2, w2_scale).  H, I multiples of 128; BF16 weights."""
+        w13_scale, w2, w2_scale).  H, I multiples of 128; BF16 weights, ValueError for others."""
         out = []
         for w in self.models:
             E, rows, cols = w.shape
