@@ -92,8 +92,18 @@ class ExpertLayer:
         self._dxs = L.make_grouped_args(self.pre, self.w13, self.dxs, *groups, input_gradient=True,
                                         device_status=self.status)
 
+    def _batch(self, name, t, width, dtypes):
+        """ValueError unless t is a [tokens, width] tensor of one of the types (the layer's buffers hold as many rows)."""
+        if tuple(t.shape) != (self.M, width):
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(self.M, width)}")
+        if t.dtype not in dtypes:
+            raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+
     def route(self, logits):
-        """Router, plan and groups from logits [tokens, E] (float32 or bfloat16)."""
+        """Router, plan and groups from logits [tokens, E] (contiguous, float32 or bfloat16)."""
+        self._batch("logits", logits, self.E, (torch.float32, torch.bfloat16))
+        if not logits.is_contiguous():
+            raise ValueError("logits: a contiguous tensor is expected")
         L.moe_route_topk(logits, self.top_k, self.topk_ids, self.topk_weights)
         L.moe_plan(self.topk_ids, self.E, self.block_m, self.sorted_ids, self.expert_ids, self.num_padded,
                    self.plan_workspace)
@@ -102,6 +112,7 @@ class ExpertLayer:
 
     def forward(self, x):
         """x [tokens, H] -> out [tokens, H] (the layer's own buffer)."""
+        self._batch("x", x, self.H, (self.dtype,))
         L.moe_gather_rows(x, self.xs, self.sorted_ids, self.top_k, self.num_padded)
         L.moe_grouped_gemm(self._up)
         L.moe_grouped_gemm(self._down)
@@ -111,6 +122,7 @@ class ExpertLayer:
     def backward(self, dout):
         """dout [tokens, H] -> (dx [tokens, H], the route weights' gradient
         [tokens, top_k]); fills grads.  Uses the last forward's buffers up."""
+        self._batch("dout", dout, self.H, (self.dtype,))
         L.moe_gather_rows(dout, self.dys, self.sorted_ids, self.top_k, self.num_padded)
         L.moe_grouped_gemm(self._dh)
         self.dweights.zero_()                             # (the kernel leaves routes that the plan does not hold)

@@ -26,3 +26,36 @@ def test_only_bf16_weights_are_quantised(L, dtype):
     layer.models = [w, w]
     with pytest.raises(ValueError):
         layer.quantized()
+
+
+@pytest.fixture
+def layer(monkeypatch):
+    """A layer of 8 tokens, H 64, E 4 without its buffers; library calls fail the test."""
+    from fp8_block_scale_gb300 import training
+
+    class NoCalls:
+        def __getattr__(self, name):
+            pytest.fail(f"{name} was reached")
+
+    monkeypatch.setattr(training, "L", NoCalls())
+    layer = object.__new__(ExpertLayer)
+    layer.M, layer.H, layer.I, layer.E, layer.top_k, layer.dtype = 8, 64, 16, 4, 2, torch.bfloat16
+    return layer
+
+
+@pytest.mark.parametrize("logits", [
+    torch.zeros(9, 4), torch.zeros(7, 4), torch.zeros(8, 5), torch.zeros(8), torch.zeros(8, 4, dtype=torch.float16),
+    torch.zeros(4, 8).t(), torch.zeros(8, 8)[:, ::2]])
+def test_layer_refuses_logits_that_its_buffers_do_not_hold(layer, logits):
+    """More rows would be written past the ids and weights; fewer would leave those of a step before."""
+    with pytest.raises(ValueError):
+        layer.route(logits)
+
+
+@pytest.mark.parametrize("x", [torch.zeros(n, w, dtype=d) for n, w, d in (
+    (9, 64, torch.bfloat16), (7, 64, torch.bfloat16), (8, 72, torch.bfloat16), (8, 64, torch.float16))])
+def test_layer_refuses_other_rows(layer, x):
+    with pytest.raises(ValueError):
+        layer.forward(x)
+    with pytest.raises(ValueError):
+        layer.backward(x)
