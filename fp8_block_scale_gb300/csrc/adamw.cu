@@ -245,11 +245,19 @@ __device__ __forceinline__ uint32_t random20(uint32_t key, uint32_t i) {
   return (x ^ (x >> 16)) >> 12;
 }
 
+// The smaller one, or the NaN.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // E4M3 code of y in [0, 448.x], rounded up with probability (part cut off) /
 // (code spacing).  From 2^-6 on the spacing is 2^20 units of the FP32 pattern
 // (three mantissa bits stay), so the random bits are added below it and cut
 // off; the exponent's bias goes from 127 to 7.  Below, codes are multiples of
 // 2^-9.  A positive y stays at least at the smallest code.
+constexpr uint32_t kCodeNan = 0x7Fu;
 __device__ __forceinline__ uint32_t encode_random_high(float y, uint32_t u20) {
   return min(((__float_as_uint(y) + u20) >> 20) - ((127u - 7u) << 3), 0x7Eu);
 }
@@ -266,6 +274,47 @@ struct Group8 {
   uint32_t mw, vw;
   float ms, vs;
 };
+
+// The quotients and scales of a group (a whole warp's) that holds values so
+// small that a residual could underflow, or infinities.  An infinite scale would
+// make the group's other elements NaN or infinite at the next step: a v beyond
+// FP32 has a root within it, formed here from values 2^-80 times as large, and
+// what has not is held as the largest finite value.  (Apart, as its code between
+// the usual groups' cost 3%: 268 million elements 737 us against 716.)
+struct Scaled8 {
+  float4 m, r;
+  float m_scale, r_scale;
+};
+__device__ __noinline__ Scaled8 scale_unusual(const AdamParams& a, float4 m4, float4 r4, uint32_t old_codes,
+                                              float old_scale, float4 g4, float gs) {
+  float m[4] = {m4.x, m4.y, m4.z, m4.w}, r[4] = {r4.x, r4.y, r4.z, r4.w};
+  const float g[4] = {g4.x, g4.y, g4.z, g4.w};
+  float mmax = 0.f, rmax = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 old = e4m3x2_to_f32(old_codes >> (16 * (j / 2)) & 0xFFFFu);
+    if (r[j] > FLT_MAX) {
+      const float ro = __fmul_rn(j & 1 ? old.y : old.x, old_scale) * 0x1p-80f, gj = __fmul_rn(g[j], gs) * 0x1p-80f;
+      r[j] = fminf(__fsqrt_rn(ro * ro * a.beta2 + gj * gj * a.one_minus_beta2) * 0x1p80f, FLT_MAX);
+    }
+    if (fabsf(m[j]) > FLT_MAX) m[j] = copysignf(FLT_MAX, m[j]);
+    mmax = fmaxf(mmax, fabsf(m[j]));
+    rmax = fmaxf(rmax, r[j]);
+  }
+  Scaled8 o;
+  o.m_scale = __fmul_rn(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mmax))), 1.f / 448.f);
+  o.r_scale = __fmul_rn(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(rmax))), 1.f / 448.f);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    // (zero, or a NaN, without a scale)
+    m[j] = o.m_scale > 0.f ? __fdiv_rn(m[j], o.m_scale) : m[j] * 0.f;
+    r[j] = o.r_scale > 0.f ? __fdiv_rn(r[j], o.r_scale) : r[j] * 0.f;
+  }
+  o.m = make_float4(m[0], m[1], m[2], m[3]);
+  o.r = make_float4(r[0], r[1], r[2], r[3]);
+  return o;
+}
+
 template <bool kWhole>
 __device__ __forceinline__ void adamw8_group(const AdamParams& a, const AdamEntry& t, float decay, float gs,
                                              uint32_t tensor, int64_t group, Group8& x, const float (&g)[4], int have) {
@@ -291,16 +340,14 @@ __device__ __forceinline__ void adamw8_group(const AdamParams& a, const AdamEntr
     mmax = fmaxf(mmax, fmaxf(fabsf(m[2 * h]), fabsf(m[2 * h + 1])));
     rmax = fmaxf(rmax, fmaxf(r[2 * h], r[2 * h + 1]));
   }
-  // (nonnegative floats order as their patterns do)
+  // (nonnegative floats order as their patterns do; fmaxf leaves a NaN out of the
+  // group's largest, so that it stays in its element)
   mmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mmax)));
   rmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(rmax)));
-  const float mns = __fmul_rn(mmax, 1.f / 448.f), vns = __fmul_rn(rmax, 1.f / 448.f);
-  if (lane == 0) {
-    t.m_scale[group] = mns;
-    t.v_scale[group] = vns;
-  }
+  float mns = __fmul_rn(mmax, 1.f / 448.f), vns = __fmul_rn(rmax, 1.f / 448.f);
   float mq[4], y[4];
-  if (fminf(mmax, rmax) > 1e-25f) {
+  bool zeros = false;
+  if (fminf(mmax, rmax) > 1e-25f && fmaxf(mmax, rmax) <= FLT_MAX) {
     const float mi = __frcp_rn(mns), vi = __frcp_rn(vns);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -311,25 +358,35 @@ __device__ __forceinline__ void adamw8_group(const AdamParams& a, const AdamEntr
       y[2 * h] = z.x;
       y[2 * h + 1] = z.y;
     }
-  } else {   // zeros, or so small that a residual could underflow
+  } else if (__all_sync(0xffffffffu, m[0] == 0.f && m[1] == 0.f && m[2] == 0.f && m[3] == 0.f && r[0] == 0.f &&
+                                         r[1] == 0.f && r[2] == 0.f && r[3] == 0.f)) {
+    zeros = true;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      mq[j] = mns > 0.f ? __fdiv_rn(m[j], mns) : 0.f;
-      y[j] = vns > 0.f ? __fdiv_rn(r[j], vns) : 0.f;
-    }
+    for (int j = 0; j < 4; ++j) mq[j] = y[j] = 0.f;
+  } else {
+    const Scaled8 o = scale_unusual(a, make_float4(m[0], m[1], m[2], m[3]), make_float4(r[0], r[1], r[2], r[3]), x.vw,
+                                    x.vs, make_float4(g[0], g[1], g[2], g[3]), gs);
+    mq[0] = o.m.x; mq[1] = o.m.y; mq[2] = o.m.z; mq[3] = o.m.w;
+    y[0] = o.r.x; y[1] = o.r.y; y[2] = o.r.z; y[3] = o.r.w;
+    mns = o.m_scale;
+    vns = o.r_scale;
+  }
+  if (lane == 0) {
+    t.m_scale[group] = mns;
+    t.v_scale[group] = vns;
   }
   const uint32_t key = random_key(a.seed, tensor, i);
   uint32_t vo = 0;
-  if (__all_sync(0xffffffffu, fminf(fminf(y[0], y[1]), fminf(y[2], y[3])) >= 0x1p-6f)) {
-    // (roots within a factor of 28672 of the group's largest: the usual case)
+  if (__all_sync(0xffffffffu, min_nan(min_nan(y[0], y[1]), min_nan(y[2], y[3])) >= 0x1p-6f)) {
+    // (roots within a factor of 28672 of the group's largest, no NaN: the usual case)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       vo |= encode_random_high(y[j], random20(key, static_cast<uint32_t>(i) + j)) << (8 * j);
-  } else {
+  } else if (!zeros) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t code = encode_random(y[j], random20(key, static_cast<uint32_t>(i) + j));
-      vo |= (r[j] > 0.f && vns > 0.f ? code : 0u) << (8 * j);
+      vo |= (isnan(r[j]) ? kCodeNan : r[j] > 0.f && vns > 0.f ? code : 0u) << (8 * j);
     }
   }
   const uint32_t mo = cvt_e4m3x2(mq[0], mq[1]) | (static_cast<uint32_t>(cvt_e4m3x2(mq[2], mq[3])) << 16);

@@ -193,6 +193,12 @@ moe_status moe_swiglu_backward(const moe_swiglu_backward_args* args, moe_stream_
  * to nearest; it is rounded up with the probability of the part cut off, from
  * an integer hash of (seed, tensor, element): give every step its own seed.
  * A positive r never becomes code 0 (m / (0 + eps) would follow).
+ * A NaN becomes code 0x7F and stays in its element.  Where v passes FP32 the
+ * update is m / inf = 0, as with FP32 states, but r is held (formed without its
+ * square), so that v returns; m or r beyond FP32 are held as its largest value.
+ * Such an element decides its group's scale: its neighbours' m become 0 and
+ * their r the smallest code, 2^-9 of the scale, until it has decayed.  A step
+ * whose gradients overflow is better left out by `skip`.
  * ------------------------------------------------------------------------ */
 typedef struct moe_adamw_tensor {
   float* param;                /* [n] FP32                                                */
