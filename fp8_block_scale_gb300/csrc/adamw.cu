@@ -56,8 +56,7 @@ struct AdamParams {
 // The new m, v, root of v and parameter of one element.  m and v are rounded
 // once per written operation; the quotient of the update comes from the
 // hardware's reciprocal (within 2 units of the last place of the update, far
-// below the parameter's own rounding).  A v below 1e-37 loses precision.
-// Two elements at a time: the packed FP32 instructions round each half as the
+// below the parameter's own rounding).  Two elements at a time: the packed FP32 instructions round each half as the
 // scalar ones do.
 struct Elem2 {
   float2 m, v, r, p;
@@ -83,11 +82,20 @@ __device__ __forceinline__ float2 neg(float2 v) { return make_float2(-v.x, -v.y)
 
 // The states' codes are to be those of the formula, so roots and quotients are
 // rounded correctly: an approximation and its exact residual, corrected once
-// (Markstein's method).
-__device__ __forceinline__ float2 root2(float2 v) {
+// (Markstein's method).  Of all floats from 2^-102 on, every root is the
+// correctly rounded one.  Below, the residual underflows: the root's last bit may be
+// off, and from v = 1e-37 down it comes out too small (0.15 of it at 1e-39).
+// kSmall: small values are taken 2^100 times as large.  That costs 2.7% with
+// 8-bit states (733 us against 714 at 268 million elements) and 0.7% with 32-bit
+// ones, so it is chosen by eps, beside which such roots vanish (moe_adamw_step).
+template <bool kSmall>
+__device__ __forceinline__ float2 root2(float2 u) {
+  const bool up_x = kSmall && u.x < 0x1p-100f, up_y = kSmall && u.y < 0x1p-100f;
+  const float2 v = kSmall ? __fmul2_rn(u, make_float2(up_x ? 0x1p100f : 1.f, up_y ? 0x1p100f : 1.f)) : u;
   const float2 y = make_float2(rsqrt_fast(fmaxf(v.x, 1e-37f)), rsqrt_fast(fmaxf(v.y, 1e-37f)));
   const float2 s = __fmul2_rn(v, y);
-  const float2 r = __ffma2_rn(__ffma2_rn(neg(s), s, v), __fmul2_rn(y, both(0.5f)), s);
+  float2 r = __ffma2_rn(__ffma2_rn(neg(s), s, v), __fmul2_rn(y, both(0.5f)), s);
+  if (kSmall) r = __fmul2_rn(r, make_float2(up_x ? 0x1p-50f : 1.f, up_y ? 0x1p-50f : 1.f));
   // (infinity is its own root; the steps above would make it a NaN)
   return make_float2(v.x > FLT_MAX ? v.x : r.x, v.y > FLT_MAX ? v.y : r.y);
 }
@@ -96,11 +104,15 @@ __device__ __forceinline__ float2 quotient2(float2 a, float b, float inv) {
   const float2 q = __fmul2_rn(a, both(inv));
   return __ffma2_rn(__ffma2_rn(neg(q), both(b), a), both(inv), q);
 }
+__device__ __forceinline__ float2 second_moment(const AdamParams& a, float2 g, float2 v) {
+  return add_unfused(__fmul2_rn(v, both(a.beta2)), __fmul2_rn(__fmul2_rn(g, g), both(a.one_minus_beta2)));
+}
+template <bool kSmall>
 __device__ __forceinline__ Elem2 adam_elem2(const AdamParams& a, float decay, float2 g, float2 p, float2 m, float2 v) {
   Elem2 e;
   e.m = add_unfused(__fmul2_rn(m, both(a.beta1)), __fmul2_rn(g, both(a.one_minus_beta1)));
-  e.v = add_unfused(__fmul2_rn(v, both(a.beta2)), __fmul2_rn(__fmul2_rn(g, g), both(a.one_minus_beta2)));
-  e.r = root2(e.v);
+  e.v = second_moment(a, g, v);
+  e.r = root2<kSmall>(e.v);
   const float2 den = __ffma2_rn(e.r, both(a.root_scale), both(a.eps));
   const float2 upd = __fmul2_rn(__fmul2_rn(e.m, both(-a.step_size)), make_float2(rcp_fast(den.x), rcp_fast(den.y)));
   e.p = __fadd2_rn(__fmul2_rn(p, both(decay)), upd);
@@ -168,7 +180,7 @@ __device__ __forceinline__ int find_entry(const AdamParams& a, int64_t c) {
 
 // A chunk, four elements a thread and step; steps that pass the tensor's end
 // are left out.
-template <int kGrad>
+template <int kGrad, bool kSmall>
 __device__ __forceinline__ void adamw32_chunk(const AdamParams& a, const AdamEntry& t, float decay, float gs,
                                               int64_t i0) {
   // every load of the chunk goes out before the first result is needed
@@ -191,9 +203,9 @@ __device__ __forceinline__ void adamw32_chunk(const AdamParams& a, const AdamEnt
     if (i + 4 > t.n) continue;
     float g[4], p[4];
     grad4<kGrad>(raw[u], g);
-    const Elem2 lo = adam_elem2(a, decay, __fmul2_rn(make_float2(g[0], g[1]), both(gs)), make_float2(p4[u].x, p4[u].y),
+    const Elem2 lo = adam_elem2<kSmall>(a, decay, __fmul2_rn(make_float2(g[0], g[1]), both(gs)), make_float2(p4[u].x, p4[u].y),
                                 make_float2(m4[u].x, m4[u].y), make_float2(v4[u].x, v4[u].y));
-    const Elem2 hi = adam_elem2(a, decay, __fmul2_rn(make_float2(g[2], g[3]), both(gs)), make_float2(p4[u].z, p4[u].w),
+    const Elem2 hi = adam_elem2<kSmall>(a, decay, __fmul2_rn(make_float2(g[2], g[3]), both(gs)), make_float2(p4[u].z, p4[u].w),
                                 make_float2(m4[u].z, m4[u].w), make_float2(v4[u].z, v4[u].w));
     p[0] = lo.p.x; p[1] = lo.p.y; p[2] = hi.p.x; p[3] = hi.p.y;
     m4[u] = make_float4(lo.m.x, lo.m.y, hi.m.x, hi.m.y);
@@ -205,7 +217,7 @@ __device__ __forceinline__ void adamw32_chunk(const AdamParams& a, const AdamEnt
   }
 }
 
-template <int kGrad>
+template <int kGrad, bool kSmall>
 __global__ void __launch_bounds__(kThreads) adamw32_kernel(const __grid_constant__ AdamParams a) {
   pdl_wait();
   if (a.skip && *a.skip) return;
@@ -215,13 +227,13 @@ __global__ void __launch_bounds__(kThreads) adamw32_kernel(const __grid_constant
     if (t.grad_dtype != kGrad) continue;
     const float decay = fmaf(-a.lr, t.weight_decay, 1.0f);
     const int64_t i0 = (c - t.first_chunk) * kChunk;
-    adamw32_chunk<kGrad>(a, t, decay, gs, i0);
+    adamw32_chunk<kGrad, kSmall>(a, t, decay, gs, i0);
     // the last one to three elements
     const int64_t k = (t.n & ~int64_t(3)) + threadIdx.x;
     if (i0 + kChunk > t.n && k < t.n) {
       float* m = static_cast<float*>(t.m);
       float* v = static_cast<float*>(t.v);
-      const Elem2 e = adam_elem2(a, decay, both(__fmul_rn(load_grad1(t, k), gs)), both(t.param[k]), both(m[k]), both(v[k]));
+      const Elem2 e = adam_elem2<kSmall>(a, decay, both(__fmul_rn(load_grad1(t, k), gs)), both(t.param[k]), both(m[k]), both(v[k]));
       t.param[k] = e.p.x;
       m[k] = e.m.x;
       v[k] = e.v.x;
@@ -275,47 +287,61 @@ struct Group8 {
   float ms, vs;
 };
 
-// The quotients and scales of a group (a whole warp's) that holds values so
-// small that a residual could underflow, or infinities.  An infinite scale would
-// make the group's other elements NaN or infinite at the next step: a v beyond
-// FP32 has a root within it, formed here from values 2^-80 times as large, and
-// what has not is held as the largest finite value.  (Apart, as its code between
-// the usual groups' cost 3%: 268 million elements 737 us against 716.)
+// The quotients and scales of a group (a whole warp's) that holds infinities or
+// whose largest values are so small that a residual could underflow, or that
+// root2's misses would count.  An infinite scale would make the group's other
+// elements NaN or infinite at the next step: a v beyond FP32 has a root within it,
+// formed here from values 2^-80 times as large, and what has not is held as the
+// largest finite value.  (Apart, as its code between the usual groups' cost 3%:
+// 268 million elements 737 us against 716.)
 struct Scaled8 {
   float4 m, r;
   float m_scale, r_scale;
 };
+// Four values, divided by their group's scale: the largest times 1/448.
+__device__ __forceinline__ float scale_to(float (&x)[4], float largest) {
+  const float scale = __fmul_rn(largest, 1.f / 448.f), up = largest > 1e-25f ? 1.f : 0x1p90f;
+  const float by = __fmul_rn(scale, up), inv = __frcp_rn(by);
+#pragma unroll
+  for (int h = 0; h < 4; h += 2) {
+    const float2 q = quotient2(__fmul2_rn(make_float2(x[h], x[h + 1]), both(up)), by, inv);
+    // (zero, or a NaN, without a scale)
+    x[h] = scale > 0.f ? q.x : x[h] * 0.f;
+    x[h + 1] = scale > 0.f ? q.y : x[h + 1] * 0.f;
+  }
+  return scale;
+}
 __device__ __noinline__ Scaled8 scale_unusual(const AdamParams& a, float4 m4, float4 r4, uint32_t old_codes,
                                               float old_scale, float4 g4, float gs) {
   float m[4] = {m4.x, m4.y, m4.z, m4.w}, r[4] = {r4.x, r4.y, r4.z, r4.w};
   const float g[4] = {g4.x, g4.y, g4.z, g4.w};
   float mmax = 0.f, rmax = 0.f;
 #pragma unroll
+  for (int h = 0; h < 4; h += 2) {
+    const float2 ro = __fmul2_rn(e4m3x2_to_f32(old_codes >> (8 * h) & 0xFFFFu), both(old_scale));
+    const float2 gj = __fmul2_rn(make_float2(g[h], g[h + 1]), both(gs));
+    const float2 v = second_moment(a, gj, __fmul2_rn(ro, ro));
+    const float2 x = __fmul2_rn(ro, both(0x1p-80f)), y = __fmul2_rn(gj, both(0x1p-80f));
+    const float2 far = second_moment(a, y, __fmul2_rn(x, x)), near = root2<true>(v);
+    // (r is zero past the tensor's end)
+    if (r[h] > 0.f) r[h] = v.x > FLT_MAX ? fminf(__fsqrt_rn(far.x) * 0x1p80f, FLT_MAX) : near.x;
+    if (r[h + 1] > 0.f) r[h + 1] = v.y > FLT_MAX ? fminf(__fsqrt_rn(far.y) * 0x1p80f, FLT_MAX) : near.y;
+  }
+#pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float2 old = e4m3x2_to_f32(old_codes >> (16 * (j / 2)) & 0xFFFFu);
-    if (r[j] > FLT_MAX) {
-      const float ro = __fmul_rn(j & 1 ? old.y : old.x, old_scale) * 0x1p-80f, gj = __fmul_rn(g[j], gs) * 0x1p-80f;
-      r[j] = fminf(__fsqrt_rn(ro * ro * a.beta2 + gj * gj * a.one_minus_beta2) * 0x1p80f, FLT_MAX);
-    }
     if (fabsf(m[j]) > FLT_MAX) m[j] = copysignf(FLT_MAX, m[j]);
     mmax = fmaxf(mmax, fabsf(m[j]));
     rmax = fmaxf(rmax, r[j]);
   }
   Scaled8 o;
-  o.m_scale = __fmul_rn(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mmax))), 1.f / 448.f);
-  o.r_scale = __fmul_rn(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(rmax))), 1.f / 448.f);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    // (zero, or a NaN, without a scale)
-    m[j] = o.m_scale > 0.f ? __fdiv_rn(m[j], o.m_scale) : m[j] * 0.f;
-    r[j] = o.r_scale > 0.f ? __fdiv_rn(r[j], o.r_scale) : r[j] * 0.f;
-  }
+  o.m_scale = scale_to(m, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mmax))));
+  o.r_scale = scale_to(r, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(rmax))));
   o.m = make_float4(m[0], m[1], m[2], m[3]);
   o.r = make_float4(r[0], r[1], r[2], r[3]);
   return o;
 }
 
-template <bool kWhole>
+template <bool kWhole, bool kSmall>
 __device__ __forceinline__ void adamw8_group(const AdamParams& a, const AdamEntry& t, float decay, float gs,
                                              uint32_t tensor, int64_t group, Group8& x, const float (&g)[4], int have) {
   const int lane = threadIdx.x % 32;
@@ -328,7 +354,7 @@ __device__ __forceinline__ void adamw8_group(const AdamParams& a, const AdamEntr
   for (int h = 0; h < 2; ++h) {
     const float2 mo = __fmul2_rn(e4m3x2_to_f32(x.mw >> (16 * h) & 0xFFFFu), both(x.ms));
     const float2 ro = __fmul2_rn(e4m3x2_to_f32(x.vw >> (16 * h) & 0xFFFFu), both(x.vs));
-    const Elem2 e = adam_elem2(a, decay, __fmul2_rn(make_float2(g[2 * h], g[2 * h + 1]), both(gs)),
+    const Elem2 e = adam_elem2<kSmall>(a, decay, __fmul2_rn(make_float2(g[2 * h], g[2 * h + 1]), both(gs)),
                                make_float2(x.p[2 * h], x.p[2 * h + 1]), mo, __fmul2_rn(ro, ro));
     const bool in0 = kWhole || 2 * h < have, in1 = kWhole || 2 * h + 1 < have;
     m[2 * h] = in0 ? e.m.x : 0.f;
@@ -347,7 +373,9 @@ __device__ __forceinline__ void adamw8_group(const AdamParams& a, const AdamEntr
   float mns = __fmul_rn(mmax, 1.f / 448.f), vns = __fmul_rn(rmax, 1.f / 448.f);
   float mq[4], y[4];
   bool zeros = false;
-  if (fminf(mmax, rmax) > 1e-25f && fmaxf(mmax, rmax) <= FLT_MAX) {
+  // (8e-14: a v below 1e-37, whose root root2 misses, then gets the smallest code
+  // either way; a tensor of nothing but smaller roots takes 1397 us instead of 713)
+  if (mmax > 1e-25f && rmax > (kSmall ? 1e-25f : 8e-14f) && fmaxf(mmax, rmax) <= FLT_MAX) {
     const float mi = __frcp_rn(mns), vi = __frcp_rn(vns);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -423,6 +451,7 @@ __device__ __forceinline__ void load_group8(const AdamEntry& t, int64_t group, G
 }
 
 // (apart, so that its registers are not the loop's)
+template <bool kSmall>
 __device__ __noinline__ void adamw8_last(const AdamParams& a, float decay, float gs, uint32_t tensor) {
   const AdamEntry t = a.table[tensor];
   const int lane = threadIdx.x % 32;
@@ -441,14 +470,14 @@ __device__ __noinline__ void adamw8_last(const AdamParams& a, float decay, float
   x.ms = t.m_scale[group];
   x.vs = t.v_scale[group];
   __syncwarp();   // (lane 0 rewrites the scales that every lane has read)
-  adamw8_group<false>(a, t, decay, gs, tensor, group, x, g, have);
+  adamw8_group<false, kSmall>(a, t, decay, gs, tensor, group, x, g, have);
 }
 
 // While a CTA computes a chunk, its next chunk's loads are in flight (where
 // that is of the same tensor): with loads and arithmetic in turn the warps
 // mostly waited.  The CTAs walk the chunks side by side, not each a stretch of
 // its own: a thousand separate streams cost the translation of as many pages.
-template <int kGrad>
+template <int kGrad, bool kSmall>
 __global__ void __launch_bounds__(kThreads, 3) adamw8_kernel(const __grid_constant__ AdamParams a) {
   pdl_wait();
   if (a.skip && *a.skip) return;
@@ -483,13 +512,28 @@ __global__ void __launch_bounds__(kThreads, 3) adamw8_kernel(const __grid_consta
         if ((group + u * kWarps + 1) * 128 > t.n) continue;
         float g[4];
         grad4<kGrad>(x[u].graw, g);
-        adamw8_group<true>(a, t, decay, gs, id, group + u * kWarps, x[u], g, 4);
+        adamw8_group<true, kSmall>(a, t, decay, gs, id, group + u * kWarps, x[u], g, 4);
       }
       // a partly filled last group
-      if (c + 1 == past && t.n % 128 && warp == 0) adamw8_last(a, decay, gs, id);
+      if (c + 1 == past && t.n % 128 && warp == 0) adamw8_last<kSmall>(a, decay, gs, id);
       group = ahead;
     }
   }
+}
+
+using AdamKernel = void (*)(AdamParams);
+template <bool kSmall>
+AdamKernel adamw_kernel_of(int type, int state_bits) {
+  if (state_bits == 32)
+    return type == MOE_TYPE_BF16   ? adamw32_kernel<MOE_TYPE_BF16, kSmall>
+           : type == MOE_TYPE_FP16 ? adamw32_kernel<MOE_TYPE_FP16, kSmall>
+                                   : adamw32_kernel<MOE_TYPE_FP32, kSmall>;
+  return type == MOE_TYPE_BF16   ? adamw8_kernel<MOE_TYPE_BF16, kSmall>
+         : type == MOE_TYPE_FP16 ? adamw8_kernel<MOE_TYPE_FP16, kSmall>
+                                 : adamw8_kernel<MOE_TYPE_FP32, kSmall>;
+}
+AdamKernel adamw_kernel(int type, int state_bits, bool small) {
+  return small ? adamw_kernel_of<true>(type, state_bits) : adamw_kernel_of<false>(type, state_bits);
 }
 
 }  // namespace
@@ -599,16 +643,14 @@ moe_status moe_adamw_step(const moe_adamw_args* g, moe_stream_t stream) {
   // as many CTAs as are resident at once
   const int64_t most = static_cast<int64_t>(dev.sms) * (g->state_bits == 32 ? 16 : 3);
   const unsigned grid = static_cast<unsigned>(g->chunks < most ? g->chunks : most);
+  // The update's denominator is sqrt(v) root_scale + eps.  Roots that root2 misses
+  // without kSmall are below 3.2e-19 (their v below 1e-37), so from this eps on they
+  // change no more than its last bit.
+  const bool small = p.eps < 6e-12f * p.root_scale;
   // a kernel for each type of gradient that the table holds
   for (int type = 0; type < 3; ++type) {
     if (!(g->grad_types >> type & 1)) continue;
-    const auto kernel = g->state_bits == 32
-                            ? (type == MOE_TYPE_BF16   ? adamw32_kernel<MOE_TYPE_BF16>
-                               : type == MOE_TYPE_FP16 ? adamw32_kernel<MOE_TYPE_FP16>
-                                                       : adamw32_kernel<MOE_TYPE_FP32>)
-                            : (type == MOE_TYPE_BF16   ? adamw8_kernel<MOE_TYPE_BF16>
-                               : type == MOE_TYPE_FP16 ? adamw8_kernel<MOE_TYPE_FP16>
-                                                       : adamw8_kernel<MOE_TYPE_FP32>);
+    const auto kernel = adamw_kernel(type, g->state_bits, small);
     MOE_CUDA_TRY(launch_pdl(kernel, dim3(grid), dim3(kThreads), 0, stream, 1, p));
   }
   return MOE_OK;

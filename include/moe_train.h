@@ -183,6 +183,8 @@ moe_status moe_swiglu_backward(const moe_swiglu_backward_args* args, moe_stream_
  *   v = beta2 v + (1 - beta2) g^2
  *   p = p (1 - lr weight_decay) - (lr / (1 - beta1^step)) m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
  * and the rounded copy of p in `model`, where there is one.
+ * The update is right to a few roundings down to the smallest v, whatever eps;
+ * with eps = 0 an element whose v is 0 gets 0 / 0.
  *
  * State bits 32: exp_avg and exp_avg_sq hold m and v in FP32.
  * State bits 8: they hold E4M3 codes of m and of r = sqrt(v), with one FP32

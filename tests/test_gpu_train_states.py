@@ -76,3 +76,77 @@ def test_adamw8_nan_stays_in_its_element(where):
             assert (np.isnan(_values(t, name)) == hit).all(), (k, name)
         assert (np.isnan(f64(t["param"])) == hit).all()
         t["grad"] = torch.randn(n, generator=gen(7), device="cuda")
+
+
+def test_adamw_small_second_moments_without_eps():
+    """eps = 0 and v from the smallest subnormal on: the update follows the
+    stored v.  Seven roundings of at most 2^-23 each make the tolerance."""
+    n = 1 << 16
+    g = gen(13)
+    v = (10.0 ** (torch.rand(n, generator=g, device="cuda", dtype=torch.float64) * 15 - 45)).float().clamp_(min=2.0 ** -149)
+    m = torch.randn(n, generator=g, device="cuda") * v.double().sqrt().float()
+    t = {"param": torch.zeros(n, device="cuda"), "grad": torch.zeros(n, device="cuda"), "exp_avg": m, "exp_avg_sq": v}
+    _step([t], eps=0.0, beta2=0.9999)
+    m1, v1 = f64(t["exp_avg"]), f64(t["exp_avg_sq"])
+    live = v1 > 0
+    assert live.mean() > 0.9
+    b1, b2 = HYPER["beta1"], 0.9999
+    want = -HYPER["lr"] / (1 - b1 ** 3) * m1[live] / np.sqrt(v1[live] / (1 - b2 ** 3))
+    err = np.abs(f64(t["param"])[live] - want) / np.abs(want).clip(1e-30)
+    assert err.max() <= 7 * 2.0 ** -23
+
+
+def _random20(seed, tensor, n):
+    i = np.arange(n, dtype=np.uint64)
+    M = np.uint64(0xFFFFFFFF)
+    key = np.uint64((seed + 0x9E3779B9 * (tensor + 1)) & 0xFFFFFFFF)
+    x = (i * np.uint64(0x9E3779B1) + key) & M
+    x = ((x ^ (x >> np.uint64(16))) * np.uint64(0x7FEB352D)) & M
+    x = ((x ^ (x >> np.uint64(15))) * np.uint64(0x846CA68B)) & M
+    return ((x ^ (x >> np.uint64(16))) >> np.uint64(12)).astype(np.int64)
+
+
+def _formula32(t, index, seed, gs, beta1, beta2, **_):
+    """The states' codes and scales after a step, every operation of the formula
+    rounded to FP32 on its own: (m values, r values, m scale, r scale)."""
+    f = np.float32
+    n = t["param"].numel()
+    per = lambda s: np.repeat(s, 128)[:n]                                   # noqa: E731
+    state = lambda k: t[k].float().cpu().numpy() * per(t[k + "_scale"].cpu().numpy())   # noqa: E731
+    g = t["grad"].float().cpu().numpy() * f(gs)
+    m, r = state("exp_avg"), state("exp_avg_sq")
+    m = m * f(beta1) + g * f(1 - beta1)
+    r = np.sqrt((r * r) * f(beta2) + (g * g) * f(1 - beta2))
+    out = []
+    for x in (m, r):
+        b = np.zeros(-(-n // 128) * 128, f)
+        b[:n] = np.abs(x)
+        s = b.reshape(-1, 128).max(1) * f(1 / 448)
+        with np.errstate(divide="ignore", invalid="ignore"):
+            out += [np.where(per(s) > 0, x / per(s), f(0)), s]
+    mq, ms, y, rs = out
+    u = _random20(seed, index, n)
+    # from 2^-6 on a code's spacing is 2^20 units of the FP32 pattern, below it 2^-9
+    high = ((y.view(np.uint32).astype(np.int64) + u) >> 20 << 20).astype(np.uint32).view(f)
+    low = np.floor(np.maximum(y, f(2.0 ** -9)) * f(512) + u.astype(f) * f(2.0 ** -20)) / f(512)
+    code = np.where(y >= f(2.0 ** -6), np.minimum(high, f(448)), low)
+    return T.e4m3_nearest(mq.astype(np.float64)), np.where((r > 0) & (per(rs) > 0), code, 0), ms, rs
+
+
+@pytest.mark.parametrize("grad,eps", [(torch.bfloat16, 1e-6), (F32, 1e-6), (F32, 0.0)])
+def test_adamw8_codes_are_those_of_the_formula(grad, eps):
+    """Bit for bit, over enough chunks that every CTA takes several (456 or so
+    CTAs of 2048 elements), for ordinary and for very small states."""
+    g = gen(17)
+    ts = _tensors([3_000_077, 5000, 200_000], 8, grad, torch.bfloat16, g)
+    for name in ("exp_avg_scale", "exp_avg_sq_scale"):
+        ts[0][name][:4000] *= 1e-4           # (the gradients then decide)
+        ts[2][name] *= 2.0 ** -57            # second moments around and below 1e-37
+    ts[2]["grad"] = (ts[2]["grad"].double() * 2.0 ** -60).to(grad)
+    want = [_formula32(t, i, 3, 0.5, **HYPER) for i, t in enumerate(ts)]
+    _step(ts, seed=3, eps=eps, grad_scale=torch.tensor([0.5], device="cuda"))
+    for i, (t, (m, r, ms, rs)) in enumerate(zip(ts, want)):
+        for name, codes, scale in (("exp_avg", m, ms), ("exp_avg_sq", r, rs)):
+            assert (t[name + "_scale"].cpu().numpy() == scale).all(), (i, name)
+            got = f64(t[name].float())
+            assert (got == codes).all(), (i, name, int((got != codes).sum()))
