@@ -74,7 +74,9 @@ class ExpertLayer:
         self.table = L.AdamWTable(
             [{"param": p.view(-1), "model": m.view(-1), "grad": g.view(-1), **s}
              for p, m, g, s in zip(self.params, self.models, self.grads, self.states)], weight_decay=weight_decay)
-        self.steps = 0
+        self.steps = 0                                    # steps that changed the weights
+        self._calls = 0
+        self._skipped = None                              # the last step's skip flag on its way to the host
 
         groups = (self.group_start, self.group_rows)
         self._up = L.make_grouped_args(self.xs, self.w13, self.h, *groups, epilogue=L.GROUPED_SWIGLU, pre=self.pre,
@@ -134,10 +136,27 @@ class ExpertLayer:
         return self.dx, self.dweights
 
     def step(self, lr, beta1=0.9, beta2=0.999, eps=1e-8, grad_scale=None, skip=None):
-        """One AdamW step of both weights from grads."""
+        """One AdamW step of both weights from grads.
+
+        skip [1] int32: where it is not 0 the step changes nothing and does not
+        count (the bias corrections follow ``steps``).  The flag reaches the host
+        behind the step; the next call waits for it, so that the host is at most
+        a step ahead.  In a captured graph lr, the step's number and the seed
+        would stay those of the capture: call it outside."""
+        if self._skipped is not None:
+            flag, copied = self._skipped
+            copied.synchronize()
+            self.steps -= 1 if int(flag) else 0
+            self._skipped = None
         self.steps += 1
+        self._calls += 1                                  # (each call's rounding has its own seed, skipped ones too)
         L.moe_adamw_step(L.make_adamw_args(self.table, lr=lr, step=self.steps, beta1=beta1, beta2=beta2, eps=eps,
-                                           seed=self.steps, grad_scale=grad_scale, skip=skip))
+                                           seed=self._calls, grad_scale=grad_scale, skip=skip))
+        if skip is not None:
+            flag, copied = torch.empty(1, dtype=torch.int32, pin_memory=True), torch.cuda.Event()
+            flag.copy_(skip.view(-1)[:1], non_blocking=True)
+            copied.record()
+            self._skipped = flag, copied
 
     def quantized(self):
         """The trained weights as the FP8 forward takes them: (w13 interleaved,

@@ -232,7 +232,7 @@ typedef struct moe_adamw_args {
   const float* grad_scale;     /* nullable [1] device scalar                              */
   const int32_t* skip;         /* nullable [1]: not 0: the step changes nothing           */
   int64_t chunks;              /* from moe_adamw_table_init                               */
-  int64_t step;                /* 1 for the first step                                    */
+  int64_t step;                /* 1 for the first step; one that `skip` left out does not count */
   double lr, beta1, beta2, eps; /* (1 - beta is formed in double, then rounded)           */
   uint32_t seed;               /* state bits 8                                            */
   int32_t count;
@@ -240,7 +240,9 @@ typedef struct moe_adamw_args {
   int32_t grad_types;          /* from moe_adamw_table_init                               */
 } moe_adamw_args;
 
-/* lr, eps >= 0 and finite; 0 <= beta1, beta2 < 1; step >= 1. */
+/* lr, eps >= 0 and finite; 0 <= beta1, beta2 < 1; step >= 1.  lr, step and seed
+ * are taken when the call is made: a captured graph repeats those of its capture
+ * (grad_scale and skip are read by the device). */
 moe_status moe_adamw_step(const moe_adamw_args* args, moe_stream_t stream);
 
 #ifdef __cplusplus

@@ -37,3 +37,25 @@ def test_a_route_masked_later_has_no_weight_gradient():
     _, dwt = layer.backward(x)
     live = layer.topk_ids >= 0
     assert (dwt[~live] == 0).all() and (dwt[live] != 0).all()
+
+
+def test_a_skipped_step_does_not_count():
+    """A skipped first step, then one from new gradients, is the same as that step alone."""
+    layers = [ExpertLayer(8, 64, 24, 3, 2, weight_decay=0.1, generator=gen(5)) for _ in range(2)]
+    flag = torch.ones(1, dtype=torch.int32, device="cuda")
+    for grad in layers[0].grads:
+        grad.copy_(torch.randn(grad.shape, device="cuda", generator=gen(6)))
+    layers[0].step(1e-2, skip=flag)
+    layers[0].step(1e-2, skip=flag)
+    for a, b in zip(layers[0].params, layers[1].params):
+        assert torch.equal(a, b)
+    for k in range(3):
+        for layer in layers:
+            for i, grad in enumerate(layer.grads):
+                grad.copy_(torch.randn(grad.shape, device="cuda", generator=gen(7 + 10 * k + i)))
+        flag.zero_()
+        layers[0].step(1e-2, skip=flag if k == 0 else None)
+        layers[1].step(1e-2)
+        for a, b in zip(layers[0].params + layers[0].models, layers[1].params + layers[1].models):
+            assert torch.equal(a, b), k
+    assert layers[0].steps == layers[1].steps == 3
