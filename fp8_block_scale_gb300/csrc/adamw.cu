@@ -37,6 +37,7 @@ struct AdamEntry {
   float weight_decay;
   int32_t grad_dtype;
   int32_t model_dtype;
+  int32_t state_bits;   // (a kernel for other states would write past this tensor's)
 };
 
 struct AdamParams {
@@ -224,9 +225,10 @@ __global__ void __launch_bounds__(kThreads) adamw32_kernel(const __grid_constant
   const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
   for (int64_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
     const AdamEntry t = a.table[find_entry(a, c)];
-    if (t.grad_dtype != kGrad) continue;
+    if (t.grad_dtype != kGrad || t.state_bits != 32) continue;
     const float decay = fmaf(-a.lr, t.weight_decay, 1.0f);
     const int64_t i0 = (c - t.first_chunk) * kChunk;
+    if (i0 >= t.n) return;   // (more chunks than the table has)
     adamw32_chunk<kGrad, kSmall>(a, t, decay, gs, i0);
     // the last one to three elements
     const int64_t k = (t.n & ~int64_t(3)) + threadIdx.x;
@@ -489,16 +491,18 @@ __global__ void __launch_bounds__(kThreads, 3) adamw8_kernel(const __grid_consta
     const int index = find_entry(a, c);
     const AdamEntry t = a.table[index];
     const int64_t past = t.first_chunk + (t.n + kChunk - 1) / kChunk;   // the tensor's chunks end here
+    if (c >= past) return;   // (more chunks than the table has)
     const float decay = fmaf(-a.lr, t.weight_decay, 1.0f);
     const uint32_t id = static_cast<uint32_t>(index);
     Group8 next[kSteps];
     int64_t group = (c - t.first_chunk) * (kChunk / 128) + warp;
-    if (t.grad_dtype == kGrad) {
+    const bool mine = t.grad_dtype == kGrad && t.state_bits == 8;
+    if (mine) {
 #pragma unroll
       for (int u = 0; u < kSteps; ++u) load_group8<kGrad>(t, group + u * kWarps, next[u]);
     }
     for (; c < past; c += gridDim.x) {
-      if (t.grad_dtype != kGrad) continue;
+      if (!mine) continue;
       Group8 x[kSteps];
 #pragma unroll
       for (int u = 0; u < kSteps; ++u) x[u] = next[u];
@@ -586,6 +590,7 @@ moe_status moe_adamw_table_init(const moe_adamw_tensor* tensors, int count, int 
     e.first_chunk = total;
     e.weight_decay = static_cast<float>(t.weight_decay);
     e.grad_dtype = t.grad_dtype;
+    e.state_bits = state_bits;
     e.model_dtype = t.model ? t.model_dtype : MOE_TYPE_BF16;
     total += ceil_div(t.n, kChunk);
     if (t.n > 0) types |= 1 << t.grad_dtype;

@@ -240,7 +240,8 @@ typedef struct moe_adamw_args {
   int32_t grad_types;          /* from moe_adamw_table_init                               */
 } moe_adamw_args;
 
-/* lr, eps >= 0 and finite; 0 <= beta1, beta2 < 1; step >= 1.  lr, step and seed
+/* A table of other state bits is left as it is, and chunks past the table's are
+ * none.  lr, eps >= 0 and finite; 0 <= beta1, beta2 < 1; step >= 1.  lr, step and seed
  * are taken when the call is made: a captured graph repeats those of its capture
  * (grad_scale and skip are read by the device). */
 moe_status moe_adamw_step(const moe_adamw_args* args, moe_stream_t stream);

@@ -150,3 +150,23 @@ def test_adamw8_codes_are_those_of_the_formula(grad, eps):
             assert (t[name + "_scale"].cpu().numpy() == scale).all(), (i, name)
             got = f64(t[name].float())
             assert (got == codes).all(), (i, name, int((got != codes).sum()))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_arguments_that_do_not_fit_the_table(bits):
+    """More chunks than the table has change nothing; other state bits leave the tensors as they are."""
+    ts = _tensors([3001, 0, 5000, 0], bits, F32, torch.bfloat16, gen(23))
+    copies = [[{k: v.clone() for k, v in t.items()} for t in ts] for _ in range(2)]
+    for more, group in ((0, ts), (5000, copies[0])):
+        args = L.make_adamw_args(L.AdamWTable(group), seed=1, **HYPER)
+        args.chunks += more
+        L.moe_adamw_step(args)
+    before = [{k: v.clone() for k, v in t.items()} for t in copies[1]]
+    args = L.make_adamw_args(L.AdamWTable(copies[1]), seed=1, **HYPER)
+    args.state_bits = 40 - bits
+    L.moe_adamw_step(args)
+    torch.cuda.synchronize()
+    for a, b, c, d in zip(ts, copies[0], copies[1], before):
+        for k in a:
+            assert torch.equal(a[k].view(torch.uint8), b[k].view(torch.uint8)), k
+            assert torch.equal(c[k].view(torch.uint8), d[k].view(torch.uint8)), k
