@@ -567,7 +567,8 @@ def moe_w4a8_forward(args, stream=None):
 # ---------------------------------------------------------------- training side (include/moe_train.h)
 #
 # Row buffers may be strided by rows (a slice of wider rows); their elements
-# are contiguous within a row.
+# are contiguous within a row.  An argument record keeps the tensors it was made
+# from.
 
 def _rows2d(name, t, dtype=None):
     """(pointer, row stride) of a 2D row buffer; ValueError if it is not one the library can read."""
@@ -671,6 +672,7 @@ def make_grouped_args(x, w, y, group_start, group_rows, input_gradient=False, ep
     args.device_status = _opt("device_status", device_status, torch.int32, 1)
     args.rows, args.R = rows, 0 if route_weights is None else route_weights.numel()
     args.E, args.N, args.K = E, N, K
+    args._keepalive = (x, w, y, group_start, group_rows, pre, route_ids, route_weights, device_status)
     args.dtype = TYPE_CODES[w.dtype]
     args.direction = GROUPED_INPUT_GRADIENT if input_gradient else GROUPED_FORWARD
     args.epilogue = epilogue
@@ -695,6 +697,7 @@ def make_grouped_wgrad_args(dy, x, dw, group_start, group_rows, accumulate=False
     args.group_rows = _dense("group_rows", group_rows, torch.int32, E)
     args.device_status = _opt("device_status", device_status, torch.int32, 1)
     args.rows, args.E, args.N, args.K = rows, E, N, K
+    args._keepalive = (dy, x, dw, group_start, group_rows, device_status)
     args.dtype, args.dw_dtype = TYPE_CODES[x.dtype], TYPE_CODES[dw.dtype]
     args.accumulate = 1 if accumulate else 0
     return args
@@ -725,6 +728,7 @@ def make_swiglu_backward_args(dh, pre, dpre, h=None, route_ids=None, num_rows=No
     args.dweights = _opt("dweights", dweights, torch.float32, need)
     # without either, every nonnegative id names a route
     args.R = min(by_route) if by_route else 2 ** 31 - 1
+    args._keepalive = (dh, pre, dpre, h, route_ids, num_rows, route_weights, dweights)
     args.rows, args.I, args.dtype = rows, I, TYPE_CODES[dh.dtype]
     return args
 

@@ -59,3 +59,32 @@ def test_layer_refuses_other_rows(layer, x):
         layer.forward(x)
     with pytest.raises(ValueError):
         layer.backward(x)
+
+
+def test_argument_records_keep_their_tensors(L):
+    """A temporary that only the record knows must live as long as the record."""
+    import gc
+    import weakref
+
+    bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    z = torch.zeros
+    records = [
+        (lambda *t: L.make_grouped_args(*t[:5], epilogue=L.GROUPED_SWIGLU, pre=t[5], route_ids=t[6], route_weights=t[7],
+                                        device_status=t[8]),
+         [z(6, 32, dtype=bf), z(2, 64, 32, dtype=bf), z(6, 32, dtype=bf), z(2, dtype=i32), z(2, dtype=i32), z(6, 64, dtype=bf),
+          z(6, dtype=i32), z(9, dtype=f32), z(1, dtype=i32)]),
+        (lambda *t: L.make_grouped_wgrad_args(*t[:5], device_status=t[5]),
+         [z(6, 64, dtype=bf), z(6, 32, dtype=bf), z(2, 64, 32), z(2, dtype=i32), z(2, dtype=i32), z(1, dtype=i32)]),
+        (lambda *t: L.make_swiglu_backward_args(*t[:3], h=t[3], route_ids=t[4], num_rows=t[5], route_weights=t[6], dweights=t[7]),
+         [z(6, 32, dtype=bf), z(6, 64, dtype=bf), z(6, 64, dtype=bf), z(6, 32, dtype=bf), z(6, dtype=i32), z(1, dtype=i32), z(9), z(9)]),
+    ]
+    while records:
+        make, tensors = records.pop()
+        args = make(*tensors)
+        refs = [weakref.ref(t) for t in tensors]
+        del tensors
+        gc.collect()
+        assert all(r() is not None for r in refs)
+        del args
+        gc.collect()
+        assert all(r() is None for r in refs)
