@@ -343,11 +343,16 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream=None):
+def _current_stream():
     # (the raw handle: building a torch.cuda.Stream costs 3 us a call on the Grace host)
-    if stream is None:
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
-    return ctypes.c_void_p(stream.cuda_stream)
+    try:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    except AttributeError:   # a torch without these names
+        return torch.cuda.current_stream().cuda_stream
+
+
+def _stream(stream=None):
+    return ctypes.c_void_p(_current_stream() if stream is None else stream.cuda_stream)
 
 
 def _check(fn, status):

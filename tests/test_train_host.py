@@ -88,3 +88,18 @@ def test_argument_records_keep_their_tensors(L):
         del args
         gc.collect()
         assert all(r() is None for r in refs)
+
+
+def test_current_stream_without_torchs_raw_lookups(L, monkeypatch):
+    class Stream:
+        cuda_stream = 0x1234
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream)
+    for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+        with monkeypatch.context() as m:
+            m.delattr(torch._C, name, raising=False)
+            assert L._stream().value == 0x1234
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 3, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 0x100 + d, raising=False)
+    assert L._stream().value == 0x103
+    assert L._stream(Stream).value == 0x1234
