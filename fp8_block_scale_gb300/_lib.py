@@ -575,21 +575,21 @@ def moe_w4a8_forward(args, stream=None):
 # are contiguous within a row.  An argument record keeps the tensors it was made
 # from.
 
-def _rows2d(name, t, dtype=None):
-    """(pointer, row stride) of a 2D row buffer; ValueError if it is not one the library can read."""
-    if t.dim() != 2 or t.stride(1) != 1:
-        raise ValueError(f"{name}: a 2D tensor with contiguous rows is expected")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    return t.data_ptr(), t.stride(0)
-
-
 def _row_buffer(name, t):
-    """(rows, width, row stride) of a 2D row buffer."""
+    """(rows, width, row stride) of a 2D row buffer; ValueError if it is not one the library can read."""
     shape, stride = t.shape, t.stride()
     if len(shape) != 2 or stride[1] != 1:
         raise ValueError(f"{name}: a 2D tensor with contiguous rows is expected")
-    return shape[0], shape[1], stride[0]
+    # (torch gives a single row any stride: no second row follows from it)
+    return shape[0], shape[1], stride[0] if shape[0] > 1 else shape[1]
+
+
+def _rows2d(name, t, dtype=None):
+    """(pointer, row stride) of a 2D row buffer."""
+    ld = _row_buffer(name, t)[2]
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    return t.data_ptr(), ld
 
 
 def _dense(name, t, dtype=None, numel=None):

@@ -103,3 +103,19 @@ def test_current_stream_without_torchs_raw_lookups(L, monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 0x100 + d, raising=False)
     assert L._stream().value == 0x103
     assert L._stream(Stream).value == 0x1234
+
+
+def test_a_single_row_may_have_any_stride(L):
+    """torch calls a transposed column [1, n] contiguous with a row stride of 1."""
+    bf = torch.bfloat16
+    one = torch.zeros(32, 1, dtype=bf).t()
+    assert one.shape == (1, 32) and one.stride() == (1, 1) and one.is_contiguous()
+    w, y, s = torch.zeros(2, 64, 32, dtype=bf), torch.zeros(64, 1, dtype=bf).t(), torch.zeros(2, dtype=torch.int32)
+    args = L.make_grouped_args(one, w, y, s, s)
+    assert (args.ldx, args.ldy) == (32, 64)
+    args = L.make_grouped_wgrad_args(y, one, torch.zeros_like(w), s, s)
+    assert (args.lddy, args.ldx) == (64, 32)
+    args = L.make_swiglu_backward_args(one, y, torch.zeros(1, 64, dtype=bf), h=torch.zeros(32, 1, dtype=bf).t())
+    assert (args.lddh, args.ldpre, args.lddpre, args.ldh) == (32, 64, 64, 32)
+    with pytest.raises(ValueError):
+        L.make_grouped_args(torch.zeros(32, 2, dtype=bf).t(), w, torch.zeros(2, 64, dtype=bf), s, s)
