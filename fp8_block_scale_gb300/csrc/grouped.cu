@@ -1121,10 +1121,9 @@ moe_status moe_grouped_gemm(const moe_grouped_args* a, moe_stream_t stream) {
   if (a->rows == 0) return MOE_OK;
   if (!a->x || !a->w || !a->y || !a->group_start || !a->group_rows) return MOE_ERR_NULL;
   if (!aligned16(a->x) || !aligned16(a->w) || !aligned16(a->y) || (pre && !aligned16(a->pre))) return MOE_ERR_ALIGN;
-  const int64_t bx = extent_bytes(a->rows, a->ldx, in, 2), by = extent_bytes(a->rows, a->ldy, out, 2);
-  const int64_t bw = 2ll * a->E * a->N * a->K, bp = pre ? extent_bytes(a->rows, a->ldpre, a->N, 2) : 0;
-  if (overlap(a->y, by, a->x, bx) || overlap(a->y, by, a->w, bw) || overlap(a->pre, bp, a->x, bx) ||
-      overlap(a->pre, bp, a->w, bw) || overlap(a->pre, bp, a->y, by))
+  const Rows rx{a->x, a->rows, a->ldx, in}, ry{a->y, a->rows, a->ldy, out}, rp{a->pre, pre ? a->rows : 0, a->ldpre, a->N};
+  const Rows rw{a->w, 1, 0, static_cast<int64_t>(a->E) * a->N * a->K};   // (one row)
+  if (overlap(ry, rx, 2) || overlap(ry, rw, 2) || overlap(rp, rx, 2) || overlap(rp, rw, 2) || overlap(rp, ry, 2))
     return MOE_ERR_SHAPE;
   DeviceInfo dev;
   if (current_device(&dev) != MOE_OK) return MOE_ERR_CUDA;

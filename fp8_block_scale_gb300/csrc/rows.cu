@@ -265,7 +265,7 @@ moe_status moe_gather_rows(const void* x, int64_t M, int width, int64_t ldx, voi
   if (rows == 0) return MOE_OK;
   if ((M > 0 && !x) || !xs || !route_ids) return MOE_ERR_NULL;   // (without tokens every row becomes zero)
   if (!aligned16(x) || !aligned16(xs)) return MOE_ERR_ALIGN;
-  if (overlap(x, extent_bytes(M, ldx, width, eb), xs, extent_bytes(rows, ldxs, width, eb))) return MOE_ERR_SHAPE;
+  if (overlap(Rows{x, M, ldx, width}, Rows{xs, rows, ldxs, width}, eb)) return MOE_ERR_SHAPE;
   DeviceInfo dev;
   if (current_device(&dev) != MOE_OK) return MOE_ERR_CUDA;
   const void* ptrs[] = {x, xs, route_ids, num_rows};
@@ -288,7 +288,7 @@ moe_status moe_sum_routes(const void* y, int64_t rows, int width, int64_t ldy, v
   if (M == 0) return MOE_OK;
   if ((rows > 0 && !y) || !out || !route_slot) return MOE_ERR_NULL;   // (without rows every sum is empty)
   if (!aligned16(y) || !aligned16(out)) return MOE_ERR_ALIGN;
-  if (overlap(y, extent_bytes(rows, ldy, width, eb), out, extent_bytes(M, ldout, width, eb))) return MOE_ERR_SHAPE;
+  if (overlap(Rows{y, rows, ldy, width}, Rows{out, M, ldout, width}, eb)) return MOE_ERR_SHAPE;
   DeviceInfo dev;
   if (current_device(&dev) != MOE_OK) return MOE_ERR_CUDA;
   const void* ptrs[] = {y, out, route_slot};
@@ -319,13 +319,11 @@ moe_status moe_swiglu_backward(const moe_swiglu_backward_args* a, moe_stream_t s
   if (!a->dh || !a->pre || !a->dpre) return MOE_ERR_NULL;
   if (!aligned16(a->dh) || !aligned16(a->pre) || !aligned16(a->dpre) || !aligned16(a->h)) return MOE_ERR_ALIGN;
   // in place only element by element: the same rows at the same stride
-  const int64_t bdh = extent_bytes(a->rows, a->lddh, I, 2), bpre = extent_bytes(a->rows, a->ldpre, 2 * I, 2);
-  const int64_t bdp = extent_bytes(a->rows, a->lddpre, 2 * I, 2);
-  const int64_t bh = a->h ? extent_bytes(a->rows, a->ldh, I, 2) : 0;
+  const Rows dh{a->dh, a->rows, a->lddh, I}, pre{a->pre, a->rows, a->ldpre, 2 * I};
+  const Rows dpre{a->dpre, a->rows, a->lddpre, 2 * I}, h{a->h, a->h ? a->rows : 0, a->ldh, I};
   const bool pre_in_place = a->dpre == a->pre && a->lddpre == a->ldpre, h_in_place = a->h == a->dh && a->ldh == a->lddh;
-  if ((!pre_in_place && overlap(a->dpre, bdp, a->pre, bpre)) || overlap(a->dpre, bdp, a->dh, bdh) ||
-      overlap(a->h, bh, a->dpre, bdp) || overlap(a->h, bh, a->pre, bpre) ||
-      (!h_in_place && overlap(a->h, bh, a->dh, bdh)))
+  if ((!pre_in_place && overlap(dpre, pre, 2)) || overlap(dpre, dh, 2) || overlap(h, dpre, 2) || overlap(h, pre, 2) ||
+      (!h_in_place && overlap(h, dh, 2)))
     return MOE_ERR_SHAPE;
   DeviceInfo dev;
   if (current_device(&dev) != MOE_OK) return MOE_ERR_CUDA;

@@ -21,6 +21,22 @@ inline int64_t extent_bytes(int64_t rows, int64_t ld, int64_t width, int elem) {
   return rows > 0 ? ((rows - 1) * ld + width) * elem : 0;
 }
 
+// A row buffer: `width` elements of each row, the next row `ld` further on.
+struct Rows {
+  const void* p;
+  int64_t rows, ld, width;
+};
+// Whether two of them share a byte.  Buffers of one row stride may lie beside one
+// another as columns of a wider one; of different strides they may not interleave.
+inline bool overlap(const Rows& a, const Rows& b, int elem) {
+  if (!overlap(a.p, extent_bytes(a.rows, a.ld, a.width, elem), b.p, extent_bytes(b.rows, b.ld, b.width, elem))) return false;
+  const int64_t ld = a.rows > 1 ? a.ld : b.ld, period = ld * elem;
+  if ((b.rows > 1 && b.ld != ld) || period <= 0) return true;
+  int64_t at = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)) % period;
+  if (at < 0) at += period;
+  return at < a.width * elem || at + b.width * elem > period;
+}
+
 template <typename T> struct Pack2;
 template <> struct Pack2<__nv_bfloat16> {
   static __device__ __forceinline__ float2 load(uint32_t v) {

@@ -16,6 +16,9 @@
  * Plan order: rows of an expert are contiguous "slots" of a row buffer.  The
  * layout moe_plan makes is one such order (moe_plan_groups reads it); any
  * other is described by group_start and group_rows directly.
+ *
+ * Where buffers must not overlap, row buffers of one row stride may be columns of
+ * one wider buffer; rows of different strides must not interleave.
  */
 #ifndef MOE_TRAIN_H
 #define MOE_TRAIN_H

@@ -37,3 +37,37 @@ def test_single_rows_of_any_stride():
         assert torch.equal(xs, dense) and torch.equal(out, dense) and (y != 0).any()
         outs.append((y.clone(), dx.clone(), dw))
     assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
+def test_columns_of_one_buffer():
+    """Inputs and outputs side by side in wider rows: the results of separate buffers."""
+    g = gen(4)
+    n, I, K = 300, 64, 64
+    a = torch.randn(n, 3 * I, device="cuda", generator=g).to(BF16)
+    outs = []
+    for beside in (False, True):
+        wide = torch.zeros(n, 8 * I, dtype=BF16, device="cuda")
+        place = iter(range(0, 8 * I, I))
+
+        def new(width, fill=None):
+            if beside:
+                at = [next(place) for _ in range(width // I)][0]
+                t = wide[:, at:at + width]
+            else:
+                t = torch.zeros(n, width, dtype=BF16, device="cuda")
+            return t if fill is None else t.copy_(fill)
+
+        s = torch.tensor([0, 100], dtype=torch.int32, device="cuda")
+        r = torch.tensor([100, 200], dtype=torch.int32, device="cuda")
+        w = torch.randn(2, 2 * I, K, device="cuda", generator=gen(5)).to(BF16)
+        x, pre, h, dpre, dh = new(K, a[:, :K]), new(2 * I), new(I), new(2 * I), new(I, a[:, K:2 * K])
+        L.moe_grouped_gemm(L.make_grouped_args(x, w, h, s, r, epilogue=L.GROUPED_SWIGLU, pre=pre))
+        first = h.clone()
+        L.moe_swiglu_backward(L.make_swiglu_backward_args(dh, pre, dpre, h=h))
+        ids = torch.arange(n, dtype=torch.int32, device="cuda").flip(0).contiguous()
+        xs = new(I)
+        L.moe_gather_rows(dh, xs, ids, 1)
+        L.moe_sum_routes(xs, x, ids, 1)
+        outs.append([t.clone() for t in (first, pre, h, dpre, xs, x)])
+    assert all(torch.equal(p, q) for p, q in zip(*outs))
+    assert torch.equal(outs[0][5], a[:, K:2 * K]) and (outs[0][3] != 0).any()

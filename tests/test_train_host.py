@@ -119,3 +119,43 @@ def test_a_single_row_may_have_any_stride(L):
     assert (args.lddh, args.ldpre, args.lddpre, args.ldh) == (32, 64, 64, 32)
     with pytest.raises(ValueError):
         L.make_grouped_args(torch.zeros(32, 2, dtype=bf).t(), w, torch.zeros(2, 64, dtype=bf), s, s)
+
+
+def test_columns_beside_one_another_do_not_overlap(L):
+    """Outputs and inputs may be columns of one wider buffer; columns that share an element may not."""
+    SHAPE, bf, i32 = 2, torch.bfloat16, torch.int32
+    lib = L.load()
+    buf, s = torch.zeros(20, 256, dtype=bf), torch.zeros(2, dtype=i32)
+    cols = lambda a, n: buf[:, a:a + n]                                              # noqa: E731
+    w = torch.zeros(2, 64, 32, dtype=bf)
+
+    def status(make, call, *a, **kw):
+        args = make(*a, **kw)
+        return getattr(lib, call)(args, None)
+
+    def gemm(x, y, **kw):
+        return status(L.make_grouped_args, "moe_grouped_gemm", x, w, y, s, s, **kw)
+
+    def back(*a, **kw):
+        return status(L.make_swiglu_backward_args, "moe_swiglu_backward", *a, **kw)
+
+    # (without a device the calls end there; what counts is that their sizes are not refused)
+    glu = dict(epilogue=L.GROUPED_SWIGLU)
+    assert gemm(cols(0, 32), cols(32, 64)) != SHAPE and gemm(cols(0, 32), cols(24, 64)) == SHAPE
+    assert gemm(cols(64, 32), cols(0, 64)) != SHAPE and gemm(cols(56, 32), cols(0, 64)) == SHAPE
+    assert gemm(cols(128, 32), cols(160, 32), pre=cols(0, 64), **glu) != SHAPE
+    assert gemm(cols(128, 32), cols(160, 32), pre=cols(104, 64), **glu) == SHAPE
+    assert gemm(cols(128, 32), cols(160, 32), pre=cols(176, 64), **glu) == SHAPE
+    # rows from one on: the end of a row and the start of the next are neighbours too
+    assert gemm(buf.view(-1)[128:128 + 19 * 256].view(19, 256)[:, :32], buf[:19, 0:64]) != SHAPE
+    assert gemm(buf.view(-1)[240:240 + 19 * 256].view(19, 256)[:, :32], buf[:19, 0:64]) == SHAPE
+    # another stride cannot be told apart
+    assert gemm(buf.view(40, 128)[:20, :32], cols(64, 64)) == SHAPE
+    assert back(cols(0, 32), cols(32, 64), cols(96, 64), h=cols(160, 32)) != SHAPE
+    assert back(cols(0, 32), cols(32, 64), cols(88, 64), h=cols(160, 32)) == SHAPE
+    assert back(cols(0, 32), cols(32, 64), cols(96, 64), h=cols(152, 32)) == SHAPE
+    assert back(cols(0, 32), cols(32, 64), cols(32, 64), h=cols(0, 32)) != SHAPE      # in place
+    rows = lambda f, a, b: getattr(lib, f)(                                          # noqa: E731
+        a.data_ptr(), 20, 64, 256, b.data_ptr(), 20, 256, s.data_ptr(), *((1, None) if "gather" in f else (1, 0)), 0, None)
+    for f in ("moe_gather_rows", "moe_sum_routes"):
+        assert rows(f, cols(0, 64), cols(64, 64)) != SHAPE and rows(f, cols(0, 64), cols(56, 64)) == SHAPE
