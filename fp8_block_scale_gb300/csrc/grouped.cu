@@ -1098,8 +1098,10 @@ bool window_map(CUtensorMap* m, int dtype, const void* base, int64_t width, int6
 }
 
 bool ok_sizes(int64_t rows, int E, int N, int K) {
-  return rows >= 0 && rows < (int64_t(1) << 31) && E >= 1 && E <= 2048 && N >= 8 && N % 8 == 0 && K >= 8 && K % 8 == 0;
+  return rows >= 0 && rows < (int64_t(1) << 31) && E >= 1 && E <= 2048 && N >= 8 && N % 8 == 0 && K >= 8 && K % 8 == 0 &&
+         static_cast<int64_t>(N) * K <= kMostElements / E;
 }
+bool ok_stride(int64_t ld, int64_t width) { return ld % 8 == 0 && ld >= width && ld <= kMostElements; }
 
 }  // namespace
 }  // namespace moe
@@ -1116,8 +1118,7 @@ moe_status moe_grouped_gemm(const moe_grouped_args* a, moe_stream_t stream) {
     return MOE_ERR_SHAPE;
   const int64_t in = fwd ? a->K : a->N, out = fwd ? (glu ? a->N / 2 : a->N) : a->K;
   const bool pre = glu && a->pre;
-  if (a->ldx % 8 || a->ldx < in || a->ldy % 8 || a->ldy < out || (pre && (a->ldpre % 8 || a->ldpre < a->N)))
-    return MOE_ERR_SHAPE;
+  if (!ok_stride(a->ldx, in) || !ok_stride(a->ldy, out) || (pre && !ok_stride(a->ldpre, a->N))) return MOE_ERR_SHAPE;
   if (a->rows == 0) return MOE_OK;
   if (!a->x || !a->w || !a->y || !a->group_start || !a->group_rows) return MOE_ERR_NULL;
   if (!aligned16(a->x) || !aligned16(a->w) || !aligned16(a->y) || (pre && !aligned16(a->pre))) return MOE_ERR_ALIGN;
@@ -1198,8 +1199,7 @@ moe_status moe_grouped_wgrad(const moe_grouped_wgrad_args* a, moe_stream_t strea
   if (!a) return MOE_ERR_NULL;
   if (!is_half_type(a->dtype) || (a->dw_dtype != a->dtype && a->dw_dtype != MOE_TYPE_FP32)) return MOE_ERR_DTYPE;
   if (a->accumulate && a->dw_dtype != MOE_TYPE_FP32) return MOE_ERR_DTYPE;
-  if (!ok_sizes(a->rows, a->E, a->N, a->K) || a->lddy % 8 || a->ldx % 8 || a->lddy < a->N || a->ldx < a->K)
-    return MOE_ERR_SHAPE;
+  if (!ok_sizes(a->rows, a->E, a->N, a->K) || !ok_stride(a->lddy, a->N) || !ok_stride(a->ldx, a->K)) return MOE_ERR_SHAPE;
   if (!a->dw || !a->group_start || !a->group_rows || (a->rows > 0 && (!a->dy || !a->x))) return MOE_ERR_NULL;
   if (!aligned16(a->dy) || !aligned16(a->x) || !aligned16(a->dw)) return MOE_ERR_ALIGN;
   const int64_t bd = static_cast<int64_t>(type_bytes(a->dw_dtype)) * a->E * a->N * a->K;

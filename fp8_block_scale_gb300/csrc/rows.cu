@@ -259,8 +259,8 @@ moe_status moe_gather_rows(const void* x, int64_t M, int width, int64_t ldx, voi
   using namespace moe;
   if (!is_type(dtype)) return MOE_ERR_DTYPE;
   const int eb = type_bytes(dtype), vec = 16 / eb;
-  if (M < 0 || rows < 0 || rows >= (int64_t(1) << 31) || M * top_k >= (int64_t(1) << 31) || top_k < 1 || width < vec ||
-      width % vec || ldx % vec || ldxs % vec || ldx < width || ldxs < width)
+  if (!ok_routes(M, top_k) || rows < 0 || rows >= (int64_t(1) << 31) || width < vec || width % vec || ldx % vec ||
+      ldxs % vec || ldx < width || ldxs < width || ldx > kMostElements || ldxs > kMostElements)
     return MOE_ERR_SHAPE;
   if (rows == 0) return MOE_OK;
   if ((M > 0 && !x) || !xs || !route_ids) return MOE_ERR_NULL;   // (without tokens every row becomes zero)
@@ -282,8 +282,8 @@ moe_status moe_sum_routes(const void* y, int64_t rows, int width, int64_t ldy, v
   using namespace moe;
   if (!is_type(dtype)) return MOE_ERR_DTYPE;
   const int eb = type_bytes(dtype), vec = 16 / eb;
-  if (M < 0 || rows < 0 || rows >= (int64_t(1) << 31) || top_k < 1 || M * top_k >= (int64_t(1) << 31) || width < vec ||
-      width % vec || ldy % vec || ldout % vec || ldy < width || ldout < width)
+  if (!ok_routes(M, top_k) || rows < 0 || rows >= (int64_t(1) << 31) || width < vec || width % vec || ldy % vec ||
+      ldout % vec || ldy < width || ldout < width || ldy > kMostElements || ldout > kMostElements)
     return MOE_ERR_SHAPE;
   if (M == 0) return MOE_OK;
   if ((rows > 0 && !y) || !out || !route_slot) return MOE_ERR_NULL;   // (without rows every sum is empty)
@@ -312,8 +312,9 @@ moe_status moe_swiglu_backward(const moe_swiglu_backward_args* a, moe_stream_t s
   if (!is_half_type(a->dtype)) return MOE_ERR_DTYPE;
   const int64_t I = a->I;
   if (a->rows < 0 || a->rows >= (int64_t(1) << 31) || a->R < 0 || I < 8 || I % 8 || a->lddh % 8 || a->ldpre % 8 ||
-      a->lddpre % 8 || a->lddh < I || a->ldpre < 2 * I || a->lddpre < 2 * I ||
-      (a->h && (a->ldh % 8 || a->ldh < I)))
+      a->lddpre % 8 || a->lddh < I || a->ldpre < 2 * I || a->lddpre < 2 * I || a->lddh > kMostElements ||
+      a->ldpre > kMostElements || a->lddpre > kMostElements ||
+      (a->h && (a->ldh % 8 || a->ldh < I || a->ldh > kMostElements)))
     return MOE_ERR_SHAPE;
   if (a->rows == 0) return MOE_OK;
   if (!a->dh || !a->pre || !a->dpre) return MOE_ERR_NULL;

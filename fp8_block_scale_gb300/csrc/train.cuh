@@ -11,6 +11,13 @@ inline bool is_half_type(int dtype) { return dtype == MOE_TYPE_BF16 || dtype == 
 inline bool is_type(int dtype) { return is_half_type(dtype) || dtype == MOE_TYPE_FP32; }
 inline int type_bytes(int dtype) { return dtype == MOE_TYPE_FP32 ? 4 : 2; }
 
+// More elements than any buffer has: products of sizes below it fit 64 bits.
+constexpr int64_t kMostElements = int64_t(1) << 40;
+// M * top_k route ids of 32 bits.
+inline bool ok_routes(int64_t M, int top_k) {
+  return M >= 0 && M < (int64_t(1) << 31) && top_k >= 1 && M * top_k < (int64_t(1) << 31);
+}
+
 // Whether the byte ranges [a, a + na) and [b, b + nb) share a byte.
 inline bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
   const auto x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);

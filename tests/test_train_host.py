@@ -159,3 +159,29 @@ def test_columns_beside_one_another_do_not_overlap(L):
         a.data_ptr(), 20, 64, 256, b.data_ptr(), 20, 256, s.data_ptr(), *((1, None) if "gather" in f else (1, 0)), 0, None)
     for f in ("moe_gather_rows", "moe_sum_routes"):
         assert rows(f, cols(0, 64), cols(64, 64)) != SHAPE and rows(f, cols(0, 64), cols(56, 64)) == SHAPE
+
+
+def test_sizes_whose_products_pass_64_bits_are_refused(L):
+    import ctypes
+
+    SHAPE, p, lib = 2, ctypes.c_void_p, L.load()
+    for M, k in ((1 << 33, 1 << 30), (1 << 34, 1 << 29), (1 << 32, 1), (1 << 40, 1 << 24), (1 << 62, 4)):
+        assert lib.moe_gather_rows(p(1 << 20), M, 64, 64, p(2 << 20), 20, 64, p(3 << 20), k, None, 0, None) == SHAPE, (M, k)
+        assert lib.moe_sum_routes(p(1 << 20), 20, 64, 64, p(2 << 20), M, 64, p(3 << 20), k, 0, 0, None) == SHAPE, (M, k)
+    far = 1 << 62
+    assert lib.moe_gather_rows(p(1 << 20), 5, 64, far, p(2 << 20), 20, 64, p(3 << 20), 1, None, 0, None) == SHAPE
+    assert lib.moe_sum_routes(p(1 << 20), 20, 64, 64, p(2 << 20), 5, far, p(3 << 20), 1, 0, 0, None) == SHAPE
+    a = L.MoeGroupedArgs()
+    a.x, a.w, a.y, a.group_start, a.group_rows = 1 << 20, 2 << 20, 4 << 20, 8 << 20, 9 << 20
+    a.rows, a.E, a.N, a.K, a.ldx, a.ldy = 100, 4, 64, 32, far, 64
+    assert lib.moe_grouped_gemm(ctypes.byref(a), None) == SHAPE
+    a.ldx, a.E, a.N, a.K = 1 << 30, 2048, 1 << 30, 1 << 30
+    a.ldy = 1 << 30
+    assert lib.moe_grouped_gemm(ctypes.byref(a), None) == SHAPE
+    b = L.MoeGroupedWgradArgs()
+    b.dy, b.x, b.dw, b.group_start, b.group_rows = 1 << 20, 2 << 20, 4 << 20, 8 << 20, 9 << 20
+    b.rows, b.E, b.N, b.K, b.lddy, b.ldx = 100, 2048, 1 << 30, 1 << 30, 1 << 30, 1 << 30
+    assert lib.moe_grouped_wgrad(ctypes.byref(b), None) == SHAPE
+    c = L.MoeSwigluBackwardArgs()
+    c.dh, c.pre, c.dpre, c.rows, c.I, c.lddh, c.ldpre, c.lddpre = 1 << 20, 2 << 20, 4 << 20, 100, 64, far, 128, 128
+    assert lib.moe_swiglu_backward(ctypes.byref(c), None) == SHAPE
