@@ -574,8 +574,7 @@ moe_status moe_adamw_table_init(const moe_adamw_tensor* tensors, int count, int 
       if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq) return MOE_ERR_NULL;
       if (state_bits == 8 && (!t.exp_avg_scale || !t.exp_avg_sq_scale)) return MOE_ERR_NULL;
       if (!aligned16(t.param) || !aligned16(t.model) || !aligned16(t.grad) || !aligned16(t.exp_avg) ||
-          !aligned16(t.exp_avg_sq) || (reinterpret_cast<uintptr_t>(t.exp_avg_scale) & 3u) ||
-          (reinterpret_cast<uintptr_t>(t.exp_avg_sq_scale) & 3u))
+          !aligned16(t.exp_avg_sq) || !aligned4(t.exp_avg_scale, t.exp_avg_sq_scale))
         return MOE_ERR_ALIGN;
     }
     AdamEntry& e = host[static_cast<size_t>(i)];
@@ -623,6 +622,7 @@ moe_status moe_adamw_step(const moe_adamw_args* g, moe_stream_t stream) {
       !(g->beta2 >= 0 && g->beta2 < 1))
     return MOE_ERR_SHAPE;
   if (!g->table) return MOE_ERR_NULL;
+  if (!aligned16(g->table) || !aligned4(g->grad_scale, g->skip)) return MOE_ERR_ALIGN;
   if (g->chunks == 0) return MOE_OK;
   DeviceInfo dev;
   if (current_device(&dev) != MOE_OK) return MOE_ERR_CUDA;

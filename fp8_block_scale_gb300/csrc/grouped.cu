@@ -1121,7 +1121,9 @@ moe_status moe_grouped_gemm(const moe_grouped_args* a, moe_stream_t stream) {
   if (!ok_stride(a->ldx, in) || !ok_stride(a->ldy, out) || (pre && !ok_stride(a->ldpre, a->N))) return MOE_ERR_SHAPE;
   if (a->rows == 0) return MOE_OK;
   if (!a->x || !a->w || !a->y || !a->group_start || !a->group_rows) return MOE_ERR_NULL;
-  if (!aligned16(a->x) || !aligned16(a->w) || !aligned16(a->y) || (pre && !aligned16(a->pre))) return MOE_ERR_ALIGN;
+  if (!aligned16(a->x) || !aligned16(a->w) || !aligned16(a->y) || (pre && !aligned16(a->pre)) ||
+      !aligned4(a->group_start, a->group_rows, a->device_status) || (glu && !aligned4(a->route_ids, a->route_weights)))
+    return MOE_ERR_ALIGN;
   const Rows rx{a->x, a->rows, a->ldx, in}, ry{a->y, a->rows, a->ldy, out}, rp{a->pre, pre ? a->rows : 0, a->ldpre, a->N};
   const Rows rw{a->w, 1, 0, static_cast<int64_t>(a->E) * a->N * a->K};   // (one row)
   if (overlap(ry, rx, 2) || overlap(ry, rw, 2) || overlap(rp, rx, 2) || overlap(rp, rw, 2) || overlap(rp, ry, 2))
@@ -1201,7 +1203,9 @@ moe_status moe_grouped_wgrad(const moe_grouped_wgrad_args* a, moe_stream_t strea
   if (a->accumulate && a->dw_dtype != MOE_TYPE_FP32) return MOE_ERR_DTYPE;
   if (!ok_sizes(a->rows, a->E, a->N, a->K) || !ok_stride(a->lddy, a->N) || !ok_stride(a->ldx, a->K)) return MOE_ERR_SHAPE;
   if (!a->dw || !a->group_start || !a->group_rows || (a->rows > 0 && (!a->dy || !a->x))) return MOE_ERR_NULL;
-  if (!aligned16(a->dy) || !aligned16(a->x) || !aligned16(a->dw)) return MOE_ERR_ALIGN;
+  if (!aligned16(a->dy) || !aligned16(a->x) || !aligned16(a->dw) ||
+      !aligned4(a->group_start, a->group_rows, a->device_status))
+    return MOE_ERR_ALIGN;
   const int64_t bd = static_cast<int64_t>(type_bytes(a->dw_dtype)) * a->E * a->N * a->K;
   if (overlap(a->dw, bd, a->dy, extent_bytes(a->rows, a->lddy, a->N, 2)) ||
       overlap(a->dw, bd, a->x, extent_bytes(a->rows, a->ldx, a->K, 2)))

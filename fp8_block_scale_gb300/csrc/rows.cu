@@ -237,6 +237,8 @@ moe_status moe_plan_groups(const int32_t* sorted_token_ids, int64_t sorted_cap, 
   if (blocks_cap > (int64_t(1) << 31) / block_m || sorted_cap < blocks_cap * block_m) return MOE_ERR_CAPACITY;
   if (!num_tokens_post_padded || !group_start || !group_rows || (blocks_cap > 0 && (!sorted_token_ids || !expert_ids)))
     return MOE_ERR_NULL;
+  if (!aligned4(sorted_token_ids, expert_ids, num_tokens_post_padded, group_start, group_rows, route_slot))
+    return MOE_ERR_ALIGN;
   DeviceInfo dev;
   if (current_device(&dev) != MOE_OK) return MOE_ERR_CUDA;
   const void* ptrs[] = {sorted_token_ids, expert_ids, num_tokens_post_padded, group_start, group_rows, route_slot};
@@ -264,7 +266,7 @@ moe_status moe_gather_rows(const void* x, int64_t M, int width, int64_t ldx, voi
     return MOE_ERR_SHAPE;
   if (rows == 0) return MOE_OK;
   if ((M > 0 && !x) || !xs || !route_ids) return MOE_ERR_NULL;   // (without tokens every row becomes zero)
-  if (!aligned16(x) || !aligned16(xs)) return MOE_ERR_ALIGN;
+  if (!aligned16(x) || !aligned16(xs) || !aligned4(route_ids, num_rows)) return MOE_ERR_ALIGN;
   if (overlap(Rows{x, M, ldx, width}, Rows{xs, rows, ldxs, width}, eb)) return MOE_ERR_SHAPE;
   DeviceInfo dev;
   if (current_device(&dev) != MOE_OK) return MOE_ERR_CUDA;
@@ -287,7 +289,7 @@ moe_status moe_sum_routes(const void* y, int64_t rows, int width, int64_t ldy, v
     return MOE_ERR_SHAPE;
   if (M == 0) return MOE_OK;
   if ((rows > 0 && !y) || !out || !route_slot) return MOE_ERR_NULL;   // (without rows every sum is empty)
-  if (!aligned16(y) || !aligned16(out)) return MOE_ERR_ALIGN;
+  if (!aligned16(y) || !aligned16(out) || !aligned4(route_slot)) return MOE_ERR_ALIGN;
   if (overlap(Rows{y, rows, ldy, width}, Rows{out, M, ldout, width}, eb)) return MOE_ERR_SHAPE;
   DeviceInfo dev;
   if (current_device(&dev) != MOE_OK) return MOE_ERR_CUDA;
@@ -318,7 +320,9 @@ moe_status moe_swiglu_backward(const moe_swiglu_backward_args* a, moe_stream_t s
     return MOE_ERR_SHAPE;
   if (a->rows == 0) return MOE_OK;
   if (!a->dh || !a->pre || !a->dpre) return MOE_ERR_NULL;
-  if (!aligned16(a->dh) || !aligned16(a->pre) || !aligned16(a->dpre) || !aligned16(a->h)) return MOE_ERR_ALIGN;
+  if (!aligned16(a->dh) || !aligned16(a->pre) || !aligned16(a->dpre) || !aligned16(a->h) ||
+      !aligned4(a->route_ids, a->num_rows, a->route_weights, a->dweights))
+    return MOE_ERR_ALIGN;
   // in place only element by element: the same rows at the same stride
   const Rows dh{a->dh, a->rows, a->lddh, I}, pre{a->pre, a->rows, a->ldpre, 2 * I};
   const Rows dpre{a->dpre, a->rows, a->lddpre, 2 * I}, h{a->h, a->h ? a->rows : 0, a->ldh, I};

@@ -11,6 +11,12 @@ inline bool is_half_type(int dtype) { return dtype == MOE_TYPE_BF16 || dtype == 
 inline bool is_type(int dtype) { return is_half_type(dtype) || dtype == MOE_TYPE_FP32; }
 inline int type_bytes(int dtype) { return dtype == MOE_TYPE_FP32 ? 4 : 2; }
 
+// Whether pointers to 4-byte elements (tables, ids, weights, scalars) have that alignment; null has.
+template <typename... P>
+inline bool aligned4(P... p) {
+  return ((reinterpret_cast<uintptr_t>(p) | ...) & 3u) == 0;
+}
+
 // More elements than any buffer has: products of sizes below it fit 64 bits.
 constexpr int64_t kMostElements = int64_t(1) << 40;
 // M * top_k route ids of 32 bits.

@@ -124,7 +124,7 @@ typedef struct moe_grouped_args {
 
 /* 1 <= E <= 2048; N and K multiples of 8 (N of 16 with SWIGLU); row strides
  * multiples of 8 and at least the row's width; pointers 16-byte aligned
- * (group tables, route_ids and route_weights: their element's alignment);
+ * (those to 4-byte elements: 4 bytes);
  * 0 <= rows < 2^31.  y and pre overlap no input and not one another. */
 moe_status moe_grouped_gemm(const moe_grouped_args* args, moe_stream_t stream);
 

@@ -185,3 +185,41 @@ def test_sizes_whose_products_pass_64_bits_are_refused(L):
     c = L.MoeSwigluBackwardArgs()
     c.dh, c.pre, c.dpre, c.rows, c.I, c.lddh, c.ldpre, c.lddpre = 1 << 20, 2 << 20, 4 << 20, 100, 64, far, 128, 128
     assert lib.moe_swiglu_backward(ctypes.byref(c), None) == SHAPE
+
+
+def test_misaligned_tables_are_refused(L):
+    """A 4-byte element off its alignment would fault on the device."""
+    import ctypes
+
+    ALIGN, p, lib, odd = 3, ctypes.c_void_p, L.load(), (32 << 20) + 2
+
+    def refused(call, args, *names):
+        for name in names:
+            old = getattr(args, name)
+            setattr(args, name, odd)
+            assert getattr(lib, call)(ctypes.byref(args), None) == ALIGN, (call, name)
+            setattr(args, name, old)
+
+    a = L.MoeGroupedArgs()
+    a.x, a.w, a.y, a.group_start, a.group_rows = 1 << 20, 2 << 20, 4 << 20, 8 << 20, 9 << 20
+    a.rows, a.E, a.N, a.K, a.ldx, a.ldy, a.epilogue = 100, 4, 64, 32, 32, 64, 1
+    refused("moe_grouped_gemm", a, "group_start", "group_rows", "route_ids", "route_weights", "device_status")
+    b = L.MoeGroupedWgradArgs()
+    b.dy, b.x, b.dw, b.group_start, b.group_rows = 1 << 20, 2 << 20, 4 << 20, 8 << 20, 9 << 20
+    b.rows, b.E, b.N, b.K, b.lddy, b.ldx = 100, 4, 64, 32, 64, 32
+    refused("moe_grouped_wgrad", b, "group_start", "group_rows", "device_status")
+    c = L.MoeSwigluBackwardArgs()
+    c.dh, c.pre, c.dpre, c.rows, c.I, c.lddh, c.ldpre, c.lddpre = 1 << 20, 2 << 20, 4 << 20, 100, 64, 64, 128, 128
+    refused("moe_swiglu_backward", c, "route_ids", "num_rows", "route_weights", "dweights")
+    d = L.MoeAdamWArgs()
+    d.table, d.chunks, d.count, d.state_bits, d.step, d.lr = 1 << 20, 1, 1, 32, 1, 1e-3
+    refused("moe_adamw_step", d, "table", "grad_scale", "skip")
+    for k in (7, 9):
+        v = [p(1 << 20), 10, 64, 64, p(2 << 20), 20, 64, p(3 << 20), 2, None, 0, None]
+        v[k] = p(odd)
+        assert lib.moe_gather_rows(*v) == ALIGN
+    assert lib.moe_sum_routes(p(1 << 20), 20, 64, 64, p(2 << 20), 10, 64, p(odd), 2, 0, 0, None) == ALIGN
+    for k in (0, 2, 4, 8, 9, 10):
+        v = [p(4096), 640, p(8192), 10, p(64), 64, 32, 8, p(128), p(256), p(512), None]
+        v[k] = p(odd)
+        assert lib.moe_plan_groups(*v) == ALIGN, k
