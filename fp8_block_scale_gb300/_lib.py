@@ -619,6 +619,9 @@ def moe_plan_groups(sorted_token_ids, expert_ids, num_tokens_post_padded, block_
     _dense("group_start", group_start, torch.int32)
     _dense("group_rows", group_rows, torch.int32, E)
     _opt("route_slot", route_slot, torch.int32, R)
+    _dense("sorted_token_ids", sorted_token_ids, torch.int32)
+    _dense("expert_ids", expert_ids, torch.int32)
+    _dense("num_tokens_post_padded", num_tokens_post_padded, torch.int32, 1)
     _check("moe_plan_groups", load().moe_plan_groups(
         _ptr(sorted_token_ids), sorted_token_ids.numel(), _ptr(expert_ids), expert_ids.numel(),
         _ptr(num_tokens_post_padded), block_m, R, E, _ptr(group_start), _ptr(group_rows), _ptr(route_slot),

@@ -223,3 +223,15 @@ def test_misaligned_tables_are_refused(L):
         v = [p(4096), 640, p(8192), 10, p(64), 64, 32, 8, p(128), p(256), p(512), None]
         v[k] = p(odd)
         assert lib.moe_plan_groups(*v) == ALIGN, k
+
+
+def test_plan_groups_takes_int32_plans_only(L):
+    """64-bit ids would be read as pairs of 32-bit ones."""
+    z = lambda n, t=torch.int32: torch.zeros(n, dtype=t)                             # noqa: E731
+    for k in range(3):
+        plan = [z(32), z(4), z(1)]
+        plan[k] = z(plan[k].numel(), torch.int64)
+        with pytest.raises(ValueError):
+            L.moe_plan_groups(*plan, 8, 6, z(4), z(4))
+    with pytest.raises(ValueError):
+        L.moe_plan_groups(z(64)[::2], z(4), z(1), 8, 6, z(4), z(4))
