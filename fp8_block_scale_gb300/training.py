@@ -74,6 +74,7 @@ class ExpertLayer:
         self.table = L.AdamWTable(
             [{"param": p.view(-1), "model": m.view(-1), "grad": g.view(-1), **s}
              for p, m, g, s in zip(self.params, self.models, self.grads, self.states)], weight_decay=weight_decay)
+        self._forward_done = False                        # pre, h and xs are those of a forward pass
         self.steps = 0                                    # steps that changed the weights
         self._calls = 0
         self._skipped = None                              # the last step's skip flag on its way to the host
@@ -106,6 +107,7 @@ class ExpertLayer:
         self._batch("logits", logits, self.E, (torch.float32, torch.bfloat16))
         if not logits.is_contiguous():
             raise ValueError("logits: a contiguous tensor is expected")
+        self._forward_done = False
         L.moe_route_topk(logits, self.top_k, self.topk_ids, self.topk_weights)
         L.moe_plan(self.topk_ids, self.E, self.block_m, self.sorted_ids, self.expert_ids, self.num_padded,
                    self.plan_workspace)
@@ -119,12 +121,17 @@ class ExpertLayer:
         L.moe_grouped_gemm(self._up)
         L.moe_grouped_gemm(self._down)
         L.moe_sum_routes(self.ys, self.out, self.route_slot, self.top_k)
+        self._forward_done = True
         return self.out
 
     def backward(self, dout):
         """dout [tokens, H] -> (dx [tokens, H], the route weights' gradient
-        [tokens, top_k]); fills grads.  Uses the last forward's buffers up."""
+        [tokens, top_k]); fills grads.  Uses the last forward's buffers up:
+        RuntimeError without a forward pass since the last route or backward."""
         self._batch("dout", dout, self.H, (self.dtype,))
+        if not self._forward_done:
+            raise RuntimeError("backward without a forward pass since the last route or backward")
+        self._forward_done = False
         L.moe_gather_rows(dout, self.dys, self.sorted_ids, self.top_k, self.num_padded)
         L.moe_grouped_gemm(self._dh)
         self.dweights.zero_()                             # (the kernel leaves routes that the plan does not hold)

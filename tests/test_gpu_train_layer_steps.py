@@ -59,3 +59,24 @@ def test_a_skipped_step_does_not_count():
         for a, b in zip(layers[0].params + layers[0].models, layers[1].params + layers[1].models):
             assert torch.equal(a, b), k
     assert layers[0].steps == layers[1].steps == 3
+
+
+def test_backward_needs_its_forward():
+    """The gradient of pre takes pre's place: a second backward would run on gradients."""
+    layer = ExpertLayer(8, 64, 24, 3, 2, generator=gen(8))
+    x = torch.randn(8, 64, device="cuda", generator=gen(9)).to(BF16)
+    logits = torch.randn(8, 3, device="cuda", generator=gen(10))
+    layer.route(logits)
+    with pytest.raises(RuntimeError):
+        layer.backward(x)
+    layer.forward(x)
+    layer.backward(x)
+    with pytest.raises(RuntimeError):
+        layer.backward(x)
+    layer.forward(x)
+    layer.route(logits)
+    with pytest.raises(RuntimeError):
+        layer.backward(x)
+    layer.forward(x)
+    layer.forward(x)
+    layer.backward(x)
