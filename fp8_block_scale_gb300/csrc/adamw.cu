@@ -229,6 +229,7 @@ __global__ void __launch_bounds__(kThreads) adamw32_kernel(const __grid_constant
     const float decay = fmaf(-a.lr, t.weight_decay, 1.0f);
     const int64_t i0 = (c - t.first_chunk) * kChunk;
     if (i0 >= t.n) return;   // (more chunks than the table has)
+    if (!MOE_IN_BOUNDS(i0 >= 0 && i0 / kChunk < (t.n + kChunk - 1) / kChunk)) continue;
     adamw32_chunk<kGrad, kSmall>(a, t, decay, gs, i0);
     // the last one to three elements
     const int64_t k = (t.n & ~int64_t(3)) + threadIdx.x;
@@ -441,7 +442,7 @@ __device__ __forceinline__ void adamw8_group(const AdamParams& a, const AdamEntr
 template <int kGrad>
 __device__ __forceinline__ void load_group8(const AdamEntry& t, int64_t group, Group8& x) {
   const int64_t i = group * 128 + 4 * (threadIdx.x % 32);
-  const bool ok = (group + 1) * 128 <= t.n;
+  const bool ok = (group + 1) * 128 <= t.n && MOE_IN_BOUNDS(group >= 0);
   x.graw = load_grad4<kGrad>(t, i, ok);
   float4 p4 = {};
   if (ok) p4 = __ldcs(reinterpret_cast<const float4*>(t.param + i));
@@ -458,6 +459,7 @@ __device__ __noinline__ void adamw8_last(const AdamParams& a, float decay, float
   const AdamEntry t = a.table[tensor];
   const int lane = threadIdx.x % 32;
   const int64_t group = t.n / 128, i = group * 128 + 4 * lane;
+  if (!MOE_IN_BOUNDS(tensor < static_cast<uint32_t>(a.count) && t.n % 128)) return;   // (a scale for the group)
   const int have = t.n - i >= 4 ? 4 : t.n > i ? static_cast<int>(t.n - i) : 0;
   Group8 x = {};
   float g[4] = {};
@@ -513,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 3) adamw8_kernel(const __grid_consta
       }
 #pragma unroll
       for (int u = 0; u < kSteps; ++u) {
-        if ((group + u * kWarps + 1) * 128 > t.n) continue;
+        if ((group + u * kWarps + 1) * 128 > t.n || !MOE_IN_BOUNDS(index >= 0 && index < a.count && group >= 0)) continue;
         float g[4];
         grad4<kGrad>(x[u].graw, g);
         adamw8_group<true, kSmall>(a, t, decay, gs, id, group + u * kWarps, x[u], g, 4);

@@ -557,7 +557,8 @@ __device__ __forceinline__ void few_slots_finish(const Params& p, Ctl* ctl, cons
       const int slot = 2 * c + lane / 16;
       if (slot > group.x % kFewSlots) continue;
       id[c] = static_cast<int64_t>(group.y) + slot;
-      if (p.route_ids) id[c] = p.route_ids[id[c]];
+      if (!MOE_IN_BOUNDS(id[c] >= 0 && id[c] < p.rows)) id[c] = -1;
+      if (p.route_ids && id[c] >= 0) id[c] = p.route_ids[id[c]];
     }
   };
   auto fetch_weights = [&](float (&w)[kMine]) {
@@ -573,7 +574,9 @@ __device__ __forceinline__ void few_slots_finish(const Params& p, Ctl* ctl, cons
   uint32_t n = 0;
   for (uint32_t u = blockIdx.x; u < f.total; u += gridDim.x, ++n) {
     const int2 group = ctl->group[u / f.steps];
-    const int s0 = group.y, slots = group.x % kFewSlots + 1;
+    const int s0 = group.y;
+    // (a group outside the buffer: no slot is written)
+    const int slots = MOE_IN_BOUNDS(s0 >= 0 && s0 <= p.rows - 1 - group.x % kFewSlots) ? group.x % kFewSlots + 1 : 0;
     fetch_weights(next_wt);
     fetch_ids(u + 2 * gridDim.x);
     const uint32_t buf = n % F::kBuffers;
@@ -628,6 +631,7 @@ __device__ __forceinline__ void slot_weights(const Params& p, const Tile& t, int
   for (int i = 0; i < 4; ++i) {
     const int k = 32 * i + lane, col = k / 16 * 32 + 16 * turn + k % 16;
     r[i] = col < t.nt ? static_cast<int64_t>(t.s0) + t.n0 + col : -1;
+    if (!MOE_IN_BOUNDS(r[i] < p.rows)) r[i] = -1;
     if (r[i] >= 0 && p.route_ids) {
       r[i] = p.route_ids[r[i]];
       if (r[i] >= p.R) r[i] = -1;

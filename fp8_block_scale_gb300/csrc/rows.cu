@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(256)
       int64_t a = 0, b = nb;
       while (a < b) {
         const int64_t m = (a + b) / 2;
-        if (experts[m] < e + i) a = m + 1; else b = m;
+        if (MOE_IN_BOUNDS(m >= 0 && m < blocks_cap) && experts[m] < e + i) a = m + 1; else b = m;
       }
       lo[i] = a;
     }
@@ -43,7 +43,10 @@ __global__ void __launch_bounds__(256)
       int a = 0, b = block_m;
       while (a < b) {
         const int m = (a + b) / 2;
-        if (ids[m] >= 0 && ids[m] < R) a = m + 1; else b = m;
+        if (MOE_IN_BOUNDS((lo[1] - 1) * block_m + m < blocks_cap * block_m) && ids[m] >= 0 && ids[m] < R)
+          a = m + 1;
+        else
+          b = m;
       }
       n = (lo[1] - 1 - lo[0]) * block_m + a;
     }
@@ -54,7 +57,7 @@ __global__ void __launch_bounds__(256)
     const int64_t slots = nb * block_m, stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
     for (int64_t s = tid; s < slots; s += stride) {
       const int32_t r = sorted[s];
-      if (r >= 0 && r < R) route_slot[r] = static_cast<int32_t>(s);
+      if (r >= 0 && r < R && MOE_IN_BOUNDS(s < blocks_cap * block_m)) route_slot[r] = static_cast<int32_t>(s);
     }
   }
 }
@@ -78,7 +81,7 @@ __global__ void __launch_bounds__(256)
        s += static_cast<int64_t>(gridDim.x) * 8) {
     const int32_t r = route_ids[s];
     const int64_t t = r >= 0 ? r / top_k : M;
-    const bool live = t < M;
+    const bool live = t < M && MOE_IN_BOUNDS(t >= 0 && s < rows);
     const uint4* src = live ? x + t * ldx : x;
     uint4* dst = xs + s * ldxs;
     for (int v = lane; v < vecs; v += 32) __stcs(dst + v, live ? src[v] : make_uint4(0, 0, 0, 0));
@@ -127,6 +130,7 @@ __global__ void __launch_bounds__(256)
        i += static_cast<int64_t>(gridDim.x) * 256) {
     const int64_t t = i / vecs;
     const int v = static_cast<int>(i - t * vecs);
+    if (!MOE_IN_BOUNDS(t >= 0 && t < M && v >= 0 && v < vecs)) continue;
     float acc[8] = {};
     if (accumulate) add_vec<T>(out[t * ldout + v], acc);
     for (int j0 = 0; j0 < top_k; j0 += kBatch) {
@@ -137,7 +141,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
         row[j] = make_uint4(0, 0, 0, 0);
-        if (slot[j] >= 0 && slot[j] < rows) row[j] = __ldcs(y + slot[j] * ldy + v);
+        if (slot[j] >= 0 && slot[j] < rows && MOE_IN_BOUNDS(ldy >= vecs)) row[j] = __ldcs(y + slot[j] * ldy + v);
       }
 #pragma unroll
       for (int j = 0; j < kBatch; ++j)
@@ -186,6 +190,7 @@ __global__ void __launch_bounds__(256) swiglu_backward_kernel(const SwigluParams
       r = p.route_ids[s];
       if (r < 0 || r >= p.R) continue;
     }
+    if (!MOE_IN_BOUNDS(s >= 0 && s < p.rows && r >= 0 && (p.route_ids ? r < p.R : r < p.rows))) continue;
     const float wt = p.weights ? p.weights[r] : 1.0f;
     float dot = 0.f;
     for (int i = 8 * lane; i < p.I; i += 256) {

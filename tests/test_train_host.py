@@ -235,3 +235,14 @@ def test_plan_groups_takes_int32_plans_only(L):
             L.moe_plan_groups(*plan, 8, 6, z(4), z(4))
     with pytest.raises(ValueError):
         L.moe_plan_groups(z(64)[::2], z(4), z(1), 8, 6, z(4), z(4))
+
+
+@pytest.mark.parametrize("name", ["grouped.cu", "rows.cu", "adamw.cu"])
+def test_training_kernels_have_bounds_checks(name):
+    """What the bounds-checking build reports about a file is worth something only where it checks."""
+    import os
+
+    import fp8_block_scale_gb300
+    with open(os.path.join(os.path.dirname(fp8_block_scale_gb300.__file__), "csrc", name)) as f:
+        text = f.read()
+    assert "MOE_BOUNDS_TU()" in text and text.count("MOE_IN_BOUNDS(") >= 4
