@@ -35,10 +35,10 @@ struct AdamEntry {
   int64_t n;
   int64_t first_chunk;
   float weight_decay;
-  int32_t grad_dtype;
+  int32_t kind;   // the gradients' type, and kEightBits (a kernel for other states would write past this tensor's)
   int32_t model_dtype;
-  int32_t state_bits;   // (a kernel for other states would write past this tensor's)
 };
+constexpr int32_t kEightBits = 4;
 
 struct AdamParams {
   const AdamEntry* table;
@@ -147,9 +147,10 @@ __device__ __forceinline__ void grad4(const uint4& raw, float (&g)[4]) {
   g[0] = a.x; g[1] = a.y; g[2] = b.x; g[3] = b.y;
 }
 __device__ __forceinline__ float load_grad1(const AdamEntry& t, int64_t i) {
-  if (t.grad_dtype == MOE_TYPE_FP32) return static_cast<const float*>(t.grad)[i];
+  const int dtype = t.kind % kEightBits;
+  if (dtype == MOE_TYPE_FP32) return static_cast<const float*>(t.grad)[i];
   const uint32_t v = static_cast<const uint16_t*>(t.grad)[i];
-  return t.grad_dtype == MOE_TYPE_BF16 ? Pack2<__nv_bfloat16>::load(v).x : Pack2<__half>::load(v).x;
+  return dtype == MOE_TYPE_BF16 ? Pack2<__nv_bfloat16>::load(v).x : Pack2<__half>::load(v).x;
 }
 __device__ __forceinline__ uint2 model4(const AdamEntry& t, const float (&p)[4]) {
   if (t.model_dtype == MOE_TYPE_BF16)
@@ -225,15 +226,14 @@ __global__ void __launch_bounds__(kThreads) adamw32_kernel(const __grid_constant
   const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
   for (int64_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
     const AdamEntry t = a.table[find_entry(a, c)];
-    if (t.grad_dtype != kGrad || t.state_bits != 32) continue;
+    if (t.kind != kGrad) continue;
     const float decay = fmaf(-a.lr, t.weight_decay, 1.0f);
     const int64_t i0 = (c - t.first_chunk) * kChunk;
-    if (i0 >= t.n) return;   // (more chunks than the table has)
-    if (!MOE_IN_BOUNDS(i0 >= 0 && i0 / kChunk < (t.n + kChunk - 1) / kChunk)) continue;
+    if (!MOE_IN_BOUNDS(i0 >= 0)) continue;
     adamw32_chunk<kGrad, kSmall>(a, t, decay, gs, i0);
-    // the last one to three elements
+    // the last one to three elements, in their chunk (past the table's chunks there is none)
     const int64_t k = (t.n & ~int64_t(3)) + threadIdx.x;
-    if (i0 + kChunk > t.n && k < t.n) {
+    if (k < t.n && static_cast<uint64_t>(k - i0) < kChunk) {
       float* m = static_cast<float*>(t.m);
       float* v = static_cast<float*>(t.v);
       const Elem2 e = adam_elem2<kSmall>(a, decay, both(__fmul_rn(load_grad1(t, k), gs)), both(t.param[k]), both(m[k]), both(v[k]));
@@ -248,8 +248,9 @@ __global__ void __launch_bounds__(kThreads) adamw32_kernel(const __grid_constant
 
 // ---------------------------------------------------------------- 8-bit states
 
-// Twenty bits for one element: an integer hash (two multiply-xorshift rounds)
-// of seed, tensor and element; `key` is what the elements of 2^32 share.
+// Twenty bits for one element: an integer hash of seed, tensor and element;
+// `key` is what the elements of 2^32 share.  The two multiply-xorshift rounds
+// are the published mixer of C. Wellons ("Prospecting for Hash Functions", 2018).
 __device__ __forceinline__ uint32_t random_key(uint32_t seed, uint32_t tensor, int64_t i) {
   return static_cast<uint32_t>(i >> 32) * 0x85EBCA77u + seed + 0x9E3779B9u * (tensor + 1u);
 }
@@ -498,13 +499,12 @@ __global__ void __launch_bounds__(kThreads, 3) adamw8_kernel(const __grid_consta
     const uint32_t id = static_cast<uint32_t>(index);
     Group8 next[kSteps];
     int64_t group = (c - t.first_chunk) * (kChunk / 128) + warp;
-    const bool mine = t.grad_dtype == kGrad && t.state_bits == 8;
-    if (mine) {
+    if (t.kind == kGrad + kEightBits) {
 #pragma unroll
       for (int u = 0; u < kSteps; ++u) load_group8<kGrad>(t, group + u * kWarps, next[u]);
     }
     for (; c < past; c += gridDim.x) {
-      if (!mine) continue;
+      if (t.kind != kGrad + kEightBits) continue;
       Group8 x[kSteps];
 #pragma unroll
       for (int u = 0; u < kSteps; ++u) x[u] = next[u];
@@ -590,8 +590,7 @@ moe_status moe_adamw_table_init(const moe_adamw_tensor* tensors, int count, int 
     e.n = t.n;
     e.first_chunk = total;
     e.weight_decay = static_cast<float>(t.weight_decay);
-    e.grad_dtype = t.grad_dtype;
-    e.state_bits = state_bits;
+    e.kind = t.grad_dtype + (state_bits == 8 ? kEightBits : 0);
     e.model_dtype = t.model ? t.model_dtype : MOE_TYPE_BF16;
     total += ceil_div(t.n, kChunk);
     if (t.n > 0) types |= 1 << t.grad_dtype;
@@ -647,7 +646,9 @@ moe_status moe_adamw_step(const moe_adamw_args* g, moe_stream_t stream) {
   p.eps = static_cast<float>(g->eps);
   p.seed = g->seed;
   p.count = g->count;
-  // as many CTAs as are resident at once
+  // 8-bit states: as many CTAs as are resident at once.  32-bit states: three times
+  // the five that are (80-92 registers a thread), as their chunks end at different
+  // times: 268 million elements 1153 us, with five CTAs an SM 1195, with ten 1196.
   const int64_t most = static_cast<int64_t>(dev.sms) * (g->state_bits == 32 ? 16 : 3);
   const unsigned grid = static_cast<unsigned>(g->chunks < most ? g->chunks : most);
   // The update's denominator is sqrt(v) root_scale + eps.  Roots that root2 misses

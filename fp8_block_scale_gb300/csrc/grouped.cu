@@ -29,7 +29,7 @@
 // What bounds it, and what it measures on one GB300 (BF16, bursts):
 //  - many rows (8 experts of 8192, K 4096, N 2048): a block of 64 contraction
 //    elements takes 0.30 us, of which 0.27 the MMAs and 0.24 the 32 KB that each
-//    SM receives (about 135 GB/s at most); 1777 TFLOP/s forward, 1860 input
+//    SM receives (about 135 GB/s at most); 1777 TFLOP/s forward, 1852 input
 //    gradient, 1740 weight gradient;
 //  - a training batch (288 experts of 228 rows): the weights' bytes; forward 854
 //    us (6.6 TB/s), with SwiGLU and its inputs kept 885 us, input gradient 848

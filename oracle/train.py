@@ -125,7 +125,8 @@ def e4m3_random(y, u20):
 
 
 def hash20(seed, tensor, n, first=0):
-    """The twenty random bits of elements first .. first + n - 1 of a tensor."""
+    """The twenty random bits of elements first .. first + n - 1 of a tensor.  The
+    mixer is C. Wellons' published one ("Prospecting for Hash Functions", 2018)."""
     M = (1 << 32) - 1
     key = (seed + 0x9E3779B9 * (tensor + 1)) & M
     out = np.empty(n, np.int64)
