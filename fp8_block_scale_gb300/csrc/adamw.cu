@@ -7,8 +7,8 @@
 // and the states once: HBM bounds it.
 //
 // The arithmetic is FP32.  268 million elements, BF16 gradients and copy: 32-bit
-// states 1145 us (28 bytes an element, 6.6 TB/s, the measured copy rate), 8-bit
-// states 714 us (16.1 bytes, 6.05 TB/s; some 50 instructions an element keep the
+// states 1141 us (28 bytes an element, 6.6 TB/s, the measured copy rate), 8-bit
+// states 715 us (16.1 bytes, 6.05 TB/s; some 50 instructions an element keep the
 // schedulers busy enough that the loads have to run a chunk ahead).
 #include <cfloat>
 #include <cmath>
@@ -87,7 +87,7 @@ __device__ __forceinline__ float2 neg(float2 v) { return make_float2(-v.x, -v.y)
 // correctly rounded one.  Below, the residual underflows: the root's last bit may be
 // off, and from v = 1e-37 down it comes out too small (0.15 of it at 1e-39).
 // kSmall: small values are taken 2^100 times as large.  That costs 2.7% with
-// 8-bit states (733 us against 714 at 268 million elements) and 0.7% with 32-bit
+// 8-bit states (733 us against 715 at 268 million elements) and 0.7% with 32-bit
 // ones, so it is chosen by eps, beside which such roots vanish (moe_adamw_step).
 template <bool kSmall>
 __device__ __forceinline__ float2 root2(float2 u) {
@@ -297,7 +297,7 @@ struct Group8 {
 // elements NaN or infinite at the next step: a v beyond FP32 has a root within it,
 // formed here from values 2^-80 times as large, and what has not is held as the
 // largest finite value.  (Apart, as its code between the usual groups' cost 3%:
-// 268 million elements 737 us against 716.)
+// 268 million elements 737 us against 715.)
 struct Scaled8 {
   float4 m, r;
   float m_scale, r_scale;
@@ -378,7 +378,7 @@ __device__ __forceinline__ void adamw8_group(const AdamParams& a, const AdamEntr
   float mq[4], y[4];
   bool zeros = false;
   // (8e-14: a v below 1e-37, whose root root2 misses, then gets the smallest code
-  // either way; a tensor of nothing but smaller roots takes 1397 us instead of 713)
+  // either way; a tensor of nothing but smaller roots takes 1397 us instead of 715)
   if (mmax > 1e-25f && rmax > (kSmall ? 1e-25f : 8e-14f) && fmaxf(mmax, rmax) <= FLT_MAX) {
     const float mi = __frcp_rn(mns), vi = __frcp_rn(vns);
 #pragma unroll
@@ -646,9 +646,9 @@ moe_status moe_adamw_step(const moe_adamw_args* g, moe_stream_t stream) {
   p.eps = static_cast<float>(g->eps);
   p.seed = g->seed;
   p.count = g->count;
-  // 8-bit states: as many CTAs as are resident at once.  32-bit states: three times
-  // the five that are (80-92 registers a thread), as their chunks end at different
-  // times: 268 million elements 1153 us, with five CTAs an SM 1195, with ten 1196.
+  // 8-bit states: as many CTAs as are resident at once.  32-bit states: about three
+  // times the five or six that are (80-92 registers a thread); measured side by side
+  // at 268 million elements, 16 CTAs an SM took 1153 us, five 1195, six 1314, ten 1196.
   const int64_t most = static_cast<int64_t>(dev.sms) * (g->state_bits == 32 ? 16 : 3);
   const unsigned grid = static_cast<unsigned>(g->chunks < most ? g->chunks : most);
   // The update's denominator is sqrt(v) root_scale + eps.  Roots that root2 misses
