@@ -379,8 +379,9 @@ __device__ __forceinline__ void adamw8_group(const AdamParams& a, const AdamEntr
   bool zeros = false;
   // (8e-14: a v below 1e-37, whose root root2 misses, then gets the smallest code
   // either way; a tensor of nothing but smaller roots takes 1397 us instead of 715)
-  if (mmax > 1e-25f && rmax > (kSmall ? 1e-25f : 8e-14f) && fmaxf(mmax, rmax) <= FLT_MAX) {
-    const float mi = __frcp_rn(mns), vi = __frcp_rn(vns);
+  if ((mmax > 1e-25f || mmax == 0.f) && rmax > (kSmall ? 1e-25f : 8e-14f) && fmaxf(mmax, rmax) <= FLT_MAX) {
+    // (m is zero, its root not, where an expert has had no rows for long: 0 / 0 is 0 here)
+    const float mi = mmax > 0.f ? __frcp_rn(mns) : 0.f, vi = __frcp_rn(vns);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const float2 q = quotient2(make_float2(m[2 * h], m[2 * h + 1]), mns, mi);

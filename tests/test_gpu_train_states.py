@@ -170,3 +170,25 @@ def test_adamw_arguments_that_do_not_fit_the_table(bits):
         for k in a:
             assert torch.equal(a[k].view(torch.uint8), b[k].view(torch.uint8)), k
             assert torch.equal(c[k].view(torch.uint8), d[k].view(torch.uint8)), k
+
+
+def test_adamw8_first_moments_of_zero_beside_ordinary_roots():
+    """Groups whose first moment has decayed to nothing, some with a NaN gradient or one element alone."""
+    n = 128 * 40 + 5
+    t = _tensors([n], 8, F32, None, gen(29))[0]
+    t["exp_avg"].view(torch.uint8).zero_()
+    t["grad"].zero_()
+    t["grad"][128 * 7 + 3] = 0.25
+    t["grad"][128 * 9 + 4] = 1e-30
+    m, r, ms, rs = _formula32(t, 0, 3, 1.0, **HYPER)
+    _step([t], seed=3)
+    for name, codes, scale in (("exp_avg", m, ms), ("exp_avg_sq", r, rs)):
+        assert (t[name + "_scale"].cpu().numpy() == scale).all(), name
+        assert (f64(t[name].float()) == codes).all(), name
+    assert int((f64(t["exp_avg"].float()) != 0).sum()) == 2
+    t["grad"].zero_()
+    t["grad"][128 * 5 + 1] = float("nan")
+    _step([t], seed=4, step=4)
+    for name in ("exp_avg", "exp_avg_sq", "param"):
+        bad = torch.isnan(t[name].float()).nonzero().view(-1)
+        assert bad.tolist() == [128 * 5 + 1], name
