@@ -182,7 +182,7 @@ def prepare(c, seed):
     st["w_post"] = normal(H, std=0.1, mean=0.5, dtype=weights) if c["post"] else None
     st["w_pre"] = normal(H, std=0.2, mean=1.0, dtype=weights) if c["pre"] else None
     st["gate"] = {"none": lambda: None, "channel": lambda: normal(H, std=0.1, mean=0.3, dtype=weights),
-                  "token": lambda: torch.sigmoid(normal(M)), "full": lambda: normal(M, H, std=0.5, dtype=branch)}[c["gate"]]()
+                  "token": lambda: torch.sigmoid(normal(M, 1)), "full": lambda: normal(M, H, std=0.5, dtype=branch)}[c["gate"]]()
     if c["op"] == "norm":
         st["r"] = normal(M, H, std=2.0, dtype=stream) if c["residual"] else None
         st["h"] = zeros(M, H, dtype=stream)
@@ -198,7 +198,7 @@ def prepare(c, seed):
     st["dr"] = zeros(M, H, dtype=stream) if c["residual"] else None
     st["dw_pre"] = zeros(H) if c["pre"] else None
     st["dw_post"] = zeros(H) if c["post"] else None
-    st["dgate"] = {"none": lambda: None, "channel": lambda: zeros(H), "token": lambda: zeros(M),
+    st["dgate"] = {"none": lambda: None, "channel": lambda: zeros(H), "token": lambda: zeros(M, 1),
                    "full": lambda: zeros(M, H, dtype=branch)}[c["gate"]]()
     return st
 
@@ -256,9 +256,7 @@ def _plain_route_grad(c, st):
 def _gate(c, st, n):
     if c["gate"] == "none":
         return 1.0
-    if c["gate"] == "channel":
-        return st["gate"].float()
-    return st["gate"][:n].float().reshape(n, -1)
+    return st["gate"].float() if c["gate"] == "channel" else st["gate"][:n].float()
 
 
 def _inverse_rms(x):
@@ -318,7 +316,7 @@ def _plain_norm_grad(c, st):
         if c["gate"] == "channel":
             st["dgate"].copy_(dg.sum(0))
         elif c["gate"] == "token":
-            st["dgate"][:n] = dg.sum(1)
+            st["dgate"][:n] = dg.sum(1, keepdim=True)
         else:
             st["dgate"][:n] = dg.to(st["dgate"].dtype)
         got["dgate"] = st["dgate"]
@@ -452,8 +450,7 @@ def _rows64(M, n, v):
 def _exact_gate(c, st, n):
     if c["gate"] == "none":
         return None
-    g = st["gate"].double()
-    return {"channel": lambda: g.unsqueeze(0), "token": lambda: g[:n].unsqueeze(1), "full": lambda: g[:n]}[c["gate"]]()
+    return st["gate"].double() if c["gate"] == "channel" else st["gate"][:n].double()
 
 
 def _exact_codes(v, powers):
@@ -509,7 +506,7 @@ def _exact_norm_grad(c, st):
     if g is not None:
         u = y / torch.sqrt((y * y).sum(1, keepdim=True) / H + EPS) * st["w_post"].double() if c["post"] else y
         dg = total * u
-        got["dgate"] = {"channel": lambda: dg.sum(0), "token": lambda: _rows64(M, n, dg.sum(1)),
+        got["dgate"] = {"channel": lambda: dg.sum(0), "token": lambda: _rows64(M, n, dg.sum(1, keepdim=True)),
                         "full": lambda: _rows64(M, n, dg)}[c["gate"]]()
     if c["post"]:
         d, got["dw_post"] = through(y, st["w_post"].double(), d)
