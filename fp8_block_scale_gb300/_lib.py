@@ -213,6 +213,127 @@ class MoeAdamWArgs(ctypes.Structure):
     ]
 
 
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+GROUP_MAX, GROUP_TOP2 = 0, 1
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
+
+
+class MoeRouteScoresArgs(ctypes.Structure):
+    """Mirror of ``struct moe_route_scores_args`` (include/moe_block.h)."""
+    _fields_ = [
+        ("logits", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p),
+        ("topk_ids", ctypes.c_void_p),
+        ("topk_weights", ctypes.c_void_p),
+        ("num_tokens", ctypes.c_void_p),
+        ("M", ctypes.c_int64),
+        ("ldlogits", ctypes.c_int64),
+        ("E", ctypes.c_int32),
+        ("top_k", ctypes.c_int32),
+        ("groups", ctypes.c_int32),
+        ("topk_groups", ctypes.c_int32),
+        ("group_score", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("id_bits", ctypes.c_int32),
+        ("routed_scale", ctypes.c_float),
+    ]
+
+
+class MoeRouteScoresBackwardArgs(ctypes.Structure):
+    """Mirror of ``struct moe_route_scores_backward_args``."""
+    _fields_ = [
+        ("logits", ctypes.c_void_p),
+        ("topk_ids", ctypes.c_void_p),
+        ("dweights", ctypes.c_void_p),
+        ("dlogits", ctypes.c_void_p),
+        ("num_tokens", ctypes.c_void_p),
+        ("M", ctypes.c_int64),
+        ("ldlogits", ctypes.c_int64),
+        ("lddlogits", ctypes.c_int64),
+        ("E", ctypes.c_int32),
+        ("top_k", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("id_bits", ctypes.c_int32),
+        ("routed_scale", ctypes.c_float),
+    ]
+
+
+class MoeNormArgs(ctypes.Structure):
+    """Mirror of ``struct moe_norm_args``."""
+    _fields_ = [
+        ("y", ctypes.c_void_p),
+        ("r", ctypes.c_void_p),
+        ("gate", ctypes.c_void_p),
+        ("w_post", ctypes.c_void_p),
+        ("w_pre", ctypes.c_void_p),
+        ("h", ctypes.c_void_p),
+        ("z", ctypes.c_void_p),
+        ("q", ctypes.c_void_p),
+        ("q_scale", ctypes.c_void_p),
+        ("num_rows", ctypes.c_void_p),
+        ("M", ctypes.c_int64),
+        ("ldy", ctypes.c_int64),
+        ("ldr", ctypes.c_int64),
+        ("ldh", ctypes.c_int64),
+        ("ldz", ctypes.c_int64),
+        ("ldgate", ctypes.c_int64),
+        ("H", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("stream_dtype", ctypes.c_int32),
+        ("weight_dtype", ctypes.c_int32),
+        ("gate_mode", ctypes.c_int32),
+        ("post_norm", ctypes.c_int32),
+        ("scale_mode", ctypes.c_int32),
+        ("residual_scale", ctypes.c_float),
+        ("weight_offset", ctypes.c_float),
+        ("eps", ctypes.c_float),
+    ]
+
+
+class MoeNormBackwardArgs(ctypes.Structure):
+    """Mirror of ``struct moe_norm_backward_args``."""
+    _fields_ = [
+        ("y", ctypes.c_void_p),
+        ("h", ctypes.c_void_p),
+        ("gate", ctypes.c_void_p),
+        ("w_post", ctypes.c_void_p),
+        ("w_pre", ctypes.c_void_p),
+        ("dh", ctypes.c_void_p),
+        ("dz", ctypes.c_void_p),
+        ("dy", ctypes.c_void_p),
+        ("dr", ctypes.c_void_p),
+        ("dgate", ctypes.c_void_p),
+        ("dw_post", ctypes.c_void_p),
+        ("dw_pre", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("num_rows", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+        ("M", ctypes.c_int64),
+        ("ldy", ctypes.c_int64),
+        ("ldh", ctypes.c_int64),
+        ("ldgate", ctypes.c_int64),
+        ("lddh", ctypes.c_int64),
+        ("lddz", ctypes.c_int64),
+        ("lddy", ctypes.c_int64),
+        ("lddr", ctypes.c_int64),
+        ("lddgate", ctypes.c_int64),
+        ("H", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("stream_dtype", ctypes.c_int32),
+        ("weight_dtype", ctypes.c_int32),
+        ("gate_mode", ctypes.c_int32),
+        ("post_norm", ctypes.c_int32),
+        ("accumulate", ctypes.c_int32),
+        ("residual_scale", ctypes.c_float),
+        ("weight_offset", ctypes.c_float),
+        ("eps", ctypes.c_float),
+    ]
+
+
 _libs = {}
 _active = LIB_PATH
 
@@ -272,6 +393,13 @@ _SIGS = {
                                             ctypes.c_void_p, ctypes.c_size_t, ctypes.POINTER(ctypes.c_int64),
                                             ctypes.POINTER(ctypes.c_int32), ctypes.c_void_p]),
     "moe_adamw_step": (ctypes.c_int, [ctypes.POINTER(MoeAdamWArgs), ctypes.c_void_p]),
+    "moe_route_scores": (ctypes.c_int, [ctypes.POINTER(MoeRouteScoresArgs), ctypes.c_void_p]),
+    "moe_route_scores_backward": (ctypes.c_int, [ctypes.POINTER(MoeRouteScoresBackwardArgs), ctypes.c_void_p]),
+    "moe_route_balance": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                         ctypes.c_float, ctypes.c_void_p]),
+    "moe_norm_residual": (ctypes.c_int, [ctypes.POINTER(MoeNormArgs), ctypes.c_void_p]),
+    "moe_norm_residual_workspace_size": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int]),
+    "moe_norm_residual_backward": (ctypes.c_int, [ctypes.POINTER(MoeNormBackwardArgs), ctypes.c_void_p]),
     "moe_debug_bounds_enabled": (ctypes.c_int, []),
     "moe_debug_bounds_selftest": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_void_p,
                                                  ctypes.c_void_p]),
@@ -806,3 +934,218 @@ def make_adamw_args(table, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, seed=0, g
 
 def moe_adamw_step(args, stream=None):
     _check("moe_adamw_step", load().moe_adamw_step(ctypes.byref(args), _stream(stream)))
+
+
+# ---------------------------------------------------------------- around the experts (include/moe_block.h)
+#
+# Row buffers and argument records as on the training side.
+
+ID_BITS = {torch.int32: 32, torch.int64: 64}
+
+
+def _code(name, t, codes, names):
+    if t.dtype not in codes:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {names}")
+    return codes[t.dtype]
+
+
+def _logits(name, t):
+    """(pointer, M, E, elements from a row to the next, type) of router logits."""
+    M, E, ld = _row_buffer(name, t)
+    return t.data_ptr(), M, E, ld, _code(name, t, TYPE_CODES, "bfloat16, float16 or float32")
+
+
+def _routes(ids, other_name, other, M):
+    """top_k and id width of a token's routes: ids [M, top_k] and a float32 tensor of that shape."""
+    if len(ids.shape) != 2 or ids.shape[0] != M:
+        raise ValueError(f"topk_ids: shape {tuple(ids.shape)}, expected ({M}, top_k)")
+    _dense("topk_ids", ids)
+    _dense(other_name, other, torch.float32)
+    _shape(other_name, other, ids.shape)
+    return ids.shape[1], _code("topk_ids", ids, ID_BITS, "int32 or int64")
+
+
+def make_route_scores_args(logits, topk_ids, topk_weights, bias=None, score=SCORE_SIGMOID, groups=1, topk_groups=1,
+                           group_score=GROUP_MAX, renormalize=True, routed_scale=1.0, num_tokens=None):
+    """Fill a ``moe_route_scores_args``: logits [M, E] (bfloat16, float16 or float32), topk_ids
+    [M, top_k] int32 or int64, topk_weights [M, top_k] and bias [E] float32, num_tokens [1] int32."""
+    args = MoeRouteScoresArgs()
+    args.logits, args.M, args.E, args.ldlogits, args.dtype = _logits("logits", logits)
+    args.top_k, args.id_bits = _routes(topk_ids, "topk_weights", topk_weights, args.M)
+    args.topk_ids, args.topk_weights = topk_ids.data_ptr(), topk_weights.data_ptr()
+    if bias is not None:
+        _shape("bias", bias, (args.E,))
+    args.bias = _opt("bias", bias, torch.float32)
+    args.num_tokens = _opt("num_tokens", num_tokens, torch.int32, 1)
+    args.groups, args.topk_groups, args.group_score, args.score = groups, topk_groups, group_score, score
+    args.renormalize, args.routed_scale = 1 if renormalize else 0, routed_scale
+    args._keepalive = (logits, topk_ids, topk_weights, bias, num_tokens)
+    return args
+
+
+def moe_route_scores(args, stream=None):
+    _check("moe_route_scores", load().moe_route_scores(ctypes.byref(args), _stream(stream)))
+
+
+def make_route_scores_backward_args(logits, topk_ids, dweights, dlogits, score=SCORE_SIGMOID, renormalize=True,
+                                    routed_scale=1.0, num_tokens=None):
+    """Fill a ``moe_route_scores_backward_args``: dlogits of logits' shape and type (it may be logits)."""
+    args = MoeRouteScoresBackwardArgs()
+    args.logits, args.M, args.E, args.ldlogits, args.dtype = _logits("logits", logits)
+    args.dlogits, args.lddlogits = _rows2d("dlogits", dlogits, logits.dtype)
+    _shape("dlogits", dlogits, logits.shape)
+    args.top_k, args.id_bits = _routes(topk_ids, "dweights", dweights, args.M)
+    args.topk_ids, args.dweights = topk_ids.data_ptr(), dweights.data_ptr()
+    args.num_tokens = _opt("num_tokens", num_tokens, torch.int32, 1)
+    args.score, args.renormalize, args.routed_scale = score, 1 if renormalize else 0, routed_scale
+    args._keepalive = (logits, topk_ids, dweights, dlogits, num_tokens)
+    return args
+
+
+def moe_route_scores_backward(args, stream=None):
+    _check("moe_route_scores_backward", load().moe_route_scores_backward(ctypes.byref(args), _stream(stream)))
+
+
+def moe_route_balance(load_of_experts, bias, rate, out=None, stream=None):
+    """bias [E] float32 (or out, without touching bias) one step of `rate` towards an even load
+    (load_of_experts [E] int32, for example a plan's group_rows)."""
+    out = bias if out is None else out
+    E = bias.numel()
+    _dense("bias", bias, torch.float32)
+    _dense("out", out, torch.float32)
+    _dense("load_of_experts", load_of_experts, torch.int32)
+    for name, t in (("out", out), ("load_of_experts", load_of_experts)):
+        if t.numel() != E:
+            raise ValueError(f"{name}: {t.numel()} elements, expected {E}")
+    _check("moe_route_balance", load().moe_route_balance(_ptr(load_of_experts), _ptr(bias), _ptr(out), E, rate,
+                                                         _stream(stream)))
+
+
+def _norm_common(args, y, gate, w_post, w_pre, post_norm, residual_scale, weight_offset, eps, num_rows):
+    """The fields both directions share; returns (branch type, its shape)."""
+    M, H, args.ldy = _row_buffer("y", y)
+    args.y, args.M, args.H = y.data_ptr(), M, H
+    args.dtype = _code("y", y, TYPE_CODES, "bfloat16, float16 or float32")
+    weights = [(n, w) for n, w in (("w_post", w_post), ("w_pre", w_pre)) if w is not None]
+    if w_post is not None and not post_norm:
+        raise ValueError("w_post: given without post_norm")
+    mode = GATE_NONE
+    if gate is not None:
+        shape = tuple(gate.shape)
+        if shape == (M, H):
+            mode = GATE_FULL
+            args.gate, args.ldgate = _rows2d("gate", gate, y.dtype)
+        elif shape == (M, 1):
+            mode = GATE_TOKEN
+            args.gate = _dense("gate", gate, torch.float32)
+        elif shape == (H,):
+            mode = GATE_CHANNEL
+            args.gate = _dense("gate", gate)
+            weights.append(("gate", gate))
+        else:
+            raise ValueError(f"gate: shape {shape}, expected ({H},), ({M}, 1) or ({M}, {H})")
+    kind = weights[0][1].dtype if weights else y.dtype
+    for name, w in weights:
+        _shape(name, w, (H,))
+        if w.dtype != kind or kind not in (y.dtype, torch.float32):
+            raise ValueError(f"{name}: dtype {w.dtype}, expected one type for weights and channel gate, {y.dtype} or float32")
+    args.w_post, args.w_pre = _opt("w_post", w_post, kind), _opt("w_pre", w_pre, kind)
+    args.weight_dtype, args.gate_mode, args.post_norm = TYPE_CODES[kind], mode, 1 if post_norm else 0
+    args.residual_scale, args.weight_offset, args.eps = residual_scale, weight_offset, eps
+    args.num_rows = _opt("num_rows", num_rows, torch.int32, 1)
+    return M, H
+
+
+def _stream_rows(args, y, tensors):
+    """The residual stream's buffers: one type, y's or float32."""
+    kind = None
+    for name, t, field, ld in tensors:
+        if t is None:
+            continue
+        kind = t.dtype if kind is None else kind
+        if t.dtype != kind or kind not in (y.dtype, torch.float32):
+            raise ValueError(f"{name}: dtype {t.dtype}, expected one type for the stream, {y.dtype} or float32")
+        _shape(name, t, y.shape)
+        p, stride = _rows2d(name, t)
+        setattr(args, field, p)
+        setattr(args, ld, stride)
+    args.stream_dtype = TYPE_CODES[y.dtype if kind is None else kind]
+
+
+def _branch_rows(args, y, tensors):
+    for name, t, field, ld in tensors:
+        if t is not None:
+            _shape(name, t, y.shape)
+            p, stride = _rows2d(name, t, y.dtype)
+            setattr(args, field, p)
+            setattr(args, ld, stride)
+
+
+def make_norm_residual_args(y, h=None, z=None, r=None, gate=None, w_post=None, w_pre=None, post_norm=None,
+                            residual_scale=1.0, eps=1e-6, weight_offset=0.0, q=None, q_scale=None,
+                            scale_mode=SCALES_FP32, num_rows=None):
+    """Fill a ``moe_norm_args`` from tensors: the branch y [M, H], the stream r and h (y's type or
+    float32), z like y, q [M, H] (float8_e4m3fn or uint8) with q_scale [M, H / 128].
+
+    gate: [H] one for each channel (the weights' type), [M, 1] one for each token (float32), [M, H]
+    (y's type).  post_norm: the branch is normed (w_post None: weight 1); by default it is where
+    w_post is given."""
+    args = MoeNormArgs()
+    M, H = _norm_common(args, y, gate, w_post, w_pre, w_post is not None if post_norm is None else post_norm, residual_scale,
+                        weight_offset, eps, num_rows)
+    _stream_rows(args, y, (("r", r, "r", "ldr"), ("h", h, "h", "ldh")))
+    _branch_rows(args, y, (("z", z, "z", "ldz"),))
+    if (q is None) != (q_scale is None):
+        raise ValueError("q and q_scale go together")
+    if q is not None:
+        if q.dtype not in (torch.float8_e4m3fn, torch.uint8):
+            raise ValueError(f"q: dtype {q.dtype}, expected {torch.float8_e4m3fn}")
+        _shape("q", q, (M, H))
+        _shape("q_scale", q_scale, (M, H // 128))
+        args.q, args.q_scale = _dense("q", q), _dense("q_scale", q_scale, torch.float32)
+    args.scale_mode = scale_mode
+    args._keepalive = (y, h, z, r, gate, w_post, w_pre, q, q_scale, num_rows)
+    return args
+
+
+def moe_norm_residual(args, stream=None):
+    _check("moe_norm_residual", load().moe_norm_residual(ctypes.byref(args), _stream(stream)))
+
+
+def moe_norm_residual_workspace_size(M, H):
+    return load().moe_norm_residual_workspace_size(M, H)
+
+
+def make_norm_residual_backward_args(y, dh=None, dz=None, h=None, gate=None, w_post=None, w_pre=None, post_norm=None,
+                                     residual_scale=1.0, eps=1e-6, weight_offset=0.0, dy=None, dr=None, dgate=None,
+                                     dw_post=None, dw_pre=None, workspace=None, accumulate=False, num_rows=None):
+    """Fill a ``moe_norm_backward_args``: the forward's y, h, gate and weights, the gradients dh (at h,
+    from the stream) and dz that arrive, and those asked for.  dw_post, dw_pre and a channel gate's
+    dgate are float32 [H], a token gate's float32 of its shape, a full one's like y."""
+    args = MoeNormBackwardArgs()
+    M, H = _norm_common(args, y, gate, w_post, w_pre, w_post is not None if post_norm is None else post_norm, residual_scale,
+                        weight_offset, eps, num_rows)
+    _stream_rows(args, y, (("h", h, "h", "ldh"), ("dh", dh, "dh", "lddh"), ("dr", dr, "dr", "lddr")))
+    _branch_rows(args, y, (("dz", dz, "dz", "lddz"), ("dy", dy, "dy", "lddy")))
+    if dgate is not None:
+        if gate is None:
+            raise ValueError("dgate: given without a gate")
+        _shape("dgate", dgate, gate.shape)
+        if args.gate_mode == GATE_FULL:
+            args.dgate, args.lddgate = _rows2d("dgate", dgate, y.dtype)
+        else:
+            args.dgate = _dense("dgate", dgate, torch.float32)
+    for name, t in (("dw_post", dw_post), ("dw_pre", dw_pre)):
+        if t is not None:
+            _shape(name, t, (H,))
+    args.dw_post, args.dw_pre = _opt("dw_post", dw_post, torch.float32), _opt("dw_pre", dw_pre, torch.float32)
+    if workspace is not None:
+        args.workspace = _dense("workspace", workspace)
+        args.workspace_bytes = workspace.numel() * workspace.element_size()
+    args.accumulate = 1 if accumulate else 0
+    args._keepalive = (y, dh, dz, h, gate, w_post, w_pre, dy, dr, dgate, dw_post, dw_pre, workspace, num_rows)
+    return args
+
+
+def moe_norm_residual_backward(args, stream=None):
+    _check("moe_norm_residual_backward", load().moe_norm_residual_backward(ctypes.byref(args), _stream(stream)))

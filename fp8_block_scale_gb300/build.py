@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libmoe_fp8.so")
 BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libmoe_fp8_debug.so")
 SOURCES = ["api.cu", "plan.cu", "prep.cu", "forward.cu", "vector.cu", "noalloc.cu", "router.cu", "w4a8.cu", "w4a8_tc.cu",
-           "rows.cu", "grouped.cu", "adamw.cu"]
+           "rows.cu", "grouped.cu", "adamw.cu", "route_scores.cu", "norm.cu", "norm_backward.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-I", os.path.join(ROOT, "include")]
