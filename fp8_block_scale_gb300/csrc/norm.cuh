@@ -84,6 +84,101 @@ __device__ __forceinline__ void row_sums(float (&v)[kN], float (*part)[kN][32], 
   turn ^= 1;
 }
 
+// ---- pairs of FP32 values: one instruction each for two (packed arithmetic of sm_100)
+
+__device__ __forceinline__ uint64_t bits2(float2 a) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ float2 pair2(uint64_t a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return pair2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return pair2(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return pair2(r);
+}
+__device__ __forceinline__ void copy4(const float2 (&a)[4], float2 (&b)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b[i] = a[i];
+}
+
+template <typename T>
+__device__ __forceinline__ void widen2(const Vec8<T>& r, float2 (&f)[4]) {
+  if constexpr (sizeof(T) == 4) {
+    const uint32_t w[8] = {r.v.x, r.v.y, r.v.z, r.v.w, r.w.x, r.w.y, r.w.z, r.w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+  } else {
+    const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = Pack2<T>::load(w[i]);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store2(T* p, const float2 (&f)[4]) {
+  uint4* q = reinterpret_cast<uint4*>(p);
+  if constexpr (sizeof(T) == 4) {
+    q[0] = make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y));
+    q[1] = make_uint4(__float_as_uint(f[2].x), __float_as_uint(f[2].y), __float_as_uint(f[3].x), __float_as_uint(f[3].y));
+  } else {
+    q[0] = make_uint4(Pack2<T>::store(f[0].x, f[0].y), Pack2<T>::store(f[1].x, f[1].y), Pack2<T>::store(f[2].x, f[2].y),
+                      Pack2<T>::store(f[3].x, f[3].y));
+  }
+}
+template <typename T>
+__device__ __forceinline__ void weights2(const void* w, int wide, int c, float offset, float2 (&f)[4]) {
+  if (!w) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = both(1.f);
+    return;
+  }
+  if (wide)
+    widen2<float>(load_vec<float>(static_cast<const float*>(w) + c), f);
+  else
+    widen2<T>(load_vec<T>(static_cast<const T*>(w) + c), f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = add2(f[i], both(offset));
+}
+
+// Sums over a row by its team, one of several in a CTA: whole warps, by shuffles and, for more
+// than one, through shared memory with a barrier of its own (two buffers in turn: the
+// next call writes the other one).  Every thread gets the same bits.
+template <int kN>
+__device__ __forceinline__ void team_sums(float (&v)[kN], float (*part)[3][32], int& turn, int team, int index) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int n = 0; n < kN; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
+  if (team == 32) return;
+  const int lane = threadIdx.x % 32, warps = team / 32, first = index * warps;
+  if (lane == 0)
+#pragma unroll
+    for (int n = 0; n < kN; ++n) part[turn][n][threadIdx.x / 32] = v[n];
+  named_barrier(1 + index, team);
+#pragma unroll
+  for (int n = 0; n < kN; ++n) v[n] = lane < warps ? part[turn][n][first + lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int n = 0; n < kN; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
+  turn ^= 1;
+}
+
 // ---------------------------------------------------------------- host side
 
 // A buffer an entry point was given: rows of `width` bytes, `ld` bytes apart.

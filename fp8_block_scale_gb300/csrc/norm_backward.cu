@@ -5,6 +5,9 @@
 // a channel gate's) gather in registers, each thread's columns over all of its
 // rows; every CTA leaves its sums in the workspace, and a second launch adds
 // them in a fixed order.
+#include <atomic>
+#include <type_traits>
+
 #include "norm.cuh"
 
 namespace moe {
@@ -12,225 +15,454 @@ namespace {
 
 constexpr int kMaxParts = 320;      // CTAs whose sums over rows the workspace holds
 constexpr int kSums = 3;            // dw_pre, dw_post, a channel gate's
+constexpr int kHeld = 2;            // ... of which the last two are one sum times the other's factor
+
+// Rows of an input or output: the next one `ld` bytes further on.
+struct RowsOf {
+  const void* p;
+  int64_t ld;
+  // This thread's part of row `row`, `offset` bytes into it; kNear: ld has 32 bits.
+  template <bool kNear>
+  __device__ __forceinline__ uint8_t* at(int64_t row, uint32_t offset) const {
+    uint8_t* base = static_cast<uint8_t*>(const_cast<void*>(p)) + offset;
+    if constexpr (kNear)
+      return base + static_cast<uint64_t>(static_cast<uint32_t>(row)) * static_cast<uint32_t>(ld);
+    else
+      return base + row * ld;
+  }
+};
 
 struct NormGradParams {
-  const void* y;
-  const void* h;
-  const void* gate;
+  RowsOf y, h, gate, dh, dz, dy, dr, dgate;
   const void* w_post;
   const void* w_pre;
-  const void* dh;
-  const void* dz;
-  void* dy;
-  void* dr;
-  void* dgate;
   float* parts;                     // [kSums, CTAs, H]
   const int32_t* num_rows;
-  int64_t M, ldy, ldh, ldgate, lddh, lddz, lddy, lddr, lddgate;
+  int64_t M;
   int H, wide, gate_mode, post_norm;
   int sums;                         // bit n: sum n is asked for
+  int team;                         // threads of a row
+  int stages;                       // rows of a team in shared memory
   float residual_scale, weight_offset, eps;
 };
 
-template <typename Tb, typename Ts, int kVec, bool kWarpRow>
-__global__ void __launch_bounds__(kWarpRow ? 256 : 1024) norm_backward_kernel(const __grid_constant__ NormGradParams p) {
-  __shared__ float part[2][3][32];
-  extern __shared__ float gathered[];
+// The row sums that everything else follows from, with k = gate y (w_post + offset) and
+// t = dz (w_pre + offset): one round of them, because the sum that the branch's norm needs is
+// linear in dH:  sum k dH = sum k dh + R_h sum k t - R_h^3 mean(t h) sum k h.
+enum { kHH, kTH, kYY, kKD, kKT, kKH, kRowSums = 8 };
+
+// Sums of eight values over a warp: lane l ends with the total of value (l / 4) % 8.
+__device__ __forceinline__ float warp_sums8(float (&v)[8], int lane) {
+#pragma unroll
+  for (int half = 4; half > 0; half /= 2) {
+    const int o = 4 * half;
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float give = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
+  v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+}
+// The totals over a team's warps' parts [warps][8]: lane l adds value l % 8 of every fourth warp.
+__device__ __forceinline__ void join_sums8(const float* parts, int warps, int lane, float (&v)[8]) {
+  float sum = 0.f;
+  const float* mine = parts + lane;
+  const int more = warps - lane / 8;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (4 * i < more) sum += mine[32 * i];
+  sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+  sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+#pragma unroll
+  for (int i = 0; i <= kKH; ++i) v[i] = __shfl_sync(0xffffffffu, sum, i);
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void put16(uint32_t at, float2 a, float2 b) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y) : "memory");
+}
+__device__ __forceinline__ uint4 shared16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+template <typename T> constexpr int kPieces = static_cast<int>(sizeof(T)) / 2;
+constexpr int kPiece = 512;         // bytes of 16 for each lane of a warp
+
+// What a fixed variant keeps in shared memory: for each warp of a team the weights (pre; post, or
+// the channel gate, or their product) in FP32, which its teams share, then for each warp
+// p.stages times the pieces of a row's inputs (y, dz, h, dh, gate).
+template <typename Tb, typename Ts, int kPre, int kPost, int kGate>
+struct Layout {
+  static constexpr int kB = kPieces<Tb>, kS = kPieces<Ts>;
+  static constexpr int kAtZ = kB, kAtH = kAtZ + (kPre ? kB : 0), kAtD = kAtH + (kPre ? kS : 0), kAtG = kAtD + kS,
+                       kUnits = kAtG + (kGate == MOE_GATE_FULL ? kB : 0);
+  static constexpr int kAtPost = kPre ? 2 : 0, kWeights = kAtPost + (kPost || kGate == MOE_GATE_CHANNEL ? 2 : 0);
+  // bytes of `teams` teams of `team` threads
+  static __host__ __device__ constexpr int bytes(int team, int teams, int stages) {
+    return (kWeights + teams * stages * kUnits) * (kPiece / 32) * team;
+  }
+};
+constexpr int kMostStages = 3;      // (a fourth takes L1 and gives nothing; two: 8192 x 4096 75 us against 69 without post_norm)
+// Threads of a fixed variant's CTA, by registers.  Up to 512 a thread keeps a row's vectors from
+// the sums to the outputs (65536 rows of 256 columns: 39 us, 52 with 1024 threads that read
+// shared memory twice); 7168 columns take 896, whose 72 registers just hold a thread's share: with
+// the 64 of 1024 threads a few bytes spill, and beside a full shared memory the L1 has no room
+// for them (16384 x 7168 with a full gate: 419 us against 305).
+constexpr int kKeepThreads = 512, kFixedThreads = 896, kAnyThreads = 1024;
+
+// A row's team is `team` threads with kVec vectors each; a CTA holds as many teams as fit, and
+// each takes its own rows.  All sums of a row are formed in one round, so that its one barrier
+// and the shuffles around it are what is not hidden; meanwhile the next rows'
+// inputs are on their way into shared memory, every thread's vectors to its own place (the
+// copies need no barrier), and with them HBM stays busy.
+//
+// kPre (dz and h given), kPost, kGate (a token's as none: it is a number): a variant fixed
+// at compile time, its rows and weights in shared memory, kVec 1.  Branches on run-time flags cost
+// 40% more instructions and, because loads do not move across them, half of the speed;
+// weights from memory cost another 20%: they fall out of the L1 beside a full shared
+// memory.  kPre = -1: any variant, from memory itself.
+template <typename Tb, typename Ts, int kVec, int kPre, int kPost, int kGate, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1) norm_backward_kernel(const __grid_constant__ NormGradParams p) {
+  constexpr bool kFixed = kPre >= 0;
+  using At = Layout<Tb, Ts, kPre == 1, kPost == 1, kGate>;
+  static_assert(!kFixed || kVec == 1, "one vector a thread");
+  constexpr bool kShared = kFixed && sizeof(Ts) == 4;      // a warp's FP32 pieces are its lanes' together
+  constexpr bool kKeep = kFixed && kThreads <= kKeepThreads;
+  __shared__ float s_parts[2][kThreads / 32][kRowSums];
+  extern __shared__ __align__(16) uint8_t memory[];
   pdl_wait();
   pdl_launch_dependents();
-  int turn = 0;
-  const int team = kWarpRow ? 32 : blockDim.x, tid = kWarpRow ? threadIdx.x % 32 : threadIdx.x;
-  const int64_t live = p.num_rows ? min(static_cast<int64_t>(max(*p.num_rows, 0)), p.M) : p.M;
-  const int64_t row0 = kWarpRow ? static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
-  const int64_t step = kWarpRow ? static_cast<int64_t>(gridDim.x) * (blockDim.x / 32) : gridDim.x;
+  const int team = p.team, mine = threadIdx.x / team, tid = threadIdx.x - mine * team, teams = blockDim.x / team;
+  const int lane = threadIdx.x % 32, warps = team / 32;
+  const int gate = kFixed ? kGate : p.gate_mode == MOE_GATE_TOKEN ? MOE_GATE_NONE : p.gate_mode;
+  const bool post = kFixed ? kPost != 0 : p.post_norm != 0, pre = kFixed ? kPre != 0 : p.dz.p != nullptr;
+  const bool own_h = kFixed ? kPre != 0 : p.h.p != nullptr, has_dh = p.dh.p != nullptr;
+  const bool token_gate = gate == MOE_GATE_NONE && p.gate_mode == MOE_GATE_TOKEN;
+  const bool dots = post || (token_gate && p.dgate.p);
+  const uint32_t M = static_cast<uint32_t>(p.M), live = p.num_rows ? min(static_cast<uint32_t>(max(*p.num_rows, 0)), M) : M;
+  const uint32_t step = gridDim.x * teams;
   const float inv_h = 1.f / static_cast<float>(p.H);
-  float acc[kSums][kVec][8];
+  // a piece of 16-bit elements is the lane's own; of FP32 the warp's 1024 bytes come (and go) in two
+  // runs of 512, so that whole sectors move, at places that a lane reads its 32 bytes from without conflicts
+  const uint32_t mine16 = 16u * lane, run16 = 16u * (lane ^ ((lane >> 3) & 1)), low16 = 32u * lane + 16u * ((lane >> 2) & 1),
+                 high16 = low16 ^ 16u;
+  const uint32_t of_weights = (tid / 32) * (At::kWeights * kPiece) + 16u * lane, w_at = smem_u32(memory) + of_weights;
+  auto column = [&](int v) { return 8 * (tid + v * team); };
+
+  // one vector of an input of row `row`, which is at `at` in shared memory
+  auto get = [&](auto* type, const RowsOf& rows, int piece, uint32_t at, uint32_t row, int c, float2 (&f)[4]) {
+    using T = std::remove_pointer_t<decltype(type)>;
+    Vec8<T> r;
+    if constexpr (kFixed) {
+      if constexpr (sizeof(T) == 4) {
+        r.v = shared16((at + low16) + piece * kPiece);
+        r.w = shared16((at + high16) + piece * kPiece);
+      } else {
+        r.v = shared16((at + mine16) + piece * kPiece);
+      }
+    } else {
+      r = load_vec<T>(reinterpret_cast<const T*>(rows.at<false>(row, c * sizeof(T))));
+    }
+    widen2<T>(r, f);
+  };
+  Tb* const of_branch = nullptr;
+  Ts* const of_stream = nullptr;
+  auto weights = [&](int piece, float2 (&f)[4]) {
+    widen2<float>(Vec8<float>{shared16(w_at + piece * kPiece), shared16(w_at + (piece + 1) * kPiece)}, f);
+  };
+
+  // the columns' factor of the branch: its norm's weights, a channel gate, or their product
+  auto factor = [&](int c, float2 (&f)[4]) {
+    if (post) weights2<Tb>(p.w_post, p.wide, c, p.weight_offset, f);
+    if (gate == MOE_GATE_CHANNEL) {
+      float2 g[4];
+      weights2<Tb>(p.gate.p, p.wide, c, 0.f, g);
 #pragma unroll
-  for (int n = 0; n < kSums; ++n)
+      for (int i = 0; i < 4; ++i) f[i] = post ? mul2(f[i], g[i]) : g[i];
+    }
+  };
+
+  auto fetch_row = [&](uint32_t at, uint32_t row) {
+    if constexpr (kFixed) {
+      if (row < live) {
+        const int c = column(0), c4 = c - 4 * lane;        // (FP32: four columns a lane, 128 further on the others)
+        auto bring = [&](int piece, int pieces, const RowsOf& rows) {
+          if (pieces == 1) {
+            if (c < p.H) copy16((at + mine16) + piece * kPiece, rows.at<true>(row, 2 * c));
+          } else {
+            if (c4 < p.H) copy16((at + run16) + piece * kPiece, rows.at<true>(row, 4 * c4));
+            if (c4 + 128 < p.H) copy16((at + run16) + (piece + 1) * kPiece, rows.at<true>(row, 4 * c4 + 512));
+          }
+        };
+        bring(0, At::kB, p.y);
+        if (pre) bring(At::kAtZ, At::kB, p.dz), bring(At::kAtH, At::kS, p.h);
+        if (has_dh) bring(At::kAtD, At::kS, p.dh);
+        if (gate == MOE_GATE_FULL) bring(At::kAtG, At::kB, p.gate);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  };
+  // one vector of an output: to memory, or (FP32, fixed variants) to the place of an input that
+  // has been used, from where flush_row takes it
+  auto put = [&](auto* type, const RowsOf& rows, int piece, uint32_t at, uint32_t row, int c, const float2 (&f)[4]) {
+    using T = std::remove_pointer_t<decltype(type)>;
+    if constexpr (kFixed && sizeof(T) == 4) {
+      put16((at + low16) + piece * kPiece, f[0], f[1]);
+      put16((at + high16) + piece * kPiece, f[2], f[3]);
+    } else {
+      store2<T>(reinterpret_cast<T*>(rows.at<kFixed>(row, c * sizeof(T))), f);
+    }
+  };
+  auto flush = [&](const RowsOf& rows, int piece, uint32_t at, uint32_t row) {
+    const int c4 = column(0) - 4 * lane;
+    if (c4 < p.H) *reinterpret_cast<uint4*>(rows.at<kFixed>(row, 4 * c4)) = shared16((at + run16) + piece * kPiece);
+    if (c4 + 128 < p.H) *reinterpret_cast<uint4*>(rows.at<kFixed>(row, 4 * c4 + 512)) = shared16((at + run16) + (piece + 1) * kPiece);
+  };
+
+  if constexpr (kFixed) {
+    const int c = column(0);
+    if (mine == 0 && c < p.H) {
+      auto keep = [&](const float2 (&f)[4], int piece) {
+        float4* to = reinterpret_cast<float4*>(memory + of_weights + piece * kPiece);
+        to[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+        to[kPiece / 16] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+      };
+      float2 f[4];
+      if (pre) {
+        weights2<Tb>(p.w_pre, p.wide, c, p.weight_offset, f);
+        keep(f, 0);
+      }
+      if (post || gate == MOE_GATE_CHANNEL) {
+        factor(c, f);
+        keep(f, At::kAtPost);
+      }
+    }
+    if (teams > 1) __syncthreads();
+  }
+
+  float2 acc[kHeld][kVec][4];
+#pragma unroll
+  for (int n = 0; n < kHeld; ++n)
 #pragma unroll
     for (int v = 0; v < kVec; ++v)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[n][v][i] = 0.f;
+      for (int i = 0; i < 4; ++i) acc[n][v][i] = make_float2(0.f, 0.f);
 
-  for (int64_t row = row0; row < live; row += step) {
-    Vec8<Tb> yr[kVec], zr[kVec], gr[kVec];
-    Vec8<Ts> hr[kVec], dr[kVec];
+  uint32_t row = blockIdx.x * teams + mine;
+  // the stages in turn: `at` holds this row, `free` is for the row stages - 1 further on
+  const uint32_t first = smem_u32(memory) + (team / 32) * (At::kWeights * kPiece) +
+                         (threadIdx.x / 32) * (p.stages * (At::kUnits * kPiece));
+  const uint32_t end = first + p.stages * (At::kUnits * kPiece);
+  uint32_t at = first, free = first;
+  int turn = 0;
+  if constexpr (kFixed) {
+    for (int i = 0; i < p.stages - 1; ++i, free += At::kUnits * kPiece) fetch_row(free, row + i * step);
+  }
+  for (; row < live; row += step) {
+    if constexpr (kShared) __syncwarp();    // (every lane is done with the row that was there)
+    fetch_row(free, row + (p.stages - 1) * step);
+    if constexpr (kFixed) {
+      if (p.stages == 4)
+        asm volatile("cp.async.wait_group 3;" ::: "memory");
+      else if (p.stages == 3)
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+      else
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      if constexpr (kShared) __syncwarp();  // (the other lanes' copies)
+    }
+    // the row's inputs and the weights as they are needed; kKeep: once for both uses
+    float2 y[4], x[4] = {}, z[4] = {}, d[4] = {}, g[4], w_pre[4], w[4];
+    float2 sum[6] = {};
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
-      const int c = 8 * (tid + v * team);
+      const int c = column(v);
       if (c < p.H) {
-        yr[v] = load_vec<Tb>(static_cast<const Tb*>(p.y) + row * p.ldy + c);
-        if (p.dz) {
-          zr[v] = load_vec<Tb>(static_cast<const Tb*>(p.dz) + row * p.lddz + c);
-          if (p.h) hr[v] = load_vec<Ts>(static_cast<const Ts*>(p.h) + row * p.ldh + c);
+        float2 k[4];
+        get(of_branch, p.y, 0, at, row, c, y);
+        if (pre) {
+          if constexpr (kFixed) weights(0, w_pre); else weights2<Tb>(p.w_pre, p.wide, c, p.weight_offset, w_pre);
+          if (own_h) get(of_stream, p.h, At::kAtH, at, row, c, x); else copy4(y, x);
+          get(of_branch, p.dz, At::kAtZ, at, row, c, z);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            sum[kHH] = fma2(x[i], x[i], sum[kHH]);
+            sum[kTH] = fma2(mul2(z[i], w_pre[i]), x[i], sum[kTH]);
+          }
         }
-        if (p.dh) dr[v] = load_vec<Ts>(static_cast<const Ts*>(p.dh) + row * p.lddh + c);
-        if (p.gate_mode == MOE_GATE_FULL) gr[v] = load_vec<Tb>(static_cast<const Tb*>(p.gate) + row * p.ldgate + c);
+        if (kKeep || dots) {
+          copy4(y, k);
+          if (post || gate == MOE_GATE_CHANNEL) {
+            if constexpr (kFixed) weights(At::kAtPost, w); else factor(c, w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (post) sum[kYY] = fma2(y[i], y[i], sum[kYY]);
+              k[i] = mul2(y[i], w[i]);
+            }
+          }
+          if (gate == MOE_GATE_FULL) {
+            get(of_branch, p.gate, At::kAtG, at, row, c, g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) k[i] = mul2(k[i], g[i]);
+          }
+          if (has_dh) {
+            get(of_stream, p.dh, At::kAtD, at, row, c, d);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[kKD] = fma2(k[i], d[i], sum[kKD]);
+          }
+          if (pre) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              sum[kKT] = fma2(k[i], mul2(z[i], w_pre[i]), sum[kKT]);
+              sum[kKH] = fma2(k[i], x[i], sum[kKH]);
+            }
+          }
+        }
       }
     }
-    // first round: squares of h and y, and dz w h
-    float sum[3] = {0.f, 0.f, 0.f};
+    float s[8] = {};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) s[i] = sum[i].x + sum[i].y;
+    const float total = warp_sums8(s, lane);
+    if (lane % 4 == 0) s_parts[turn][threadIdx.x / 32][lane / 4] = total;
+    if (warps == 1)
+      __syncwarp();
+    else
+      named_barrier(1 + mine, team);
+    join_sums8(&s_parts[turn][mine * warps][0], warps, lane, s);
+    turn ^= 1;                              // (the next row's parts: a thread behind still reads these)
+    const float root_h = pre ? rsqrtf(fmaf(s[kHH], inv_h, p.eps)) : 0.f, root_y = post ? rsqrtf(fmaf(s[kYY], inv_h, p.eps)) : 1.f;
+    const float back_h = pre ? root_h * root_h * root_h * (s[kTH] * inv_h) : 0.f;
+    const float token = token_gate ? __ldg(static_cast<const float*>(p.gate.p) + row) : 1.f;
+    const float dot = fmaf(root_h, s[kKT], s[kKD]) - back_h * s[kKH];      // sum k dH (without a token's gate)
+    const float back_y = post ? root_y * root_y * root_y * (token * dot * inv_h) : 0.f;
+    if (token_gate && p.dgate.p && tid == 0) static_cast<float*>(const_cast<void*>(p.dgate.p))[row] = root_y * dot;
+    const float2 rh2 = both(root_h), bh2 = both(-back_h), ry2 = both(root_y), by2 = both(-back_y), token2 = both(token);
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
-      const int c = 8 * (tid + v * team);
+      const int c = column(v);
       if (c < p.H) {
-        float x[8];
-        if (p.dz) {
-          float z[8], w[8];
-          if (p.h) widen<Ts>(hr[v], x); else widen<Tb>(yr[v], x);
-          widen<Tb>(zr[v], z);
-          load_weights<Tb>(p.w_pre, p.wide, c, p.weight_offset, w);
+        if (!kKeep) {
+          get(of_branch, p.y, 0, at, row, c, y);
+          if (has_dh) {
+            get(of_stream, p.dh, At::kAtD, at, row, c, d);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            sum[0] = fmaf(x[i], x[i], sum[0]);
-            sum[1] = fmaf(z[i] * w[i], x[i], sum[1]);
+            for (int i = 0; i < 4; ++i) d[i] = make_float2(0.f, 0.f);
           }
         }
-        if (p.post_norm) {
-          widen<Tb>(yr[v], x);
+        if (pre) {
+          if (!kKeep) {
+            if constexpr (kFixed) weights(0, w_pre); else weights2<Tb>(p.w_pre, p.wide, c, p.weight_offset, w_pre);
+            if (own_h) get(of_stream, p.h, At::kAtH, at, row, c, x); else copy4(y, x);
+            get(of_branch, p.dz, At::kAtZ, at, row, c, z);
+          }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum[2] = fmaf(x[i], x[i], sum[2]);
+          for (int i = 0; i < 4; ++i) {
+            z[i] = mul2(z[i], rh2);
+            acc[0][v][i] = fma2(z[i], x[i], acc[0][v][i]);
+            d[i] = fma2(z[i], w_pre[i], fma2(x[i], bh2, d[i]));
+          }
         }
+        if (p.dr.p) {
+          float2 o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = mul2(d[i], both(p.residual_scale));
+          put(of_stream, p.dr, At::kAtD, at, row, c, o);
+        }
+        if ((post || gate == MOE_GATE_CHANNEL) && !kKeep) {
+          if constexpr (kFixed) weights(At::kAtPost, w); else factor(c, w);
+        }
+        if (gate == MOE_GATE_FULL) {
+          float2 o[4];                      // dH u, u = y R(y) (w_post + offset) or y
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            o[i] = mul2(d[i], y[i]);
+            if (post) o[i] = mul2(mul2(o[i], w[i]), ry2);
+          }
+          if (!kKeep) get(of_branch, p.gate, At::kAtG, at, row, c, g);
+          if (p.dgate.p) put(of_branch, p.dgate, At::kAtG, at, row, c, o);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[i] = mul2(d[i], g[i]);
+        } else if (gate == MOE_GATE_NONE) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[i] = mul2(d[i], token2);
+        }
+        if (post || gate == MOE_GATE_CHANNEL) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            d[i] = mul2(d[i], ry2);
+            acc[1][v][i] = fma2(d[i], y[i], acc[1][v][i]);
+            d[i] = post ? fma2(d[i], w[i], mul2(y[i], by2)) : mul2(d[i], w[i]);
+          }
+        }
+        if (p.dy.p) put(of_branch, p.dy, 0, at, row, c, d);
       }
     }
-    row_sums<3, kWarpRow>(sum, part, turn);
-    const float root_h = rsqrtf(fmaf(sum[0], inv_h, p.eps)), root_y = p.post_norm ? rsqrtf(fmaf(sum[2], inv_h, p.eps)) : 1.f;
-    const float back_h = root_h * root_h * root_h * (sum[1] * inv_h);
-    const float token = p.gate_mode == MOE_GATE_TOKEN ? __ldg(static_cast<const float*>(p.gate) + row) : 1.f;
-
-    // second round: dH, and with it du w y (a token gate's share of it once for the row)
-    float d[kVec][8];
-    float dot[3] = {0.f, 0.f, 0.f};
-#pragma unroll
-    for (int v = 0; v < kVec; ++v) {
-      const int c = 8 * (tid + v * team);
-      if (c < p.H) {
-        if (p.dh) {
-          widen<Ts>(dr[v], d[v]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) d[v][i] = 0.f;
-        }
-        float y[8];
-        widen<Tb>(yr[v], y);
-        if (p.dz) {
-          float x[8], z[8], w[8];
-          if (p.h) widen<Ts>(hr[v], x); else widen<Tb>(yr[v], x);
-          widen<Tb>(zr[v], z);
-          load_weights<Tb>(p.w_pre, p.wide, c, p.weight_offset, w);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            acc[0][v][i] = fmaf(z[i] * x[i], root_h, acc[0][v][i]);
-            d[v][i] = fmaf(z[i] * w[i], root_h, fmaf(-x[i], back_h, d[v][i]));
-          }
-        }
-        if (p.dr) {
-          float o[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = p.residual_scale * d[v][i];
-          store_vec<Ts>(static_cast<Ts*>(p.dr) + row * p.lddr + c, o);
-        }
-        float u[8];                       // y R(y) (w + offset), or y
-        float w[8];
-        if (p.post_norm) {
-          load_weights<Tb>(p.w_post, p.wide, c, p.weight_offset, w);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) u[i] = y[i] * root_y * w[i];
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) u[i] = y[i];
-        }
-        if (p.gate_mode == MOE_GATE_TOKEN) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            dot[1] = fmaf(d[v][i], u[i], dot[1]);
-            d[v][i] *= token;
-          }
-        } else if (p.gate_mode == MOE_GATE_CHANNEL) {
-          float g[8];
-          load_weights<Tb>(p.gate, p.wide, c, 0.f, g);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            acc[2][v][i] = fmaf(d[v][i], u[i], acc[2][v][i]);
-            d[v][i] *= g[i];
-          }
-        } else if (p.gate_mode == MOE_GATE_FULL) {
-          float g[8], o[8];
-          widen<Tb>(gr[v], g);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            o[i] = d[v][i] * u[i];
-            d[v][i] *= g[i];
-          }
-          if (p.dgate) store_vec<Tb>(static_cast<Tb*>(p.dgate) + row * p.lddgate + c, o);
-        }
-        if (p.post_norm) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            acc[1][v][i] = fmaf(d[v][i] * y[i], root_y, acc[1][v][i]);
-            dot[0] = fmaf(d[v][i] * w[i], y[i], dot[0]);
-          }
-        }
+    if constexpr (kShared) {
+      __syncwarp();
+      if (p.dr.p) flush(p.dr, At::kAtD, at, row);
+      if constexpr (sizeof(Tb) == 4) {
+        if (gate == MOE_GATE_FULL && p.dgate.p) flush(p.dgate, At::kAtG, at, row);
+        if (p.dy.p) flush(p.dy, 0, at, row);
       }
     }
-    float back_y = 0.f;
-    if (p.post_norm || (p.gate_mode == MOE_GATE_TOKEN && p.dgate)) {
-      row_sums<3, kWarpRow>(dot, part, turn);
-      back_y = root_y * root_y * root_y * (dot[0] * inv_h);
-      if (p.gate_mode == MOE_GATE_TOKEN && p.dgate && tid == 0) static_cast<float*>(p.dgate)[row] = dot[1];
-    }
-    if (p.dy) {
-#pragma unroll
-      for (int v = 0; v < kVec; ++v) {
-        const int c = 8 * (tid + v * team);
-        if (c < p.H) {
-          if (p.post_norm) {
-            float w[8], y[8];
-            load_weights<Tb>(p.w_post, p.wide, c, p.weight_offset, w);
-            widen<Tb>(yr[v], y);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) d[v][i] = fmaf(d[v][i] * w[i], root_y, -(y[i] * back_y));
-          }
-          store_vec<Tb>(static_cast<Tb*>(p.dy) + row * p.lddy + c, d[v]);
-        }
-      }
-    }
+    free = at;
+    at = at + At::kUnits * kPiece == end ? first : at + At::kUnits * kPiece;
   }
 
   if (!p.sums) return;
-  if (kWarpRow) {
-    // the CTA's warps one after another into shared memory, then out
-    const int warp = threadIdx.x / 32, warps = blockDim.x / 32;
-    for (int w = 0; w < warps; ++w) {
-      if (w == warp) {
+  // the teams' sums one after another into the first one's, then out
+  if constexpr (kFixed) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  float2* gathered = reinterpret_cast<float2*>(memory);
+  for (int m = 1; m < teams; ++m) {
+    __syncthreads();                             // (the ring, then the last team's sums, are no longer read)
+    if (mine == m) {
 #pragma unroll
-        for (int n = 0; n < kSums; ++n)
+      for (int n = 0; n < kHeld; ++n)
 #pragma unroll
-          for (int v = 0; v < kVec; ++v) {
-            const int c = 8 * (tid + v * team);
-            if (c < p.H)
+        for (int v = 0; v < kVec; ++v)
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                float* at = gathered + n * p.H + c + i;
-                *at = w == 0 ? acc[n][v][i] : *at + acc[n][v][i];
-              }
-          }
-      }
-      __syncthreads();
+          for (int i = 0; i < 4; ++i) gathered[((n * kVec + v) * 4 + i) * team + tid] = acc[n][v][i];
     }
-    for (int n = 0; n < kSums; ++n)
-      if ((p.sums >> n) & 1)
-        for (int c = threadIdx.x; c < p.H; c += blockDim.x)
-          p.parts[(static_cast<int64_t>(n) * gridDim.x + blockIdx.x) * p.H + c] = gathered[n * p.H + c];
-  } else {
+    __syncthreads();
+    if (mine == 0) {
 #pragma unroll
-    for (int n = 0; n < kSums; ++n)
-      if ((p.sums >> n) & 1)
+      for (int n = 0; n < kHeld; ++n)
 #pragma unroll
-        for (int v = 0; v < kVec; ++v) {
-          const int c = 8 * (tid + v * team);
-          if (c < p.H) store_vec<float>(p.parts + (static_cast<int64_t>(n) * gridDim.x + blockIdx.x) * p.H + c, acc[n][v]);
+        for (int v = 0; v < kVec; ++v)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[n][v][i] = add2(acc[n][v][i], gathered[((n * kVec + v) * 4 + i) * team + tid]);
+    }
+  }
+  if (mine == 0) {
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) {
+      const int c = column(v);
+      if (c < p.H) {
+        auto leave = [&](int n, const float2 (&f)[4]) {
+          if ((p.sums >> n) & 1) store2<float>(p.parts + (static_cast<int64_t>(n) * gridDim.x + blockIdx.x) * p.H + c, f);
+        };
+        leave(0, acc[0][v]);
+        if (gate == MOE_GATE_CHANNEL) {
+          // one sum, dH y R(y), times what each gradient has beside it
+          float2 f[4], g[4];
+          weights2<Tb>(p.gate.p, p.wide, c, 0.f, g);
+          weights2<Tb>(post ? p.w_post : nullptr, p.wide, c, p.weight_offset, f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) g[i] = mul2(g[i], acc[1][v][i]), f[i] = mul2(f[i], acc[1][v][i]);
+          leave(1, g);
+          leave(2, f);
+        } else {
+          leave(1, acc[1][v]);
         }
+      }
+    }
   }
 }
 
@@ -259,21 +491,64 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__
   }
 }
 
+constexpr int kMostShared = 224 * 1024;
+
+template <typename Tb, typename Ts, int kVec, int kPre, int kPost, int kGate, int kThreads>
+cudaError_t launch_teams(NormGradParams& p, int sms, int* ctas, cudaStream_t stream) {
+  constexpr bool kFixed = kPre >= 0;
+  using At = Layout<Tb, Ts, kPre == 1, kPost == 1, kGate>;
+  p.team = team_threads(p.H / 8, kVec);
+  // teams: as many as threads, named barriers and shared memory allow, but first one on every SM;
+  // then as many stages as fit
+  int teams = kThreads / p.team;
+  if (p.team > 32 && teams > 15) teams = 15;
+  while (kFixed && teams > 1 && At::bytes(p.team, teams, 2) > kMostShared) --teams;
+  const int64_t rows = p.M < 1 ? 1 : p.M;
+  if (ceil_div(rows, sms) < teams) teams = static_cast<int>(ceil_div(rows, sms));
+  const int threads = p.team * teams;
+  const int64_t want = ceil_div(rows, teams);
+  *ctas = static_cast<int>(want < sms ? want : sms < kMaxParts ? sms : kMaxParts);
+  p.stages = 2;
+  while (kFixed && p.stages < kMostStages && At::bytes(p.team, teams, p.stages + 1) <= kMostShared) ++p.stages;
+  const int held = kFixed ? At::bytes(p.team, teams, p.stages) : 0, join = teams > 1 ? kHeld * kVec * 32 * p.team : 0;
+  auto kernel = norm_backward_kernel<Tb, Ts, kVec, kPre, kPost, kGate, kThreads>;
+  static std::atomic<bool> sized[64];            // per device: the attribute outlasts the call
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err == cudaSuccess && (dev >= 64 || !sized[dev].load())) {
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
+    if (err == cudaSuccess && dev < 64) sized[dev].store(true);
+  }
+  if (err != cudaSuccess) return err;
+  return launch_pdl(kernel, dim3(*ctas), dim3(threads), static_cast<size_t>(held > join ? held : join), stream, 1, p);
+}
+
+// The fixed variant where a row of it fits, else the one for any.
+template <typename Tb, typename Ts, int kPre, int kPost, int kGate>
+cudaError_t launch_fixed(NormGradParams& p, int sms, int* ctas, cudaStream_t stream) {
+  const int team = team_threads(p.H / 8, 1);
+  return Layout<Tb, Ts, kPre, kPost, kGate>::bytes(team, 1, 2) > kMostShared ? launch_teams<Tb, Ts, 1, -1, -1, -1, kAnyThreads>(p, sms, ctas, stream)
+         : team <= kKeepThreads     ? launch_teams<Tb, Ts, 1, kPre, kPost, kGate, kKeepThreads>(p, sms, ctas, stream)
+         : team <= kFixedThreads    ? launch_teams<Tb, Ts, 1, kPre, kPost, kGate, kFixedThreads>(p, sms, ctas, stream)
+                                    : launch_teams<Tb, Ts, 1, kPre, kPost, kGate, kAnyThreads>(p, sms, ctas, stream);
+}
+template <typename Tb, typename Ts, int kPre, int kPost>
+cudaError_t launch_gate(NormGradParams& p, int sms, int* ctas, cudaStream_t stream) {
+  return p.gate_mode == MOE_GATE_FULL      ? launch_fixed<Tb, Ts, kPre, kPost, MOE_GATE_FULL>(p, sms, ctas, stream)
+         : p.gate_mode == MOE_GATE_CHANNEL ? launch_fixed<Tb, Ts, kPre, kPost, MOE_GATE_CHANNEL>(p, sms, ctas, stream)
+                                           : launch_fixed<Tb, Ts, kPre, kPost, MOE_GATE_NONE>(p, sms, ctas, stream);
+}
+
 template <typename Tb, typename Ts>
 cudaError_t launch_backward(NormGradParams& p, int sms, int* ctas, cudaStream_t stream) {
-  const int vecs = p.H / 8;
-  const int64_t most = 2 * sms < kMaxParts ? 2 * sms : kMaxParts;
-  if (vecs <= 64) {
-    const int64_t want = ceil_div(p.M, 8);
-    *ctas = static_cast<int>(want < 1 ? 1 : want < most ? want : most);
-    const size_t smem = static_cast<size_t>(kSums) * p.H * 4;
-    return vecs <= 32 ? launch_pdl(norm_backward_kernel<Tb, Ts, 1, true>, dim3(*ctas), dim3(256), smem, stream, 1, p)
-                      : launch_pdl(norm_backward_kernel<Tb, Ts, 2, true>, dim3(*ctas), dim3(256), smem, stream, 1, p);
-  }
-  *ctas = static_cast<int>(p.M < 1 ? 1 : p.M < most ? p.M : most);
-  if (vecs <= 512)
-    return launch_pdl(norm_backward_kernel<Tb, Ts, 1, false>, dim3(*ctas), dim3(team_threads(vecs, 1)), 0, stream, 1, p);
-  return launch_pdl(norm_backward_kernel<Tb, Ts, 2, false>, dim3(*ctas), dim3(team_threads(vecs, 2)), 0, stream, 1, p);
+  if (p.H > 8 * kAnyThreads) return launch_teams<Tb, Ts, 2, -1, -1, -1, kAnyThreads>(p, sms, ctas, stream);
+  bool near = true;                              // row strides below 4 GB
+  for (const RowsOf* r : {&p.y, &p.h, &p.gate, &p.dh, &p.dz, &p.dy, &p.dr, &p.dgate}) near = near && r->ld < (int64_t(1) << 32);
+  if (!near || !p.dz.p != !p.h.p || (!p.dz.p && !p.post_norm))
+    return launch_teams<Tb, Ts, 1, -1, -1, -1, kAnyThreads>(p, sms, ctas, stream);
+  return !p.dz.p       ? launch_gate<Tb, Ts, 0, 1>(p, sms, ctas, stream)
+         : p.post_norm ? launch_gate<Tb, Ts, 1, 1>(p, sms, ctas, stream)
+                       : launch_gate<Tb, Ts, 1, 0>(p, sms, ctas, stream);
 }
 
 }  // namespace
@@ -342,27 +617,19 @@ moe_status moe_norm_residual_backward(const moe_norm_backward_args* a, moe_strea
   for (const void* p : ptrs)
     if (p && !on_device(p, dev.device)) return MOE_ERR_DEVICE;
   NormGradParams p;
-  p.y = a->y;
-  p.h = h;
-  p.gate = gate;
+  p.y = {a->y, a->ldy * eb};
+  p.h = {h, a->ldh * es};
+  p.gate = {gate, full ? a->ldgate * eb : 0};
+  p.dh = {a->dh, a->lddh * es};
+  p.dz = {a->dz, a->lddz * eb};
+  p.dy = {a->dy, a->lddy * eb};
+  p.dr = {a->dr, a->lddr * es};
+  p.dgate = {a->dgate, full ? a->lddgate * eb : 0};
   p.w_post = w_post;
   p.w_pre = w_pre;
-  p.dh = a->dh;
-  p.dz = a->dz;
-  p.dy = a->dy;
-  p.dr = a->dr;
-  p.dgate = a->dgate;
   p.parts = static_cast<float*>(a->workspace);
   p.num_rows = a->num_rows;
   p.M = M;
-  p.ldy = a->ldy;
-  p.ldh = a->ldh;
-  p.ldgate = a->ldgate;
-  p.lddh = a->lddh;
-  p.lddz = a->lddz;
-  p.lddy = a->lddy;
-  p.lddr = a->lddr;
-  p.lddgate = a->lddgate;
   p.H = H;
   p.wide = a->weight_dtype == MOE_TYPE_FP32;
   p.gate_mode = a->gate_mode;
