@@ -3,27 +3,28 @@
 // input in FP8.
 //
 // Each byte is read and written once, a row at a time: its elements stay in
-// registers between the two norms, which need a sum over the row each.  HBM bounds
-// it; what there is to hide is the chain load, sum, sum, store of a row, so
-// several rows are in flight on an SM.
+// registers between the two norms, which need a sum over the row each.  (h's
+// could be formed from sums known before it, but not where r and the branch cancel.)
+// HBM bounds it; what there is to hide is a row's chain of sums.
+#include <atomic>
+#include <type_traits>
+
 #include "norm.cuh"
 
 namespace moe {
 namespace {
 
 struct NormParams {
-  const void* y;
-  const void* r;
-  const void* gate;
+  RowsOf y, r, gate, h, z;
   const void* w_post;
   const void* w_pre;
-  void* h;
-  void* z;
   uint8_t* q;
   float* q_scale;
   const int32_t* num_rows;
-  int64_t M, ldy, ldr, ldh, ldz, ldgate;
+  int64_t M;
   int H, wide, gate_mode, post_norm, pow2;
+  int team;                         // threads of a row
+  int stages;                       // rows of a team in shared memory
   float residual_scale, weight_offset, eps;
 };
 
@@ -37,135 +38,312 @@ __device__ __forceinline__ float scale_to_pow2(float s) {
   return top + 1 >= 23 ? __uint_as_float(1u << 23) : __uint_as_float(1u << (top + 1));
 }
 
-// kVec vectors of eight elements a thread; kWarpRow: a warp per row, else a CTA.
-template <typename Tb, typename Ts, int kVec, bool kWarpRow>
-__global__ void __launch_bounds__(kWarpRow ? 256 : 1024) norm_kernel(const __grid_constant__ NormParams p) {
-  __shared__ float part[2][1][32];
+// Eight values over one scale as E4M3 codes, each from the correctly rounded quotient: the product
+// with the reciprocal, corrected twice by its residual (Markstein), which is exact where no
+// value that rounds to a code is near FP32's smallest; one of them by a divide otherwise.
+__device__ __forceinline__ uint2 codes_of(const float2 (&f)[4], float s) {
+  uint32_t code[2] = {0, 0};
+  if (s >= 0x1p-80f && s <= 0x1p100f) {
+    const float2 inv = both(__frcp_rn(s)), minus = both(-s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float2 q = mul2(f[i], inv);
+      q = fma2(fma2(minus, q, f[i]), inv, q);
+      q = fma2(fma2(minus, q, f[i]), inv, q);
+      code[i / 2] |= static_cast<uint32_t>(cvt_e4m3x2(q.x, q.y)) << (16 * (i % 2));
+    }
+  } else if (s > 0.f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      code[i / 2] |= static_cast<uint32_t>(cvt_e4m3x2(__fdiv_rn(f[i].x, s), __fdiv_rn(f[i].y, s))) << (16 * (i % 2));
+  }
+  return make_uint2(code[0], code[1]);
+}
+
+// What a fixed variant keeps in shared memory, as the gradient does: for each warp of a team the
+// weights (post, or the channel gate, or their product; pre) in FP32, which its teams
+// share, then for each warp p.stages times the pieces of a row's inputs (y, r, gate).
+template <typename Tb, typename Ts, int kVec, int kPost, int kGate>
+struct Layout {
+  static constexpr int kB = kPieces<Tb>, kS = kPieces<Ts>;
+  static constexpr int kAtR = kVec * kB, kAtG = kAtR + kVec * kS, kUnits = kAtG + (kGate == MOE_GATE_FULL ? kVec * kB : 0);
+  static constexpr int kAtPost = 2 * kVec, kWeights = kAtPost + (kPost || kGate == MOE_GATE_CHANNEL ? 2 * kVec : 0);
+  static __host__ __device__ constexpr int bytes(int team, int teams, int stages) {
+    return (kWeights + teams * stages * kUnits) * (kPiece / 32) * team;
+  }
+};
+constexpr int kMostStages = 3;
+
+// The sum over a team of one value: every thread gets the same bits.
+__device__ __forceinline__ float team_sum(float v, float (*part)[32], int& turn, int warps, int index) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (warps == 1) return v;
+  const int lane = threadIdx.x % 32;
+  if (lane == 0) part[turn][threadIdx.x / 32] = v;
+  named_barrier(1 + index, 32 * warps);
+  v = lane < warps ? part[turn][index * warps + lane] : 0.f;
+  turn ^= 1;                                // (the next sum's parts: a thread behind still reads these)
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// A row's team is `team` threads with kVec vectors of eight columns each; a CTA holds several
+// teams, each with its own rows and barrier, and keeps their next rows' inputs on the way into
+// shared memory.  kPost, kGate (a token's as none: it is a number): a variant fixed at compile time;
+// kGate = -1: any variant, from memory itself.
+template <typename Tb, typename Ts, int kVec, int kPost, int kGate>
+__global__ void __launch_bounds__(1024, 1) norm_kernel(const __grid_constant__ NormParams p) {
+  constexpr bool kFixed = kGate >= 0;
+  constexpr bool kShared = kFixed && sizeof(Ts) == 4;
+  using At = Layout<Tb, Ts, kVec, kPost == 1, kGate>;
+  __shared__ float part[2][32];
+  extern __shared__ __align__(16) uint8_t memory[];
   pdl_wait();
   pdl_launch_dependents();
-  int turn = 0;
-  const int team = kWarpRow ? 32 : blockDim.x, tid = kWarpRow ? threadIdx.x % 32 : threadIdx.x;
-  const int64_t live = p.num_rows ? min(static_cast<int64_t>(max(*p.num_rows, 0)), p.M) : p.M;
-  const int64_t row0 = kWarpRow ? static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
-  const int64_t step = kWarpRow ? static_cast<int64_t>(gridDim.x) * (blockDim.x / 32) : gridDim.x;
+  const int team = p.team, mine = threadIdx.x / team, tid = threadIdx.x - mine * team, teams = blockDim.x / team;
+  const int lane = threadIdx.x % 32, warps = team / 32;
+  const int gate = kFixed ? kGate : p.gate_mode == MOE_GATE_TOKEN ? MOE_GATE_NONE : p.gate_mode;
+  const bool post = kFixed ? kPost != 0 : p.post_norm != 0, has_r = p.r.p != nullptr, second = p.z.p || p.q;
+  const bool token_gate = gate == MOE_GATE_NONE && p.gate_mode == MOE_GATE_TOKEN;
+  const uint32_t M = static_cast<uint32_t>(p.M), live = p.num_rows ? min(static_cast<uint32_t>(max(*p.num_rows, 0)), M) : M;
+  const uint32_t step = gridDim.x * teams;
   const float inv_h = 1.f / static_cast<float>(p.H);
-  for (int64_t row = row0; row < live; row += step) {
-    Vec8<Tb> yr[kVec], gr[kVec];
-    Vec8<Ts> rr[kVec];
+  const Places in = places(lane);
+  const uint32_t w_at = smem_u32(memory) + (tid / 32) * (At::kWeights * kPiece) + 16u * lane;
+  auto column = [&](int v) { return 8 * (tid + v * team); };
+  Tb* const of_branch = nullptr;
+  Ts* const of_stream = nullptr;
+
+  auto get = [&](auto* type, const RowsOf& rows, int piece, uint32_t at, uint32_t row, int c, float2 (&f)[4]) {
+    using T = std::remove_pointer_t<decltype(type)>;
+    if constexpr (kFixed)
+      widen2<T>(from_pieces<T>(in, at, piece), f);
+    else
+      widen2<T>(load_vec<T>(reinterpret_cast<const T*>(rows.at<false>(row, c * sizeof(T)))), f);
+  };
+  auto put = [&](auto* type, const RowsOf& rows, int piece, uint32_t at, uint32_t row, int c, const float2 (&f)[4]) {
+    using T = std::remove_pointer_t<decltype(type)>;
+    if constexpr (kFixed && sizeof(T) == 4)
+      put_pieces(in, at, piece, f);
+    else
+      store2<T>(reinterpret_cast<T*>(rows.at<kFixed>(row, c * sizeof(T))), f);
+  };
+  auto weights = [&](int piece, float2 (&f)[4]) {
+    widen2<float>(Vec8<float>{shared16(w_at + piece * kPiece), shared16(w_at + (piece + 1) * kPiece)}, f);
+  };
+  // the columns' factor of the branch: its norm's weights, a channel gate, or their product
+  auto factor = [&](int c, float2 (&f)[4]) {
+    if (post) weights2<Tb>(p.w_post, p.wide, c, p.weight_offset, f);
+    if (gate == MOE_GATE_CHANNEL) {
+      float2 g[4];
+      weights2<Tb>(p.gate.p, p.wide, c, 0.f, g);
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) {
-      const int c = 8 * (tid + v * team);
-      if (c < p.H) {
-        yr[v] = load_vec<Tb>(static_cast<const Tb*>(p.y) + row * p.ldy + c);
-        if (p.r) rr[v] = load_vec<Ts>(static_cast<const Ts*>(p.r) + row * p.ldr + c);
-        if (p.gate_mode == MOE_GATE_FULL) gr[v] = load_vec<Tb>(static_cast<const Tb*>(p.gate) + row * p.ldgate + c);
+      for (int i = 0; i < 4; ++i) f[i] = post ? mul2(f[i], g[i]) : g[i];
+    }
+  };
+  auto fetch_row = [&](uint32_t at, uint32_t row) {
+    if constexpr (kFixed) {
+      if (row < live) {
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) {
+          const int c = column(v);
+          to_pieces(in, at, v * At::kB, At::kB, p.y, row, c, p.H);
+          if (has_r) to_pieces(in, at, At::kAtR + v * At::kS, At::kS, p.r, row, c, p.H);
+          if (gate == MOE_GATE_FULL) to_pieces(in, at, At::kAtG + v * At::kB, At::kB, p.gate, row, c, p.H);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  };
+
+  uint32_t row = blockIdx.x * teams + mine;
+  const uint32_t first = smem_u32(memory) + (team / 32) * (At::kWeights * kPiece) +
+                         (threadIdx.x / 32) * (p.stages * (At::kUnits * kPiece));
+  const uint32_t end = first + p.stages * (At::kUnits * kPiece);
+  uint32_t at = first, free = first;
+  int turn = 0;
+  if constexpr (kFixed) {
+    for (int i = 0; i < p.stages - 1; ++i, free += At::kUnits * kPiece) fetch_row(free, row + i * step);
+    if (mine == 0) {
+#pragma unroll
+      for (int v = 0; v < kVec; ++v) {
+        const int c = column(v);
+        if (c < p.H) {
+          float2 f[4];
+          weights2<Tb>(p.w_pre, p.wide, c, p.weight_offset, f);
+          put16(w_at + 2 * v * kPiece, f[0], f[1]);
+          put16(w_at + (2 * v + 1) * kPiece, f[2], f[3]);
+          if (post || gate == MOE_GATE_CHANNEL) {
+            factor(c, f);
+            put16(w_at + (At::kAtPost + 2 * v) * kPiece, f[0], f[1]);
+            put16(w_at + (At::kAtPost + 2 * v + 1) * kPiece, f[2], f[3]);
+          }
+        }
       }
     }
-    float h[kVec][8];
+    if (teams > 1) __syncthreads();
+  }
+
+  for (; row < live; row += step) {
+    if constexpr (kShared) __syncwarp();    // (every lane is done with the row that was there)
+    fetch_row(free, row + (p.stages - 1) * step);
+    if constexpr (kFixed) {
+      if (p.stages == 3)
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+      else
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      if constexpr (kShared) __syncwarp();  // (the other lanes' copies)
+    }
+    float2 h[kVec][4];
     float root = 1.f;
-    if (p.post_norm) {
-      float sum[1] = {0.f};
+#pragma unroll
+    for (int v = 0; v < kVec; ++v)
+      if (column(v) < p.H) get(of_branch, p.y, v * At::kB, at, row, column(v), h[v]);
+    if (post) {
+      float2 sum = {};
 #pragma unroll
       for (int v = 0; v < kVec; ++v)
-        if (8 * (tid + v * team) < p.H) {
-          widen<Tb>(yr[v], h[v]);
+        if (column(v) < p.H) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum[0] = fmaf(h[v][i], h[v][i], sum[0]);
+          for (int i = 0; i < 4; ++i) sum = fma2(h[v][i], h[v][i], sum);
         }
-      row_sums<1, kWarpRow>(sum, part, turn);
-      root = rsqrtf(fmaf(sum[0], inv_h, p.eps));
+      root = rsqrtf(fmaf(team_sum(sum.x + sum.y, part, turn, warps, mine), inv_h, p.eps));
     }
-    const float token = p.gate_mode == MOE_GATE_TOKEN ? __ldg(static_cast<const float*>(p.gate) + row) : 1.f;
-    float sum[1] = {0.f};
+    if (token_gate) root *= __ldg(static_cast<const float*>(p.gate.p) + row);
+    float2 sum = {};
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
-      const int c = 8 * (tid + v * team);
+      const int c = column(v);
       if (c < p.H) {
-        widen<Tb>(yr[v], h[v]);
-        if (p.post_norm) {
-          float w[8];
-          load_weights<Tb>(p.w_post, p.wide, c, p.weight_offset, w);
+        if (post || token_gate) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) h[v][i] = h[v][i] * root * w[i];
+          for (int i = 0; i < 4; ++i) h[v][i] = mul2(h[v][i], both(root));
         }
-        if (p.gate_mode == MOE_GATE_TOKEN) {
+        if (post || gate == MOE_GATE_CHANNEL) {
+          float2 w[4];
+          if constexpr (kFixed) weights(At::kAtPost + 2 * v, w); else factor(c, w);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) h[v][i] *= token;
-        } else if (p.gate_mode != MOE_GATE_NONE) {
-          float g[8];
-          if (p.gate_mode == MOE_GATE_FULL)
-            widen<Tb>(gr[v], g);
-          else
-            load_weights<Tb>(p.gate, p.wide, c, 0.f, g);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) h[v][i] *= g[i];
+          for (int i = 0; i < 4; ++i) h[v][i] = mul2(h[v][i], w[i]);
         }
-        if (p.r) {
-          float r[8];
-          widen<Ts>(rr[v], r);
+        if (gate == MOE_GATE_FULL) {
+          float2 g[4];
+          get(of_branch, p.gate, At::kAtG + v * At::kB, at, row, c, g);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) h[v][i] = fmaf(p.residual_scale, r[i], h[v][i]);
+          for (int i = 0; i < 4; ++i) h[v][i] = mul2(h[v][i], g[i]);
         }
-        if (p.h) store_vec<Ts>(static_cast<Ts*>(p.h) + row * p.ldh + c, h[v]);
+        if (has_r) {
+          float2 r[4];
+          get(of_stream, p.r, At::kAtR + v * At::kS, at, row, c, r);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[0] = fmaf(h[v][i], h[v][i], sum[0]);
+          for (int i = 0; i < 4; ++i) h[v][i] = fma2(both(p.residual_scale), r[i], h[v][i]);
+        }
+        if (p.h.p) put(of_stream, p.h, At::kAtR + v * At::kS, at, row, c, h[v]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum = fma2(h[v][i], h[v][i], sum);
       }
     }
-    if (!p.z && !p.q) continue;
-    row_sums<1, kWarpRow>(sum, part, turn);
-    root = rsqrtf(fmaf(sum[0], inv_h, p.eps));
+    if constexpr (kShared) {
+      __syncwarp();
+      if (p.h.p) {
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) {
-      const int c = 8 * (tid + v * team);
-      // (a group of 128 columns is 16 neighbouring lanes of one warp: all of them or none have columns)
-      if (c < p.H) {
-        float w[8];
-        load_weights<Tb>(p.w_pre, p.wide, c, p.weight_offset, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[v][i] = h[v][i] * root * w[i];
-        if (p.z) store_vec<Tb>(static_cast<Tb*>(p.z) + row * p.ldz + c, h[v]);
+        for (int v = 0; v < kVec; ++v) flush_pieces(in, at, At::kAtR + v * At::kS, p.h, row, column(v), p.H);
       }
-      if (p.q) {
-        float amax = 0.f;
-        if (c < p.H) {
+    }
+    if (second) {
+      root = rsqrtf(fmaf(team_sum(sum.x + sum.y, part, turn, warps, mine), inv_h, p.eps));
 #pragma unroll
-          for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(h[v][i]));
+      for (int v = 0; v < kVec; ++v) {
+        const int c = column(v);
+        const bool live_column = c < p.H;
+        if (live_column) {
+          float2 w[4];
+          if constexpr (kFixed) weights(2 * v, w); else weights2<Tb>(p.w_pre, p.wide, c, p.weight_offset, w);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[v][i] = mul2(mul2(h[v][i], both(root)), w[i]);
+          if (p.z.p) put(of_branch, p.z, v * At::kB, at, row, c, h[v]);
         }
+        if (p.q) {
+          // (a group of 128 columns is 16 neighbouring lanes: all of them or none have columns)
+          float amax = 0.f;
+          if (live_column) {
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        float s = __fdiv_rn(amax, 448.f);
-        if (p.pow2 && s > 0.f) s = scale_to_pow2(s);
-        if (c < p.H) {
-          uint32_t code[2] = {0, 0};
-          if (s > 0.f) {
-#pragma unroll
-            for (int i = 0; i < 8; i += 2)
-              code[i / 4] |= static_cast<uint32_t>(cvt_e4m3x2(__fdiv_rn(h[v][i], s), __fdiv_rn(h[v][i + 1], s))) << (8 * (i % 4));
+            for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fmaxf(fabsf(h[v][i].x), fabsf(h[v][i].y)));
           }
-          if (MOE_IN_BOUNDS(row >= 0 && row < p.M)) {
-            *reinterpret_cast<uint2*>(p.q + row * p.H + c) = make_uint2(code[0], code[1]);
-            if (tid % 16 == 0) p.q_scale[row * (p.H / 128) + c / 128] = s;
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          float s = __fdiv_rn(amax, 448.f);
+          if (p.pow2 && s > 0.f) s = scale_to_pow2(s);
+          if (live_column && MOE_IN_BOUNDS(row < M)) {
+            *reinterpret_cast<uint2*>(p.q + static_cast<int64_t>(row) * p.H + c) = codes_of(h[v], s);
+            if (lane % 16 == 0) p.q_scale[static_cast<int64_t>(row) * (p.H / 128) + c / 128] = s;
           }
         }
       }
+      if constexpr (kFixed && sizeof(Tb) == 4) {
+        __syncwarp();
+        if (p.z.p) {
+#pragma unroll
+          for (int v = 0; v < kVec; ++v) flush_pieces(in, at, v * At::kB, p.z, row, column(v), p.H);
+        }
+      }
     }
+    free = at;
+    at = at + At::kUnits * kPiece == end ? first : at + At::kUnits * kPiece;
   }
 }
 
-template <typename Tb, typename Ts>
-cudaError_t launch_norm(const NormParams& p, int sms, cudaStream_t stream) {
-  const int vecs = p.H / 8;
-  if (vecs <= 64) {
-    const int64_t ctas = ceil_div(p.M, 8), most = static_cast<int64_t>(sms) * 64;
-    const dim3 grid(static_cast<unsigned>(ctas < most ? ctas : most));
-    return vecs <= 32 ? launch_pdl(norm_kernel<Tb, Ts, 1, true>, grid, dim3(256), 0, stream, 1, p)
-                      : launch_pdl(norm_kernel<Tb, Ts, 2, true>, grid, dim3(256), 0, stream, 1, p);
+constexpr int kMostShared = 224 * 1024;
+
+template <typename Tb, typename Ts, int kVec, int kPost, int kGate>
+cudaError_t launch_teams(NormParams& p, int sms, cudaStream_t stream) {
+  constexpr bool kFixed = kGate >= 0;
+  using At = Layout<Tb, Ts, kVec, kPost == 1, kGate>;
+  p.team = team_threads(p.H / 8, kVec);
+  int teams = 1024 / p.team;
+  if (p.team > 32 && teams > 15) teams = 15;     // (a named barrier each)
+  while (kFixed && teams > 1 && At::bytes(p.team, teams, 2) > kMostShared) --teams;
+  if (ceil_div(p.M, sms) < teams) teams = static_cast<int>(ceil_div(p.M, sms));
+  p.stages = 2;
+  while (kFixed && p.stages < kMostStages && At::bytes(p.team, teams, p.stages + 1) <= kMostShared) ++p.stages;
+  const int64_t want = ceil_div(p.M, teams), most = kFixed ? sms : 8 * sms;
+  auto kernel = norm_kernel<Tb, Ts, kVec, kPost, kGate>;
+  static std::atomic<bool> sized[64];            // per device: the attribute outlasts the call
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (kFixed && err == cudaSuccess && (dev >= 64 || !sized[dev].load())) {
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
+    if (err == cudaSuccess && dev < 64) sized[dev].store(true);
   }
-  const int64_t most = static_cast<int64_t>(sms) * 64;
-  const dim3 grid(static_cast<unsigned>(p.M < most ? p.M : most));
-  if (vecs <= 1024 && p.M <= sms)
-    return launch_pdl(norm_kernel<Tb, Ts, 1, false>, grid, dim3(team_threads(vecs, 1)), 0, stream, 1, p);
-  return launch_pdl(norm_kernel<Tb, Ts, 2, false>, grid, dim3(team_threads(vecs, 2)), 0, stream, 1, p);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(want < most ? want : most)), dim3(p.team * teams),
+                    kFixed ? static_cast<size_t>(At::bytes(p.team, teams, p.stages)) : 0, stream, 1, p);
+}
+
+// The fixed variant where a row of it fits, else the one for any.
+template <typename Tb, typename Ts, int kPost, int kGate>
+cudaError_t launch_fixed(NormParams& p, int sms, cudaStream_t stream) {
+  const int vecs = p.H / 8, one = team_threads(vecs, 1), two = team_threads(vecs, 2);
+  if (vecs <= 512 || (p.M <= sms && vecs <= 1024)) {
+    if (Layout<Tb, Ts, 1, kPost, kGate>::bytes(one, 1, 2) <= kMostShared) return launch_teams<Tb, Ts, 1, kPost, kGate>(p, sms, stream);
+  } else if (Layout<Tb, Ts, 2, kPost, kGate>::bytes(two, 1, 2) <= kMostShared) {
+    return launch_teams<Tb, Ts, 2, kPost, kGate>(p, sms, stream);
+  }
+  return vecs <= 1024 ? launch_teams<Tb, Ts, 1, -1, -1>(p, sms, stream) : launch_teams<Tb, Ts, 2, -1, -1>(p, sms, stream);
+}
+template <typename Tb, typename Ts, int kPost>
+cudaError_t launch_gate(NormParams& p, int sms, cudaStream_t stream) {
+  return p.gate_mode == MOE_GATE_FULL      ? launch_fixed<Tb, Ts, kPost, MOE_GATE_FULL>(p, sms, stream)
+         : p.gate_mode == MOE_GATE_CHANNEL ? launch_fixed<Tb, Ts, kPost, MOE_GATE_CHANNEL>(p, sms, stream)
+                                           : launch_fixed<Tb, Ts, kPost, MOE_GATE_NONE>(p, sms, stream);
+}
+template <typename Tb, typename Ts>
+cudaError_t launch_norm(NormParams& p, int sms, cudaStream_t stream) {
+  bool near = true;                              // row strides below 4 GB
+  for (const RowsOf* r : {&p.y, &p.r, &p.gate, &p.h, &p.z}) near = near && r->ld < (int64_t(1) << 32);
+  if (!near) return launch_teams<Tb, Ts, 2, -1, -1>(p, sms, stream);
+  return p.post_norm ? launch_gate<Tb, Ts, 1>(p, sms, stream) : launch_gate<Tb, Ts, 0>(p, sms, stream);
 }
 
 }  // namespace
@@ -213,22 +391,17 @@ moe_status moe_norm_residual(const moe_norm_args* a, moe_stream_t stream) {
                         static_cast<const void*>(a->q), static_cast<const void*>(a->q_scale), static_cast<const void*>(a->num_rows)})
     if (p && !on_device(p, dev.device)) return MOE_ERR_DEVICE;
   NormParams p;
-  p.y = a->y;
-  p.r = a->r;
-  p.gate = gate;
+  p.y = {a->y, a->ldy * eb};
+  p.r = {a->r, a->ldr * es};
+  p.gate = {gate, a->gate_mode == MOE_GATE_FULL ? a->ldgate * eb : 0};
+  p.h = {a->h, a->ldh * es};
+  p.z = {a->z, a->ldz * eb};
   p.w_post = w_post;
   p.w_pre = w_pre;
-  p.h = a->h;
-  p.z = a->z;
   p.q = a->q;
   p.q_scale = a->q_scale;
   p.num_rows = a->num_rows;
   p.M = M;
-  p.ldy = a->ldy;
-  p.ldr = a->ldr;
-  p.ldh = a->ldh;
-  p.ldz = a->ldz;
-  p.ldgate = a->ldgate;
   p.H = H;
   p.wide = a->weight_dtype == MOE_TYPE_FP32;
   p.gate_mode = a->gate_mode;

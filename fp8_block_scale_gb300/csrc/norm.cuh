@@ -22,68 +22,6 @@ __device__ __forceinline__ Vec8<T> load_vec(const T* p) {
     return {*reinterpret_cast<const uint4*>(p)};
   }
 }
-template <typename T>
-__device__ __forceinline__ void widen(const Vec8<T>& r, float (&f)[8]) {
-  if constexpr (sizeof(T) == 4) {
-    const uint32_t w[8] = {r.v.x, r.v.y, r.v.z, r.v.w, r.w.x, r.w.y, r.w.z, r.w.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
-  } else {
-    unpack8<T>(r.v, f);
-  }
-}
-// One rounding to the type.
-template <typename T>
-__device__ __forceinline__ void store_vec(T* p, const float (&f)[8]) {
-  uint4* q = reinterpret_cast<uint4*>(p);
-  if constexpr (sizeof(T) == 4) {
-    q[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-    q[1] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
-  } else {
-    q[0] = pack8<T>(f);
-  }
-}
-
-// Eight weights from column c on: FP32 or the branch's type, plus the offset; 1 without weights.
-template <typename T>
-__device__ __forceinline__ void load_weights(const void* w, int wide, int c, float offset, float (&f)[8]) {
-  if (!w) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = 1.f;
-    return;
-  }
-  if (wide)
-    widen<float>(load_vec<float>(static_cast<const float*>(w) + c), f);
-  else
-    widen<T>(load_vec<T>(static_cast<const T*>(w) + c), f);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] += offset;
-}
-
-// Sums over a row by its team: a warp, or the whole CTA through shared memory, one
-// barrier a call (two buffers in turn: the next call writes the other one).  Every
-// thread gets the same bits.
-template <int kN, bool kWarpRow>
-__device__ __forceinline__ void row_sums(float (&v)[kN], float (*part)[kN][32], int& turn) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int n = 0; n < kN; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
-  if (kWarpRow) return;
-  const int lane = threadIdx.x % 32, warps = blockDim.x / 32;
-  if (lane == 0)
-#pragma unroll
-    for (int n = 0; n < kN; ++n) part[turn][n][threadIdx.x / 32] = v[n];
-  __syncthreads();
-#pragma unroll
-  for (int n = 0; n < kN; ++n) v[n] = lane < warps ? part[turn][n][lane] : 0.f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int n = 0; n < kN; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
-  turn ^= 1;
-}
-
 // ---- pairs of FP32 values: one instruction each for two (packed arithmetic of sm_100)
 
 __device__ __forceinline__ uint64_t bits2(float2 a) {
@@ -155,28 +93,85 @@ __device__ __forceinline__ void weights2(const void* w, int wide, int c, float o
   for (int i = 0; i < 4; ++i) f[i] = add2(f[i], both(offset));
 }
 
-// Sums over a row by its team, one of several in a CTA: whole warps, by shuffles and, for more
-// than one, through shared memory with a barrier of its own (two buffers in turn: the
-// next call writes the other one).  Every thread gets the same bits.
-template <int kN>
-__device__ __forceinline__ void team_sums(float (&v)[kN], float (*part)[3][32], int& turn, int team, int index) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int n = 0; n < kN; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
-  if (team == 32) return;
-  const int lane = threadIdx.x % 32, warps = team / 32, first = index * warps;
-  if (lane == 0)
-#pragma unroll
-    for (int n = 0; n < kN; ++n) part[turn][n][threadIdx.x / 32] = v[n];
-  named_barrier(1 + index, team);
-#pragma unroll
-  for (int n = 0; n < kN; ++n) v[n] = lane < warps ? part[turn][n][first + lane] : 0.f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int n = 0; n < kN; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
-  turn ^= 1;
+// Rows of an input or output: the next one `ld` bytes further on.
+struct RowsOf {
+  const void* p;
+  int64_t ld;
+  // This thread's part of row `row`, `offset` bytes into it; kNear: ld has 32 bits.
+  template <bool kNear>
+  __device__ __forceinline__ uint8_t* at(int64_t row, uint32_t offset) const {
+    uint8_t* base = static_cast<uint8_t*>(const_cast<void*>(p)) + offset;
+    if constexpr (kNear)
+      return base + static_cast<uint64_t>(static_cast<uint32_t>(row)) * static_cast<uint32_t>(ld);
+    else
+      return base + row * ld;
+  }
+};
+
+
+// ---- rows through shared memory
+//
+// Rows arrive by asynchronous 16-byte copies in pieces of 512 bytes, 16 for each lane of a warp.  A
+// piece of 16-bit elements is each lane's own eight columns.  A warp's FP32 columns are two
+// neighbouring pieces that its lanes fill (and empty) together in two runs of 512
+// bytes: a lane's own 32 bytes in two 16-byte accesses would ask L2 for every sector twice (8192
+// x 4096 with an FP32 stream, gradient: 136 us against 96).  The 16-byte units are placed so that a
+// lane reads its two without bank conflicts.
+constexpr int kPiece = 512;
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void put16(uint32_t at, float2 a, float2 b) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y) : "memory");
+}
+__device__ __forceinline__ uint4 shared16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+template <typename T> constexpr int kPieces = static_cast<int>(sizeof(T)) / 2;
+
+
+// Where a lane finds its parts of a piece: its own, its place in a run, its two units of FP32.
+struct Places {
+  uint32_t mine16, run16, low16, high16;
+};
+__device__ __forceinline__ Places places(int lane) {
+  const uint32_t low = 32u * lane + 16u * ((lane >> 2) & 1);
+  return {16u * lane, 16u * (lane ^ ((lane >> 3) & 1)), low, low ^ 16u};
+}
+// Asks for this warp's columns of a row (c: the lane's first of eight), `pieces` of them.
+__device__ __forceinline__ void to_pieces(const Places& in, uint32_t at, int piece, int pieces, const RowsOf& rows, uint32_t row,
+                                          int c, int H) {
+  if (pieces == 1) {
+    if (c < H) copy16((at + in.mine16) + piece * kPiece, rows.at<true>(row, 2 * c));
+  } else {
+    const int c4 = c - 4 * static_cast<int>(threadIdx.x % 32);
+    if (c4 < H) copy16((at + in.run16) + piece * kPiece, rows.at<true>(row, 4 * c4));
+    if (c4 + 128 < H) copy16((at + in.run16) + (piece + 1) * kPiece, rows.at<true>(row, 4 * c4 + 512));
+  }
+}
+template <typename T>
+__device__ __forceinline__ Vec8<T> from_pieces(const Places& in, uint32_t at, int piece) {
+  Vec8<T> r;
+  if constexpr (sizeof(T) == 4) {
+    r.v = shared16((at + in.low16) + piece * kPiece);
+    r.w = shared16((at + in.high16) + piece * kPiece);
+  } else {
+    r.v = shared16((at + in.mine16) + piece * kPiece);
+  }
+  return r;
+}
+// FP32 outputs go the other way, through the place of an input that has been used: put by every
+// lane, then (after a warp barrier) written to memory by runs.
+__device__ __forceinline__ void put_pieces(const Places& in, uint32_t at, int piece, const float2 (&f)[4]) {
+  put16((at + in.low16) + piece * kPiece, f[0], f[1]);
+  put16((at + in.high16) + piece * kPiece, f[2], f[3]);
+}
+__device__ __forceinline__ void flush_pieces(const Places& in, uint32_t at, int piece, const RowsOf& rows, uint32_t row, int c, int H) {
+  const int c4 = c - 4 * static_cast<int>(threadIdx.x % 32);
+  if (c4 < H) *reinterpret_cast<uint4*>(rows.at<true>(row, 4 * c4)) = shared16((at + in.run16) + piece * kPiece);
+  if (c4 + 128 < H) *reinterpret_cast<uint4*>(rows.at<true>(row, 4 * c4 + 512)) = shared16((at + in.run16) + (piece + 1) * kPiece);
 }
 
 // ---------------------------------------------------------------- host side

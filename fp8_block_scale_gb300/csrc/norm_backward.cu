@@ -17,21 +17,6 @@ constexpr int kMaxParts = 320;      // CTAs whose sums over rows the workspace h
 constexpr int kSums = 3;            // dw_pre, dw_post, a channel gate's
 constexpr int kHeld = 2;            // ... of which the last two are one sum times the other's factor
 
-// Rows of an input or output: the next one `ld` bytes further on.
-struct RowsOf {
-  const void* p;
-  int64_t ld;
-  // This thread's part of row `row`, `offset` bytes into it; kNear: ld has 32 bits.
-  template <bool kNear>
-  __device__ __forceinline__ uint8_t* at(int64_t row, uint32_t offset) const {
-    uint8_t* base = static_cast<uint8_t*>(const_cast<void*>(p)) + offset;
-    if constexpr (kNear)
-      return base + static_cast<uint64_t>(static_cast<uint32_t>(row)) * static_cast<uint32_t>(ld);
-    else
-      return base + row * ld;
-  }
-};
-
 struct NormGradParams {
   RowsOf y, h, gate, dh, dz, dy, dr, dgate;
   const void* w_post;
@@ -79,20 +64,6 @@ __device__ __forceinline__ void join_sums8(const float* parts, int warps, int la
 #pragma unroll
   for (int i = 0; i <= kKH; ++i) v[i] = __shfl_sync(0xffffffffu, sum, i);
 }
-
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void put16(uint32_t at, float2 a, float2 b) {
-  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y) : "memory");
-}
-__device__ __forceinline__ uint4 shared16(uint32_t at) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
-  return v;
-}
-template <typename T> constexpr int kPieces = static_cast<int>(sizeof(T)) / 2;
-constexpr int kPiece = 512;         // bytes of 16 for each lane of a warp
 
 // What a fixed variant keeps in shared memory: for each warp of a team the weights (pre; post, or
 // the channel gate, or their product) in FP32, which its teams share, then for each warp
@@ -148,10 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_kernel(const __grid
   const uint32_t M = static_cast<uint32_t>(p.M), live = p.num_rows ? min(static_cast<uint32_t>(max(*p.num_rows, 0)), M) : M;
   const uint32_t step = gridDim.x * teams;
   const float inv_h = 1.f / static_cast<float>(p.H);
-  // a piece of 16-bit elements is the lane's own; of FP32 the warp's 1024 bytes come (and go) in two
-  // runs of 512, so that whole sectors move, at places that a lane reads its 32 bytes from without conflicts
-  const uint32_t mine16 = 16u * lane, run16 = 16u * (lane ^ ((lane >> 3) & 1)), low16 = 32u * lane + 16u * ((lane >> 2) & 1),
-                 high16 = low16 ^ 16u;
+  const Places in = places(lane);
   const uint32_t of_weights = (tid / 32) * (At::kWeights * kPiece) + 16u * lane, w_at = smem_u32(memory) + of_weights;
   auto column = [&](int v) { return 8 * (tid + v * team); };
 
@@ -160,12 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_kernel(const __grid
     using T = std::remove_pointer_t<decltype(type)>;
     Vec8<T> r;
     if constexpr (kFixed) {
-      if constexpr (sizeof(T) == 4) {
-        r.v = shared16((at + low16) + piece * kPiece);
-        r.w = shared16((at + high16) + piece * kPiece);
-      } else {
-        r.v = shared16((at + mine16) + piece * kPiece);
-      }
+      r = from_pieces<T>(in, at, piece);
     } else {
       r = load_vec<T>(reinterpret_cast<const T*>(rows.at<false>(row, c * sizeof(T))));
     }
@@ -191,15 +154,8 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_kernel(const __grid
   auto fetch_row = [&](uint32_t at, uint32_t row) {
     if constexpr (kFixed) {
       if (row < live) {
-        const int c = column(0), c4 = c - 4 * lane;        // (FP32: four columns a lane, 128 further on the others)
-        auto bring = [&](int piece, int pieces, const RowsOf& rows) {
-          if (pieces == 1) {
-            if (c < p.H) copy16((at + mine16) + piece * kPiece, rows.at<true>(row, 2 * c));
-          } else {
-            if (c4 < p.H) copy16((at + run16) + piece * kPiece, rows.at<true>(row, 4 * c4));
-            if (c4 + 128 < p.H) copy16((at + run16) + (piece + 1) * kPiece, rows.at<true>(row, 4 * c4 + 512));
-          }
-        };
+        const int c = column(0);
+        auto bring = [&](int piece, int pieces, const RowsOf& rows) { to_pieces(in, at, piece, pieces, rows, row, c, p.H); };
         bring(0, At::kB, p.y);
         if (pre) bring(At::kAtZ, At::kB, p.dz), bring(At::kAtH, At::kS, p.h);
         if (has_dh) bring(At::kAtD, At::kS, p.dh);
@@ -213,25 +169,19 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_kernel(const __grid
   auto put = [&](auto* type, const RowsOf& rows, int piece, uint32_t at, uint32_t row, int c, const float2 (&f)[4]) {
     using T = std::remove_pointer_t<decltype(type)>;
     if constexpr (kFixed && sizeof(T) == 4) {
-      put16((at + low16) + piece * kPiece, f[0], f[1]);
-      put16((at + high16) + piece * kPiece, f[2], f[3]);
+      put_pieces(in, at, piece, f);
     } else {
       store2<T>(reinterpret_cast<T*>(rows.at<kFixed>(row, c * sizeof(T))), f);
     }
   };
-  auto flush = [&](const RowsOf& rows, int piece, uint32_t at, uint32_t row) {
-    const int c4 = column(0) - 4 * lane;
-    if (c4 < p.H) *reinterpret_cast<uint4*>(rows.at<kFixed>(row, 4 * c4)) = shared16((at + run16) + piece * kPiece);
-    if (c4 + 128 < p.H) *reinterpret_cast<uint4*>(rows.at<kFixed>(row, 4 * c4 + 512)) = shared16((at + run16) + (piece + 1) * kPiece);
-  };
+  auto flush = [&](const RowsOf& rows, int piece, uint32_t at, uint32_t row) { flush_pieces(in, at, piece, rows, row, column(0), p.H); };
 
   if constexpr (kFixed) {
     const int c = column(0);
     if (mine == 0 && c < p.H) {
       auto keep = [&](const float2 (&f)[4], int piece) {
-        float4* to = reinterpret_cast<float4*>(memory + of_weights + piece * kPiece);
-        to[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
-        to[kPiece / 16] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+        put16(w_at + piece * kPiece, f[0], f[1]);
+        put16(w_at + (piece + 1) * kPiece, f[2], f[3]);
       };
       float2 f[4];
       if (pre) {
