@@ -72,7 +72,6 @@ struct Layout {
     return (kWeights + teams * stages * kUnits) * (kPiece / 32) * team;
   }
 };
-constexpr int kMostStages = 3;
 
 // The sum over a team of one value: every thread gets the same bits.
 __device__ __forceinline__ float team_sum(float v, float (*part)[32], int& turn, int warps, int index) {
@@ -294,7 +293,8 @@ __global__ void __launch_bounds__(1024, 1) norm_kernel(const __grid_constant__ N
   }
 }
 
-constexpr int kMostShared = 224 * 1024;
+// (FP32 streams: beyond, one team and three stages are faster than two of two)
+constexpr int kMostShared = 224 * 1024, kMostWideRing = 112 * 1024;
 
 template <typename Tb, typename Ts, int kVec, int kPost, int kGate>
 cudaError_t launch_teams(NormParams& p, int sms, cudaStream_t stream) {
@@ -303,10 +303,16 @@ cudaError_t launch_teams(NormParams& p, int sms, cudaStream_t stream) {
   p.team = team_threads(p.H / 8, kVec);
   int teams = 1024 / p.team;
   if (p.team > 32 && teams > 15) teams = 15;     // (a named barrier each)
-  while (kFixed && teams > 1 && At::bytes(p.team, teams, 2) > kMostShared) --teams;
+  auto fits = [&](int n) {
+    const int all = At::bytes(p.team, n, 2);
+    return all <= kMostShared && (sizeof(Ts) == 2 || all - At::bytes(p.team, 0, 2) <= kMostWideRing);
+  };
+  while (kFixed && teams > 1 && !fits(teams)) --teams;
   if (ceil_div(p.M, sms) < teams) teams = static_cast<int>(ceil_div(p.M, sms));
-  p.stages = 2;
-  while (kFixed && p.stages < kMostStages && At::bytes(p.team, teams, p.stages + 1) <= kMostShared) ++p.stages;
+  // Several teams hide one another's sums, and two stages each are enough (8192 x 4096 with one norm:
+  // 43 us, 47 with three); one team needs a row more on the way (FP32 rows of 4096 columns, which
+  // fill the ring alone: 84 us, 90 with two; 87 as two teams of three stages).
+  p.stages = teams == 1 && At::bytes(p.team, 1, 3) <= kMostShared ? 3 : 2;
   const int64_t want = ceil_div(p.M, teams), most = kFixed ? sms : 8 * sms;
   auto kernel = norm_kernel<Tb, Ts, kVec, kPost, kGate>;
   static std::atomic<bool> sized[64];            // per device: the attribute outlasts the call
@@ -324,8 +330,12 @@ cudaError_t launch_teams(NormParams& p, int sms, cudaStream_t stream) {
 // The fixed variant where a row of it fits, else the one for any.
 template <typename Tb, typename Ts, int kPost, int kGate>
 cudaError_t launch_fixed(NormParams& p, int sms, cudaStream_t stream) {
+  // One vector a thread while two teams fit a CTA, for a few rows (latency), and up to 896 where
+  // a row has enough to move for the time of its sums: one norm (16384 x 7168 with FP8 output: 160
+  // us, 178 as two teams with two vectors a thread) or an FP32 stream (8192 x 7168: 105, 124);
+  // not for two norms in 16 bits (8192 x 7168: 107, 91).
   const int vecs = p.H / 8, one = team_threads(vecs, 1), two = team_threads(vecs, 2);
-  if (vecs <= 512 || (p.M <= sms && vecs <= 1024)) {
+  if (vecs <= 512 || (vecs <= 896 && (!kPost || sizeof(Ts) == 4)) || (p.M <= sms && vecs <= 1024)) {
     if (Layout<Tb, Ts, 1, kPost, kGate>::bytes(one, 1, 2) <= kMostShared) return launch_teams<Tb, Ts, 1, kPost, kGate>(p, sms, stream);
   } else if (Layout<Tb, Ts, 2, kPost, kGate>::bytes(two, 1, 2) <= kMostShared) {
     return launch_teams<Tb, Ts, 2, kPost, kGate>(p, sms, stream);

@@ -15,6 +15,8 @@
 // hundred times as long as reading them.
 #include <math_constants.h>
 
+#include <type_traits>
+
 #include "../../include/moe_block.h"
 #include "router.cuh"
 #include "train.cuh"
@@ -34,7 +36,8 @@ struct RouteParams {
   int64_t M, ld;
   int E, top_k, groups, topk_groups, group_size;
   int lanes;        // lanes per group, a power of two: lane = group * lanes + part
-  int per;          // experts per lane
+  int per;          // experts per lane, in runs of 1 << run
+  int run;
   int pair, score, renormalize, dtype, id_bits;
   float scale;
 };
@@ -82,9 +85,9 @@ __device__ __forceinline__ double sigmoid64(float l) {
   return (l >= 0.f ? 1.0 : e) / (1.0 + e);
 }
 
-// The expert of this lane's i-th place, or -1.
+// The expert of this lane's i-th place, or -1: a group's lanes take runs of 1 << run experts in turn.
 __device__ __forceinline__ int expert_at(const RouteParams& p, int i, int lane) {
-  const int off = lane % p.lanes + p.lanes * i, g = lane / p.lanes;
+  const int off = ((((i >> p.run) * p.lanes + lane % p.lanes) << p.run) | (i & ((1 << p.run) - 1))), g = lane / p.lanes;
   return g < p.groups && off < p.group_size ? g * p.group_size + off : -1;
 }
 
@@ -176,7 +179,7 @@ __device__ __noinline__ bool groups_exactly(const RouteParams& p, int64_t t, uin
   return group_stays(p, top);
 }
 
-// Lane r gets the lane whose rank is r (ranks are distinct).
+// The lane whose rank is this lane's number (ranks are distinct).
 __device__ __forceinline__ int place(int16_t* at, int rank, int lane) {
   __syncwarp();
   at[rank & 31] = static_cast<int16_t>(lane);
@@ -198,17 +201,16 @@ __device__ __noinline__ Chosen choose_exactly(const RouteParams& p, int64_t t, i
   }
   uint64_t keys[64];                            // 0: left out (p.per <= 64)
   TopTwo top;
+#pragma unroll 4
   for (int i = 0; i < p.per; ++i) {
-    keys[i] = 0;
     const int e = expert_at(p, i, lane);
-    if (e < 0) continue;
-    const float l = logit_at(p.logits, p.dtype, t * p.ld + e), b = p.bias ? __ldg(p.bias + e) : 0.f;
-    if (l == -CUDART_INF_F || b == -CUDART_INF_F) continue;
+    const float l = e >= 0 ? logit_at(p.logits, p.dtype, t * p.ld + e) : -CUDART_INF_F, b = e >= 0 && p.bias ? __ldg(p.bias + e) : 0.f;
     double v = static_cast<double>(l);
     if (by_score) v = (softmax ? exp(v - m) / total : sigmoid64(l)) + static_cast<double>(b);
-    top.take(v);
+    const bool in = l != -CUDART_INF_F && b != -CUDART_INF_F;
+    if (in) top.take(v);
     // (without a bias experts go by their logits)
-    keys[i] = order_key(p.bias ? v : static_cast<double>(l));
+    keys[i] = in ? order_key(p.bias ? v : static_cast<double>(l)) : 0;
   }
   __syncwarp();
   bool kept = true;
@@ -241,74 +243,76 @@ __device__ __noinline__ Chosen choose_exactly(const RouteParams& p, int64_t t, i
   return c;
 }
 
-// The careful value of an expert's choice: FP32, within `err` of the true one.
+// exp(x) by the hardware: 2 + 1.173 |x| units in the last place, 0 below 2^-126.
+__device__ __forceinline__ float exp_coarse(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
+}
+// 1 / x to a unit in the last place (0 for x beyond 2^126).
+__device__ __forceinline__ float reciprocal_coarse(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {      // a NaN stays
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// What the choice compares, to the error that the kernel states for it.
 template <int kMode>
-__device__ __forceinline__ float careful_value(const RouteParams& p, bool biased, float l, float b, float m, float total,
-                                               float& err) {
-  err = 0.f;
-  if (kMode == 0 || !biased) return l;
-  // in units of 2^-23 of the score: the sigmoid's exponential, sum and divide; for softmax the
-  // exponential, |x| / 2 for the rounding of x = l - m, the divide and the total's own
-  // (an average of 3 and half a unit for each of its additions)
-  const float x = l - m;
-  const float s = kMode == 1 ? sigmoid_precise(l) : __fdiv_rn(expf(x), total);
-  const float rel = kMode == 1 ? 4.f : fmaf(fabsf(x), 0.5f, 9.f + 0.5f * static_cast<float>(p.per));
-  const float v = s + b;
-  err = fmaf(fabsf(v), 0x1p-23f, fmaf(s, rel * 0x1p-23f, 0x1p-120f));
-  return v;
+__device__ __forceinline__ float coarse_value(float l, float b, float m, float inv) {
+  if (kMode == 0) return l;
+  return (kMode == 1 ? reciprocal_coarse(1.f + exp_coarse(-l)) : exp_coarse(l - m) * inv) + b;
 }
 
 // The choice where more experts reach the threshold than a warp has lanes (many
-// equal logits, as of a router's first step): top_k rounds of a warp-wide maximum over
-// the careful values.  n = -1: two of them are too near to tell.
+// equal logits, as of a router's first step): top_k rounds of a warp-wide maximum.
+// n = -1: two of them are too near to tell.
 template <int kMode>
-__device__ __noinline__ Chosen choose_of_many(const RouteParams& p, int64_t t, bool kept, float m, float total) {
+__device__ __noinline__ Chosen choose_of_many(const RouteParams& p, int64_t t, bool kept, float m, float inv, float err) {
   const int lane = threadIdx.x % 32;
-  const bool biased = kMode != 0 && p.bias != nullptr;
+  const bool by_value = kMode != 0 && p.bias;          // without a bias experts go by their logits
   Chosen c = {0, -1, 0.f};
-  float cv = 0.f, cb = 0.f, worst_err = 0.f;
-  uint64_t last = ~uint64_t(0);
-  auto at = [&](int i, int& e, float& l, float& b, float& v, float& err) {
-    e = kept ? expert_at(p, i, lane) : -1;
-    if (e < 0) return false;
-    l = logit_at(p.logits, p.dtype, t * p.ld + e);
-    b = biased ? __ldg(p.bias + e) : 0.f;
-    if (l == -CUDART_INF_F || b == -CUDART_INF_F) return false;
-    v = careful_value<kMode>(p, biased, l, b, m, total, err);
-    return true;
-  };
-  int e;
-  float l, b, v, err;
+  float values[64];                                    // (p.per <= 64)
+  uint64_t taken = 0;                                  // places that are left out or chosen
+#pragma unroll 4
+  for (int i = 0; i < p.per; ++i) {
+    const int e = kept ? expert_at(p, i, lane) : -1;
+    const float l = e >= 0 ? logit_at(p.logits, p.dtype, t * p.ld + e) : -CUDART_INF_F, b = e >= 0 && by_value ? __ldg(p.bias + e) : 0.f;
+    values[i] = by_value ? coarse_value<kMode>(l, b, m, inv) : l;
+    if (l == -CUDART_INF_F || b == -CUDART_INF_F) taken |= uint64_t(1) << i;
+  }
+  float cv = 0.f, cb = 0.f;
   for (int j = 0; j < p.top_k; ++j) {
-    uint64_t best = 0;
-    float bl = 0.f, bb = 0.f, bv = 0.f;
-    for (int i = 0; i < p.per; ++i) {
-      if (!at(i, e, l, b, v, err)) continue;
-      worst_err = fmaxf(worst_err, err);
-      const uint64_t key = (static_cast<uint64_t>(order_key(v)) << 32) | static_cast<uint32_t>(~e);
-      if (key < last && key > best) best = key, bl = l, bb = b, bv = v;
-    }
-    const uint32_t hi = __reduce_max_sync(kAll, static_cast<uint32_t>(best >> 32));
-    if (hi == 0) break;                           // none left (values' keys are above 0)
-    const uint32_t lo = __reduce_max_sync(kAll, (best >> 32) == hi ? static_cast<uint32_t>(best) : 0u);
-    const uint64_t won = (static_cast<uint64_t>(hi) << 32) | lo;
-    const int owner = __ffs(static_cast<int>(__ballot_sync(kAll, best == won))) - 1;
-    bl = __shfl_sync(kAll, bl, owner);
-    bb = __shfl_sync(kAll, bb, owner);
-    bv = __shfl_sync(kAll, bv, owner);
-    last = won;
-    if (lane == j) c.e = static_cast<int>(~lo), c.l = bl, cv = bv, cb = bb;
+    float best = -CUDART_INF_F;
+    int at = 0x7fffffff, place = 0;
+    for (int i = 0; i < p.per; ++i)
+      if (!((taken >> i) & 1) && (values[i] > best || at == 0x7fffffff)) best = values[i], place = i, at = expert_at(p, i, lane);
+    const bool some = at != 0x7fffffff;
+    const float top = warp_max(some ? best : -CUDART_INF_F);
+    const int won = __reduce_min_sync(kAll, some && best == top ? at : 0x7fffffff);
+    if (won == 0x7fffffff) break;                      // none left
+    if (some && at == won) taken |= uint64_t(1) << place;
+    if (lane == j) c.e = won, cv = top;
     c.n = j + 1;
   }
-  if (!biased || c.n == 0) return c;
-  const float near = 2.f * warp_max(worst_err);
+  if (lane < c.n) {
+    c.l = logit_at(p.logits, p.dtype, t * p.ld + c.e);
+    cb = by_value ? __ldg(p.bias + c.e) : 0.f;
+  }
+  __syncwarp();
+  if (!by_value || c.n == 0) return c;
+  const float near = 2.f * err;
   const float pv = __shfl_up_sync(kAll, cv, 1), pl = __shfl_up_sync(kAll, c.l, 1), pb = __shfl_up_sync(kAll, cb, 1);
   bool close = lane > 0 && lane < c.n && !(pv - cv > near) && !(pl == c.l && pb == cb);
   const float kv = __shfl_sync(kAll, cv, c.n - 1), kl = __shfl_sync(kAll, c.l, c.n - 1), kb = __shfl_sync(kAll, cb, c.n - 1);
   for (int i = 0; i < p.per; ++i)
-    if (at(i, e, l, b, v, err)) {
-      const uint64_t key = (static_cast<uint64_t>(order_key(v)) << 32) | static_cast<uint32_t>(~e);
-      close |= key < last && !(kv - v > near) && !(l == kl && b == kb);
+    if (!((taken >> i) & 1) && !(kv - values[i] > near)) {
+      const int e = expert_at(p, i, lane);
+      close |= !(logit_at(p.logits, p.dtype, t * p.ld + e) == kl && __ldg(p.bias + e) == kb);
     }
   if (__any_sync(kAll, close)) c.n = -1;
   return c;
@@ -325,164 +329,246 @@ __device__ __noinline__ bool all_equal(const RouteParams& p, int64_t t) {
   return __all_sync(kAll, same);
 }
 
+// A token's ids and weights, from the lanes that hold its chosen.
+__device__ __forceinline__ void write_routes(const RouteParams& p, int64_t t, int lane, const Chosen& c, bool softmax, float m, float total) {
+  const bool here = lane < c.n;
+  float w = 0.f;
+  if (p.renormalize) {
+    // scores over a common factor that cannot vanish: exp(top), where top is the
+    // largest chosen logit (for a sigmoid the smaller of that and 0)
+    float top = warp_max(here ? c.l : -CUDART_INF_F);
+    if (softmax) {
+      w = expf(c.l - top);
+    } else {
+      top = fminf(top, 0.f);
+      w = c.l != c.l ? c.l : __fdiv_rn(expf(fminf(c.l, 0.f) - top), 1.f + expf(-fabsf(c.l)));
+    }
+    w = __fdividef(w, warp_sum(here ? w : 0.f)) * p.scale;
+  } else {
+    w = (softmax ? __fdividef(expf(c.l - m), total) : sigmoid_precise(c.l)) * p.scale;
+  }
+  if (lane < p.top_k) {
+    const int64_t o = t * p.top_k + lane;
+    p.weights[o] = here ? w : 0.f;
+    if (p.id_bits == 64)
+      static_cast<int64_t*>(p.ids)[o] = here ? c.e : -1;
+    else
+      static_cast<int32_t*>(p.ids)[o] = here ? c.e : -1;
+  }
+}
+
+// A lane's places, `none` where it has no expert.  kRun experts in one load where rows allow it.
+template <int kPer, bool kGroups, int kRun, typename Load>
+__device__ __forceinline__ void load_runs(float (&to)[kPer], const RouteParams& p, int part, bool group, float none, Load load) {
+  const int step = (kGroups ? p.lanes : 32) * kRun, first = part * kRun;
+  const int left = (!kGroups || group ? p.group_size : 0) - first;      // (a lane without a group has none)
+#pragma unroll
+  for (int i = 0; i < kPer; i += kRun) {
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) to[i + j] = none;
+    if (i / kRun * step < left) load(first + i / kRun * step, &to[i]);
+  }
+}
+// The bias of a lane's experts.
+template <int kPer, bool kGroups>
+__device__ __forceinline__ void load_bias(float (&to)[kPer], const RouteParams& p, int first, int part, bool group) {
+  const float* src = p.bias + first;
+  auto four = [&](int off, float* f) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = __ldg(src + off + j);
+  };
+  if constexpr (kPer % 8 == 0) {
+    if (p.run == 3) {
+      load_runs<kPer, kGroups, 8>(to, p, part, group, 0.f, [&](int off, float* f) { four(off, f), four(off + 4, f + 4); });
+      return;
+    }
+  }
+  if constexpr (kPer % 4 == 0) {
+    if (p.run == 2) {
+      load_runs<kPer, kGroups, 4>(to, p, part, group, 0.f, four);
+      return;
+    }
+  }
+  load_runs<kPer, kGroups, 1>(to, p, part, group, 0.f, [&](int off, float* f) { f[0] = __ldg(src + off); });
+}
+template <int kPer, bool kGroups>
+__device__ __forceinline__ void load_logits(float (&to)[kPer], const RouteParams& p, int64_t at, int part, bool group) {
+  if (p.dtype == MOE_TYPE_FP32) {
+    const float* src = static_cast<const float*>(p.logits) + at;
+    if constexpr (kPer % 4 == 0) {
+      if (p.run == 2) {
+        load_runs<kPer, kGroups, 4>(to, p, part, group, -CUDART_INF_F, [&](int off, float* f) {
+          const float4 v = __ldg(reinterpret_cast<const float4*>(src + off));
+          f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+        });
+        return;
+      }
+    }
+    load_runs<kPer, kGroups, 1>(to, p, part, group, -CUDART_INF_F, [&](int off, float* f) { f[0] = __ldg(src + off); });
+    return;
+  }
+  const unsigned short* src = static_cast<const unsigned short*>(p.logits) + at;
+  const bool bf16 = p.dtype == MOE_TYPE_BF16;
+  if constexpr (kPer % 8 == 0) {
+    if (p.run == 3) {
+      load_runs<kPer, kGroups, 8>(to, p, part, group, -CUDART_INF_F, [&](int off, float* f) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + off));
+        float w[8];
+        if (bf16) unpack8<__nv_bfloat16>(v, w); else unpack8<__half>(v, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = w[j];
+      });
+      return;
+    }
+  }
+  if (bf16)
+    load_runs<kPer, kGroups, 1>(to, p, part, group, -CUDART_INF_F, [&](int off, float* f) { f[0] = __uint_as_float(static_cast<uint32_t>(__ldg(src + off)) << 16); });
+  else
+    load_runs<kPer, kGroups, 1>(to, p, part, group, -CUDART_INF_F, [&](int off, float* f) { f[0] = __half2float(__ushort_as_half(__ldg(src + off))); });
+}
+
 // kMode: what the choice compares.  0: the logits; 1: sigmoid scores (and
-// bias); 2: softmax scores (and bias).
-template <int kPer, int kMode>
-__global__ void __launch_bounds__(32 * kWarps) route_scores_kernel(const __grid_constant__ RouteParams p) {
-  __shared__ uint64_t s_key[kWarps][32];
+// bias); 2: softmax scores (and bias).  A lane holds kPer experts at most.
+template <int kPer, int kMode, bool kGroups>
+__global__ void __launch_bounds__(32 * kWarps, kPer > 16 ? 1 : kMode == 0 ? 6 : kGroups ? 3 : 4)
+    route_scores_kernel(const __grid_constant__ RouteParams p) {
+  using Mask = std::conditional_t<(kPer > 32), uint64_t, uint32_t>;
+  __shared__ __align__(16) uint64_t s_key[kWarps][32];
   __shared__ int16_t s_cand[kWarps][32];
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int g = lane / p.lanes, part = lane % p.lanes;
-  const int mine = g < p.groups ? (p.group_size - part + p.lanes - 1) / p.lanes : 0;   // experts of this lane
-  const int64_t first = static_cast<int64_t>(g) * p.group_size + part;
+  const int lanes = kGroups ? p.lanes : 32, g = kGroups ? lane / p.lanes : 0, part = lane - g * lanes;
+  const bool group = g < p.groups;
+  const int first = g * p.group_size + (part << p.run), run_step = lanes << p.run, run_mask = (1 << p.run) - 1;
   const int64_t live = p.num_tokens ? min(static_cast<int64_t>(max(*p.num_tokens, 0)), p.M) : p.M;
-  const bool softmax = p.score == MOE_SCORE_SOFTMAX;
+  const bool softmax = kMode == 2 || (kMode == 0 && p.score == MOE_SCORE_SOFTMAX);
   const bool biased = kMode != 0 && p.bias != nullptr;
-  // error of the coarse score, relative to it, in units of 2^-23: the fast exponential's
-  // 2 + 1.173 |x|, the divide's 2 and the sum's half; for softmax |x| / 2 more from the
-  // rounding of x = l - m, and the total's: half a unit for each of its kPer + 5 additions
-  // and an average of its terms' own (exp(-x) (2 + 1.7 x) <= 3)
-  constexpr float kUnit = 0x1p-23f;
-  constexpr float kBase = (kMode == 1 ? 5.f : 9.f + kPer / 2) * kUnit, kSlope = (kMode == 1 ? 1.2f : 1.7f) * kUnit;
 
   constexpr bool kHold = kMode != 0 && kPer <= 16;   // the bias stays in registers
-  float held[kHold ? kPer : 1];
+  float held[kPer];                                  // (unused: no registers)
+  float most_bias = 0.f;                             // of the finite ones
   if (kHold) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) held[i] = biased && i < mine ? __ldg(p.bias + first + i * p.lanes) : 0.f;
+    for (int i = 0; i < kPer; ++i) held[i] = 0.f;
+    if (biased) {
+      if constexpr (kHold) load_bias<kPer, kGroups>(held, p, g * p.group_size, part, group);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (fabsf(held[i]) < CUDART_INF_F) most_bias = fmaxf(most_bias, fabsf(held[i]));
+    }
+  } else if (biased) {
+    for (int e = lane; e < p.E; e += 32)
+      if (const float b = fabsf(__ldg(p.bias + e)); b < CUDART_INF_F) most_bias = fmaxf(most_bias, b);
   }
+  if (kMode != 0) most_bias = warp_max(most_bias);
 
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < p.M;
        t += static_cast<int64_t>(gridDim.x) * kWarps) {
     Chosen c = {0, -1, 0.f};
     float m = 0.f, total = 1.f;
     if (t < live) {
-      // hi: the upper end of each value's interval (-inf: left out), low: the largest lower end
-      float hi[kPer];
-      const int64_t at = t * p.ld + first;
-      if (p.dtype == MOE_TYPE_FP32) {
-        const float* src = static_cast<const float*>(p.logits) + at;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) hi[i] = i < mine ? __ldcs(src + i * p.lanes) : -CUDART_INF_F;
-      } else {
-        const unsigned short* src = static_cast<const unsigned short*>(p.logits) + at;
-        const bool bf16 = p.dtype == MOE_TYPE_BF16;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const uint32_t b = i < mine ? __ldcs(src + i * p.lanes) : bf16 ? 0xff80u : 0xfc00u;
-          hi[i] = bf16 ? __uint_as_float(b << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(b)));
-        }
-      }
-      float low = -CUDART_INF_F;
-      bool nan = false;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        low = fmaxf(low, hi[i]);
-        nan |= hi[i] != hi[i];
-      }
-      if (softmax && (kMode == 2 || !p.renormalize)) {
-        m = warp_max(low);
-        float sum = 0.f;
-        if (kMode == 0) {
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) sum += __expf(hi[i] - m);
-          total = warp_sum(sum);
-        }
-      }
-      float a1 = low, a2 = -CUDART_INF_F, slack = 0.f;      // the group's two largest, and its largest error
-      if (kMode != 0) {
-        float inv = 1.f;
-        if (kMode == 2) {
-          float sum = 0.f;
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) sum += __expf(hi[i] - m);
-          total = warp_sum(sum);
-          inv = __frcp_rn(total);
-        }
-        a1 = low = -CUDART_INF_F;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const float x = kMode == 1 ? hi[i] : hi[i] - m;
-          const float s = kMode == 1 ? __fdividef(1.f, 1.f + __expf(-x)) : __expf(x) * inv;
-          const float b = kHold ? held[kHold ? i : 0] : biased && i < mine ? __ldg(p.bias + first + i * p.lanes) : 0.f;
-          const float v = s + b;
-          const bool out = hi[i] == -CUDART_INF_F || b == -CUDART_INF_F;
-          const float err = fmaf(fabsf(v), 0x1p-22f, fmaf(s, fmaf(fabsf(x), kSlope, kBase), 0x1p-120f));
-          nan |= v != v && !out;
-          hi[i] = out ? -CUDART_INF_F : v + err;
-          low = fmaxf(low, out ? -CUDART_INF_F : v - err);
-          if (p.groups > 1) {
-            const float in = out ? -CUDART_INF_F : v;
-            a2 = fmaxf(a2, fminf(a1, in));
-            a1 = fmaxf(a1, in);
-            slack = fmaxf(slack, out ? 0.f : err);
-          }
-        }
-      }
-      int way = __any_sync(kAll, nan) ? 2 : 0;              // 1: many candidates, 2: in 64 bits
+      float inv = 1.f, err = 0.f;
+      int n = 0, way = 0;                                   // 1: many candidates, 2: in 64 bits
       bool stays = true;                                    // this lane's group
-      if (p.groups > 1 && way == 0) {
-        for (int o = 1; o < p.lanes; o <<= 1) {
-          const float b1 = __shfl_xor_sync(kAll, a1, o);
-          if (kMode != 0) {
-            const float b2 = __shfl_xor_sync(kAll, a2, o);
-            a2 = fmaxf(fmaxf(a2, b2), fminf(a1, b1));
-            slack = fmaxf(slack, __shfl_xor_sync(kAll, slack, o));
+      float v[kPer];                                        // the logits, then the values (-inf: left out)
+      load_logits<kPer, kGroups>(v, p, t * p.ld + g * p.group_size, part, group);
+      float a1 = v[0], a2 = -CUDART_INF_F;                  // the lane's (then group's) two largest
+#pragma unroll
+      for (int i = 1; i < kPer; ++i) {
+        if (kGroups && kMode == 0) a2 = fmaxf(a2, fminf(a1, v[i]));
+        a1 = max_nan(a1, v[i]);
+      }
+      bool nan = a1 != a1;
+      // No value is further than `err` from its true one.  In units of 2^-23 a score is off by
+      // the fast exponential's 2 + 1.173 |x| and the divide's and sum's 3, times itself: for a
+      // sigmoid that is most at the largest logit, or at 0.  For softmax |x| / 2 more from the
+      // rounding of x = l - m, and the total's: half a unit for each of kPer + 5 additions and an
+      // average of its terms' own (exp(-x) (2 + 1.7 x) <= 3); most where x = 0.
+      err = 0.f;
+      if (kMode != 0 || (softmax && !p.renormalize)) m = warp_max(a1);
+      if (kMode == 2 || (kMode == 0 && softmax && !p.renormalize)) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) sum += exp_coarse(v[i] - m);
+        total = warp_sum(sum);
+      }
+      if (kMode != 0) {
+        inv = kMode == 2 ? reciprocal_coarse(total) : 1.f;
+        err = kMode == 1 ? fmaf(fmaxf(m, 0.f), 1.2f, 5.f) : (10.f + kPer / 2) * inv;
+        err = fmaf(err, 0x1p-23f, fmaf(most_bias + 1.f, 0x1p-22f, 0x1p-120f));
+        a1 = -CUDART_INF_F;
+        float any = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const float s = kMode == 1 ? reciprocal_coarse(1.f + exp_coarse(-v[i])) : exp_coarse(v[i] - m) * inv;
+          float x = s + (kHold ? held[i] : 0.f);
+          if (!kHold && biased) {
+            const int e = i < p.per ? expert_at(p, i, lane) : -1;
+            x = s + (e >= 0 ? __ldg(p.bias + e) : 0.f);
           }
+          v[i] = v[i] == -CUDART_INF_F ? v[i] : x;
+          any = max_nan(any, v[i]);
+          if (kGroups) a2 = fmaxf(a2, fminf(a1, v[i]));
+          a1 = fmaxf(a1, v[i]);
+        }
+        nan |= any != any;
+      }
+      float low = a1, second = a2;                          // the lane's two largest values
+      way = __any_sync(kAll, nan) ? 2 : 0;
+      if (kGroups && way == 0) {
+        for (int o = 1; o < lanes; o <<= 1) {
+          const float b1 = __shfl_xor_sync(kAll, a1, o);
+          if (kMode != 0) a2 = fmaxf(fmaxf(a2, __shfl_xor_sync(kAll, a2, o)), fminf(a1, b1));
           a1 = fmaxf(a1, b1);
         }
-        const float v = kMode != 0 && p.pair && a2 != -CUDART_INF_F ? a1 + a2 : a1;
-        const float err = kMode != 0 ? fmaf(fabsf(v), 0x1p-22f, p.pair ? 2.f * slack : slack) : 0.f;
+        const bool pair = kMode != 0 && p.pair && a2 != -CUDART_INF_F;
+        const float x = pair ? a1 + a2 : a1;
         int rank = 0;
         for (int j = 0; j < p.groups; ++j) {
-          const float other = __shfl_sync(kAll, v, j * p.lanes);
-          rank += other > v || (other == v && j < g);
+          const float other = __shfl_sync(kAll, x, j * lanes);
+          rank += other > x || (other == x && j < g);
         }
-        bool kept = g < p.groups && rank < p.topk_groups;
+        stays = group && rank < p.topk_groups;
         if (kMode != 0) {
-          // a group that stays and one that goes nearer than their errors (an infinite
-          // value has an infinite error: its difference is NaN)
-          const float worst = -warp_max(kept ? -(v - err) : -CUDART_INF_F);
-          const float best = warp_max(!kept && g < p.groups && v != -CUDART_INF_F ? v + err : -CUDART_INF_F);
-          if (best != -CUDART_INF_F && !(worst > best) && !all_equal(p, t)) {
+          // a group that stays and one that goes nearer than their errors
+          const float worst = -warp_max(stays ? -x : -CUDART_INF_F), best = warp_max(!stays && group ? x : -CUDART_INF_F);
+          if (best != -CUDART_INF_F && !(worst - best > 4.f * err) && !all_equal(p, t)) {
             // the experts that may be among the two largest of their group, in 64 bits
-            const float floor = (p.pair && a2 != -CUDART_INF_F ? a2 : a1) - slack;
+            const float floor = (pair ? a2 : a1) - 2.f * err;
             uint64_t some = 0;
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
-              if (hi[i] != -CUDART_INF_F && !(hi[i] < floor)) some |= uint64_t(1) << i;
-            kept = groups_exactly<kMode>(p, t, some, m);
+              if (v[i] != -CUDART_INF_F && !(v[i] < floor)) some |= uint64_t(1) << i;
+            stays = groups_exactly<kMode>(p, t, some, m);
           }
         }
-        stays = kept;
-        if (!kept) {
-          low = -CUDART_INF_F;
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) hi[i] = -CUDART_INF_F;
-        }
+        if (!stays) low = second = -CUDART_INF_F;
       }
       if (way == 0) {
-        // the threshold: the top_k-th largest of the lanes' lower ends
-        float cur = low, thr = -CUDART_INF_F;
+        // the threshold: what is below the top_k-th largest of the lanes' two largest (one where all
+        // lanes are in) by more than two errors has top_k others above it
+        float thr = -CUDART_INF_F;
+#pragma unroll 2
         for (int j = 0; j < p.top_k; ++j) {
-          thr = warp_max(cur);
-          if (thr == -CUDART_INF_F) break;
-          if (cur == thr) cur = -CUDART_INF_F;
+          thr = warp_max(low);
+          if (low == thr) low = second, second = -CUDART_INF_F;
         }
-        uint64_t cand = 0;
+        // (what is left out lies below the smallest finite value; a lane whose group goes takes none)
+        thr = fmaxf(kMode == 0 ? thr : thr - 2.f * err, -3.402823466e38f);
+        if (kGroups && !stays) thr = CUDART_NAN_F;
+        Mask cand = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
-          if (hi[i] >= thr && hi[i] != -CUDART_INF_F) cand |= uint64_t(1) << i;
-        int n = 0;
+          if (v[i] >= thr) cand |= Mask(1) << i;
         __syncwarp();                                       // (the last token's reads of s_cand are done)
+        const uint32_t below = (1u << lane) - 1;
         for (uint32_t some = __ballot_sync(kAll, cand != 0); some; some = __ballot_sync(kAll, cand != 0)) {
-          const int pos = n + __popc(some & ((1u << lane) - 1));
           if (cand) {
-            const int i = __ffsll(static_cast<long long>(cand)) - 1;
+            const int pos = n + __popc(some & below);
+            const int i = (kPer > 32 ? __ffsll(static_cast<long long>(cand)) : __ffs(static_cast<int>(cand))) - 1;
             cand &= cand - 1;
-            if (pos < 32) s_cand[warp][pos] = static_cast<int16_t>(first + i * p.lanes);
+            if (pos < 32) s_cand[warp][pos] = static_cast<int16_t>(first + ((i >> p.run) * run_step + (i & run_mask)));
           }
           n += __popc(some);
           if (n > 32) break;
@@ -491,33 +577,34 @@ __global__ void __launch_bounds__(32 * kWarps) route_scores_kernel(const __grid_
         if (n > 32) {
           way = 1;
         } else {
-          const int e = lane < n ? s_cand[warp][lane] : 0;
-          const bool here = lane < n && MOE_IN_BOUNDS(e >= 0 && e < p.E);
+          // the candidates, one a lane
+          const int e = lane < n ? s_cand[warp][lane] : -1;
+          const bool here = e >= 0 && MOE_IN_BOUNDS(e < p.E);
           const float l = here ? logit_at(p.logits, p.dtype, t * p.ld + e) : 0.f;
           const float b = here && biased ? __ldg(p.bias + e) : 0.f;
-          float err;
-          const float v = careful_value<kMode>(p, biased, l, b, m, total, err);
-          if (!here) err = 0.f;
-          // rank: how many are above (equal ones: of lower index)
-          uint64_t key = (static_cast<uint64_t>(order_key(v)) << 32) | static_cast<uint32_t>(~e);
+          const float x = biased ? coarse_value<kMode>(l, b, m, inv) : l;
+          // rank: how many are above (equal ones: of lower index); idle lanes' keys are 0
+          const uint64_t key = here ? (static_cast<uint64_t>(order_key(x)) << 32) | static_cast<uint32_t>(~e) : 0;
           s_key[warp][lane] = key;
           __syncwarp();
           int rank = 0;
-          for (int j = 0; j < n; ++j) rank += s_key[warp][j] > key;
-          if (!here) rank = lane;
+#pragma unroll 1
+          for (int j = 0; j < n; j += 4) {
+            const ulonglong2 k0 = *reinterpret_cast<const ulonglong2*>(&s_key[warp][j]);
+            const ulonglong2 k1 = *reinterpret_cast<const ulonglong2*>(&s_key[warp][j + 2]);
+            rank += (k0.x > key) + (k0.y > key) + (k1.x > key) + (k1.y > key);
+          }
+          int src = place(s_cand[warp], here ? rank : lane, lane);
           c.n = min(n, p.top_k);
-          int src = place(s_cand[warp], rank, lane);
           c.e = __shfl_sync(kAll, e, src);
           c.l = __shfl_sync(kAll, l, src);
           if (biased) {
-            const float sv = __shfl_sync(kAll, v, src), sb = __shfl_sync(kAll, b, src);
-            const float near = 2.f * warp_max(err);
-            // each chosen one against the next, and the last chosen against all behind it;
-            // equal logits of equal biases are equal, whatever their error
-            const int ref = lane < p.top_k ? lane - 1 : p.top_k - 1;
-            const float rv = __shfl_sync(kAll, sv, max(ref, 0)), rl = __shfl_sync(kAll, c.l, max(ref, 0)),
-                        rb = __shfl_sync(kAll, sb, max(ref, 0));
-            const bool close = lane > 0 && lane < n && !(rv - sv > near) && !(rl == c.l && rb == sb);
+            const float sv = __shfl_sync(kAll, x, src), sb = __shfl_sync(kAll, b, src);
+            // each chosen one against the next, and the last chosen against all behind it; equal
+            // logits of equal biases are equal, whatever their error
+            const int ref = max(lane < p.top_k ? lane - 1 : p.top_k - 1, 0);
+            const float rv = __shfl_sync(kAll, sv, ref), rl = __shfl_sync(kAll, c.l, ref), rb = __shfl_sync(kAll, sb, ref);
+            const bool close = lane > 0 && lane < n && !(rv - sv > 2.f * err) && !(rl == c.l && rb == sb);
             if (__any_sync(kAll, close)) {
               rank = rank_exactly<kMode>(p, t, n, e, l, b, m);
               src = place(s_cand[warp], here ? rank : lane, lane);
@@ -527,36 +614,10 @@ __global__ void __launch_bounds__(32 * kWarps) route_scores_kernel(const __grid_
           }
         }
       }
-      if (way == 1) c = choose_of_many<kMode>(p, t, stays, m, total);
+      if (way == 1) c = choose_of_many<kMode>(p, t, stays, m, inv, err);
       if (way == 2 || c.n < 0) c = choose_exactly(p, t, kMode != 0);
     }
-
-    // the weights, by the lanes that hold the chosen
-    const bool here = lane < c.n;
-    float w = 0.f;
-    if (p.renormalize) {
-      // scores over a common factor that cannot vanish: exp(top), where top is the
-      // largest chosen logit (for a sigmoid the smaller of that and 0)
-      float top = warp_max(here ? c.l : -CUDART_INF_F);
-      if (softmax) {
-        w = expf(c.l - top);
-      } else {
-        top = fminf(top, 0.f);
-        w = c.l != c.l ? c.l : __fdiv_rn(expf(fminf(c.l, 0.f) - top), 1.f + expf(-fabsf(c.l)));
-      }
-      const float sum = warp_sum(here ? w : 0.f);
-      w = __fdiv_rn(w, sum) * p.scale;
-    } else {
-      w = (softmax ? __fdiv_rn(expf(c.l - m), total) : sigmoid_precise(c.l)) * p.scale;
-    }
-    if (lane < p.top_k) {
-      const int64_t o = t * p.top_k + lane;
-      p.weights[o] = here ? w : 0.f;
-      if (p.id_bits == 64)
-        static_cast<int64_t*>(p.ids)[o] = here ? c.e : -1;
-      else
-        static_cast<int32_t*>(p.ids)[o] = here ? c.e : -1;
-    }
+    write_routes(p, t, lane, c, softmax, m, total);
   }
 }
 
@@ -588,9 +649,10 @@ template <> struct Logit<__half> {
   static __device__ __forceinline__ __half round(float v) { return __float2half_rn(v); }
 };
 
-// kPer: logits a lane of a dense row (softmax, not renormalised; 0: the others)
+// kPer: words of a lane in a dense row (softmax, not renormalised; 0: the others)
 template <typename T, int kPer>
-__global__ void __launch_bounds__(32 * kWarps) route_scores_backward_kernel(const __grid_constant__ RouteGradParams p) {
+__global__ void __launch_bounds__(32 * kWarps, kPer <= 9 ? 8 : 1)
+    route_scores_backward_kernel(const __grid_constant__ RouteGradParams p) {
   constexpr int kDtype = Logit<T>::kDtype;
   pdl_wait();
   pdl_launch_dependents();
@@ -600,6 +662,32 @@ __global__ void __launch_bounds__(32 * kWarps) route_scores_backward_kernel(cons
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32; t < p.M;
        t += static_cast<int64_t>(gridDim.x) * kWarps) {
     T* row = static_cast<T*>(p.dlogits) + t * p.ldd;
+    // a dense row: kPer words of one or two logits a lane, on their way before the rest
+    // (16 bits: words start at even addresses, which may be one before the row)
+    constexpr int kEach = 4 / static_cast<int>(sizeof(T)), kWords = kPer == 0 ? 1 : kPer;
+    const T* in = static_cast<const T*>(p.logits) + t * p.ld;
+    const int back = kEach == 2 ? static_cast<int>(reinterpret_cast<uintptr_t>(in) >> 1) & 1 : 0;
+    float s[kWords][kEach];
+    if constexpr (kPer != 0) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const int at = kEach * (lane + 32 * i) - back;
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) s[i][j] = -CUDART_INF_F;
+        if (t < live) {
+          if constexpr (kEach == 1) {
+            if (at < p.E) s[i][0] = __ldg(in + at);
+          } else if (at >= 0 && at + 1 < p.E && p.vec) {
+            const float2 v = Pack2<T>::load(__ldg(reinterpret_cast<const unsigned int*>(in + at)));
+            s[i][0] = v.x, s[i][1] = v.y;
+          } else {
+#pragma unroll
+            for (int j = 0; j < kEach; ++j)
+              if (at + j >= 0 && at + j < p.E) s[i][j] = logit_at(in, kDtype, at + j);
+          }
+        }
+      }
+    }
     int64_t e = -1;
     float l = 0.f, dw = 0.f;
     if (t < live && lane < p.top_k) {
@@ -647,26 +735,37 @@ __global__ void __launch_bounds__(32 * kWarps) route_scores_backward_kernel(cons
         for (int i = lane; i < p.E; i += 32) row[i] = Logit<T>::round(0.f);
       }
     } else {
-      constexpr int kHeld = kPer == 0 ? 1 : kPer;
-      float s[kHeld];
       float m = -CUDART_INF_F, sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < kHeld; ++i) {
-        s[i] = t < live && lane + 32 * i < p.E ? logit_at(p.logits, kDtype, t * p.ld + lane + 32 * i) : -CUDART_INF_F;
-        m = fmaxf(m, s[i]);
-      }
+      for (int i = 0; i < kWords; ++i)
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) m = fmaxf(m, s[i][j]);
       m = warp_max(m);
+      const float ref = m == -CUDART_INF_F ? 0.f : m;              // (a row of -inf has no gradient)
 #pragma unroll
-      for (int i = 0; i < kHeld; ++i) {
-        s[i] = s[i] == -CUDART_INF_F ? 0.f : expf(s[i] - m);     // (a row of -inf has no gradient)
-        sum += s[i];
+      for (int i = 0; i < kWords; ++i)
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+          s[i][j] = exp_coarse(s[i][j] - ref);
+          sum += s[i][j];
+        }
+      sum = warp_sum(sum);
+      const float inv = sum == 0.f ? 0.f : __frcp_rn(sum);
+      const float mine = here ? exp_coarse(l - ref) * inv : 0.f;
+      const float mean = warp_sum(here ? dw * mine : 0.f), factor = -p.scale * mean * inv;
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const int at = kEach * (lane + 32 * i) - back;
+        if constexpr (kEach == 1) {
+          if (at < p.E) row[at] = Logit<T>::round(s[i][0] * factor);
+        } else if (at >= 0 && at + 1 < p.E && p.vec) {
+          *reinterpret_cast<unsigned int*>(row + at) = Pack2<T>::store(s[i][0] * factor, s[i][1] * factor);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kEach; ++j)
+            if (at + j >= 0 && at + j < p.E) row[at + j] = Logit<T>::round(s[i][j] * factor);
+        }
       }
-      const float inv = __frcp_rn(warp_sum(sum));
-      const float mine = expf(l - m) * inv;
-      const float mean = warp_sum(here ? dw * mine : 0.f);
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i)
-        if (lane + 32 * i < p.E) row[lane + 32 * i] = Logit<T>::round(s[i] == 0.f ? 0.f : -p.scale * (s[i] * inv) * mean);
       own = p.scale * mine * (sum_dw - mean);
     }
     __syncwarp();
@@ -701,25 +800,28 @@ unsigned warp_grid(int64_t tokens, int sms) {
   return static_cast<unsigned>(want < 1 ? 1 : want > most ? most : want);
 }
 
-template <int kMode>
-auto route_kernel_of(int per) {
-  return per <= 2    ? route_scores_kernel<2, kMode>
-         : per <= 4  ? route_scores_kernel<4, kMode>
-         : per <= 8  ? route_scores_kernel<8, kMode>
-         : per <= 10 ? route_scores_kernel<10, kMode>
-         : per <= 16 ? route_scores_kernel<16, kMode>
-         : per <= 32 ? route_scores_kernel<32, kMode>
-                     : route_scores_kernel<64, kMode>;
+// (places in runs: 4, 8, 12, 16, 32 and 64 hold whole runs of four, all but 4 and 12 of eight)
+template <int kMode, bool kGroups>
+auto route_kernel_of(int per, int run) {
+  return per <= 2 && run == 0   ? route_scores_kernel<2, kMode, kGroups>
+         : per <= 4 && run < 3  ? route_scores_kernel<4, kMode, kGroups>
+         : per <= 8             ? route_scores_kernel<8, kMode, kGroups>
+         : per <= 9 && run == 0 ? route_scores_kernel<9, kMode, kGroups>
+         : per <= 12 && run < 3 ? route_scores_kernel<12, kMode, kGroups>
+         : per <= 16            ? route_scores_kernel<16, kMode, kGroups>
+         : per <= 32            ? route_scores_kernel<32, kMode, kGroups>
+                                : route_scores_kernel<64, kMode, kGroups>;
 }
 
 template <typename T>
-auto route_grad_kernel_of(bool dense, int per) {
-  return !dense      ? route_scores_backward_kernel<T, 0>
-         : per <= 2  ? route_scores_backward_kernel<T, 2>
-         : per <= 4  ? route_scores_backward_kernel<T, 4>
-         : per <= 10 ? route_scores_backward_kernel<T, 10>
-         : per <= 16 ? route_scores_backward_kernel<T, 16>
-                     : route_scores_backward_kernel<T, 64>;
+auto route_grad_kernel_of(bool dense, int words) {
+  return !dense        ? route_scores_backward_kernel<T, 0>
+         : words <= 2  ? route_scores_backward_kernel<T, 2>
+         : words <= 5  ? route_scores_backward_kernel<T, 5>
+         : words <= 9  ? route_scores_backward_kernel<T, 9>
+         : words <= 16 ? route_scores_backward_kernel<T, 16>
+         : words <= 33 ? route_scores_backward_kernel<T, 33>
+                       : route_scores_backward_kernel<T, 64>;
 }
 
 // Checks that both directions share: types, sizes, choices.
@@ -779,7 +881,16 @@ moe_status moe_route_scores(const moe_route_scores_args* a, moe_stream_t stream)
   p.group_size = a->E / p.groups;
   p.lanes = 32;
   while (p.lanes * p.groups > 32) p.lanes /= 2;
+  // runs of 16 bytes where every group of every row starts on them and they waste no more than a
+  // quarter of the places
+  const int bytes = type_bytes(a->dtype), run = 16 / bytes;
+  p.run = 0;
   p.per = static_cast<int>(ceil_div(p.group_size, p.lanes));
+  const int padded = static_cast<int>(ceil_div(p.group_size, p.lanes * run)) * run;
+  if (aligned16(a->logits) && a->ldlogits * bytes % 16 == 0 && p.group_size % run == 0 && 4 * padded <= 5 * p.per) {
+    p.run = bytes == 4 ? 2 : 3;
+    p.per = padded;
+  }
   p.pair = a->group_score == MOE_GROUP_TOP2;
   p.score = a->score;
   p.renormalize = a->renormalize;
@@ -788,9 +899,13 @@ moe_status moe_route_scores(const moe_route_scores_args* a, moe_stream_t stream)
   p.scale = a->routed_scale;
   // without a bias the scores' order is the logits'; sums of two scores have none such
   const bool scored = a->bias || (p.groups > 1 && p.pair);
-  auto kernel = !scored                          ? route_kernel_of<0>(p.per)
-                : a->score == MOE_SCORE_SIGMOID ? route_kernel_of<1>(p.per)
-                                                : route_kernel_of<2>(p.per);
+  const int mode = !scored ? 0 : a->score == MOE_SCORE_SIGMOID ? 1 : 2;
+  auto kernel = p.groups > 1 ? (mode == 0   ? route_kernel_of<0, true>(p.per, p.run)
+                                : mode == 1 ? route_kernel_of<1, true>(p.per, p.run)
+                                            : route_kernel_of<2, true>(p.per, p.run))
+                             : (mode == 0   ? route_kernel_of<0, false>(p.per, p.run)
+                                : mode == 1 ? route_kernel_of<1, false>(p.per, p.run)
+                                            : route_kernel_of<2, false>(p.per, p.run));
   MOE_CUDA_TRY(launch_pdl(kernel, dim3(warp_grid(a->M, dev.sms)), dim3(32 * kWarps), 0, stream, 1, p));
   return MOE_OK;
 }
@@ -833,12 +948,15 @@ moe_status moe_route_scores_backward(const moe_route_scores_backward_args* a, mo
   p.renormalize = a->renormalize;
   p.id_bits = a->id_bits;
   p.scale = a->routed_scale;
-  p.vec = aligned16(a->dlogits) && a->lddlogits * eb % 16 == 0 && a->E * eb % 16 == 0;
   const bool dense = a->score == MOE_SCORE_SOFTMAX && !a->renormalize;
-  const int per = static_cast<int>(ceil_div(a->E, 32));
-  auto kernel = a->dtype == MOE_TYPE_BF16   ? route_grad_kernel_of<__nv_bfloat16>(dense, per)
-                : a->dtype == MOE_TYPE_FP16 ? route_grad_kernel_of<__half>(dense, per)
-                                            : route_grad_kernel_of<float>(dense, per);
+  // whole rows of zeros in 16-byte stores; dense rows of 16 bits in pairs, where input and output have them alike
+  p.vec = dense ? ((reinterpret_cast<uintptr_t>(a->logits) ^ reinterpret_cast<uintptr_t>(a->dlogits)) & 2) == 0 &&
+                      (a->M == 1 || (a->ldlogits - a->lddlogits) % 2 == 0)
+                : aligned16(a->dlogits) && a->lddlogits * eb % 16 == 0 && a->E * eb % 16 == 0;
+  const int words = static_cast<int>(eb == 4 ? ceil_div(a->E, 32) : ceil_div(a->E + 1, 64));
+  auto kernel = a->dtype == MOE_TYPE_BF16   ? route_grad_kernel_of<__nv_bfloat16>(dense, words)
+                : a->dtype == MOE_TYPE_FP16 ? route_grad_kernel_of<__half>(dense, words)
+                                            : route_grad_kernel_of<float>(dense, words);
   MOE_CUDA_TRY(launch_pdl(kernel, dim3(warp_grid(a->M, dev.sms)), dim3(32 * kWarps), 0, stream, 1, p));
   return MOE_OK;
 }
