@@ -1,9 +1,9 @@
-"""One routed expert layer in training, on the library's kernels.
+"""A routed expert layer in training, and the block around it, on the library's kernels.
 
 ``ExpertLayer`` holds the layer's buffers and strings the operators of
 include/moe_train.h together as a training step uses them:
 
-  route     moe_route_topk -> moe_plan -> moe_plan_groups
+  route     moe_route_topk or moe_route_scores -> moe_plan -> moe_plan_groups
   forward   moe_gather_rows -> moe_grouped_gemm (gate/up, SwiGLU epilogue)
             -> moe_grouped_gemm (down) -> moe_sum_routes
   backward  moe_gather_rows (of the output's gradient: the sum's gradient)
@@ -16,6 +16,13 @@ The route weight multiplies the SwiGLU output, so the combine is a plain sum
 and the weights' gradient falls out of the SwiGLU gradient.  The trained
 weights go on to moe_quantize_weight_128x128 and the FP8 forward
 (``quantized``).
+
+With ``scores`` the layer routes by scores (include/moe_block.h): ``route``
+calls moe_route_scores, ``route_backward`` gives the logits' gradient and
+``balance`` moves the balance bias.
+
+``ExpertBlock`` is the layer with what stands around it: norm, router product,
+experts, norm, gate and residual, forward, backward and served in FP8.
 """
 
 import torch
@@ -28,10 +35,14 @@ class ExpertLayer:
 
     tokens: the batch's token count (the buffers' size).  Weights are kept in
     FP32 with a copy in `dtype` that the products read; states in 32 or 8 bits.
+    scores: None for the plain router (the top_k logits, softmax over them), or the
+    keywords of make_route_scores_args that say how to route by scores (score,
+    groups, topk_groups, group_score, renormalize, routed_scale); with
+    ``"balance": True`` among them the layer has a balance bias.
     """
 
     def __init__(self, tokens, H, I, E, top_k, block_m=16, dtype=torch.bfloat16, state_bits=32, weight_decay=0.0,
-                 device="cuda", generator=None):
+                 device="cuda", generator=None, scores=None):
         self.M, self.H, self.I, self.E, self.top_k, self.block_m, self.dtype = tokens, H, I, E, top_k, block_m, dtype
         dev = torch.device(device)
         R = tokens * top_k
@@ -46,6 +57,9 @@ class ExpertLayer:
         self.plan_workspace = empty(max(L.moe_plan_workspace_size(tokens, top_k, E), 256), dt=torch.uint8)
         self.group_start, self.group_rows = empty(E, dt=torch.int32), empty(E, dt=torch.int32)
         self.route_slot = empty(R, dt=torch.int32)
+        self.scores = None if scores is None else {k: v for k, v in scores.items() if k != "balance"}
+        self.bias = torch.zeros(E, device=dev) if scores is not None and scores.get("balance") else None
+        self._routed = None                               # the last route's logits and token count
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
 
         # rows in plan order
@@ -102,17 +116,28 @@ class ExpertLayer:
         if t.dtype not in dtypes:
             raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
 
-    def route(self, logits):
-        """Router, plan and groups from logits [tokens, E] (contiguous, float32 or bfloat16)."""
-        self._batch("logits", logits, self.E, (torch.float32, torch.bfloat16))
-        if not logits.is_contiguous():
+    def route(self, logits, num_tokens=None):
+        """Router, plan and groups from logits [tokens, E] (contiguous, float32 or bfloat16; by scores
+        any row stride and float16 too).  num_tokens [1] int32 on the device, by scores only: the
+        tokens from there on are padding and get no expert."""
+        plain = self.scores is None
+        self._batch("logits", logits, self.E, (torch.float32, torch.bfloat16) + (() if plain else (torch.float16,)))
+        if plain and not logits.is_contiguous():
             raise ValueError("logits: a contiguous tensor is expected")
+        if plain and num_tokens is not None:
+            raise ValueError("num_tokens: the plain router takes whole batches")
         self._forward_done = False
-        L.moe_route_topk(logits, self.top_k, self.topk_ids, self.topk_weights)
+        self._routed = None
+        if plain:
+            L.moe_route_topk(logits, self.top_k, self.topk_ids, self.topk_weights)
+        else:
+            L.moe_route_scores(L.make_route_scores_args(logits, self.topk_ids, self.topk_weights, bias=self.bias,
+                                                        num_tokens=num_tokens, **self.scores))
         L.moe_plan(self.topk_ids, self.E, self.block_m, self.sorted_ids, self.expert_ids, self.num_padded,
                    self.plan_workspace)
         L.moe_plan_groups(self.sorted_ids, self.expert_ids, self.num_padded, self.block_m, self.M * self.top_k,
                           self.group_start, self.group_rows, self.route_slot)
+        self._routed = logits, num_tokens
 
     def forward(self, x):
         """x [tokens, H] -> out [tokens, H] (the layer's own buffer)."""
@@ -141,6 +166,25 @@ class ExpertLayer:
         L.moe_grouped_gemm(self._dxs)
         L.moe_sum_routes(self.dxs, self.dx, self.route_slot, self.top_k)
         return self.dx, self.dweights
+
+    def route_backward(self, dweights, dlogits=None):
+        """The gradient of the last route's logits from the route weights' (as ``backward`` returns
+        it), in the logits' type.  The logits must still hold what was routed."""
+        if self._routed is None:
+            raise RuntimeError("route_backward without a route")
+        logits, num_tokens = self._routed
+        how = {"score": L.SCORE_SOFTMAX} if self.scores is None else {
+            k: v for k, v in self.scores.items() if k in ("score", "renormalize", "routed_scale")}
+        dlogits = torch.empty_like(logits) if dlogits is None else dlogits
+        L.moe_route_scores_backward(L.make_route_scores_backward_args(logits, self.topk_ids, dweights, dlogits,
+                                                                      num_tokens=num_tokens, **how))
+        return dlogits
+
+    def balance(self, rate):
+        """One step of the balance bias towards an even load, from the last route's."""
+        if self.bias is None:
+            raise RuntimeError("the layer has no balance bias")
+        L.moe_route_balance(self.group_rows, self.bias, rate)
 
     def step(self, lr, beta1=0.9, beta2=0.999, eps=1e-8, grad_scale=None, skip=None):
         """One AdamW step of both weights from grads.
@@ -178,3 +222,118 @@ class ExpertLayer:
         w13 = torch.empty_like(out[0][0])
         L.moe_prep_weights(out[0][0], w13)
         return w13, out[0][1], out[1][0], out[1][1]
+
+
+class ExpertBlock:
+    """norm -> router -> experts -> norm, gate, residual, on a stream x [tokens, H] of the layer's type:
+
+      z   = N(x; w_pre)
+      y   = experts(z), routed by scores of z w_router^T
+      out = residual_scale x + gate * N(y; w_post)
+
+    All parameters are FP32; the experts are an ``ExpertLayer`` (``layer``), whose keywords
+    are passed on.  The router's product is a library product in FP32.  gate: a learned
+    factor for each channel, starting at gate_init; None for none.
+    """
+
+    def __init__(self, tokens, H, I, E, top_k, scores=None, gate_init=1.0, residual_scale=1.0, eps=1e-6, dtype=torch.bfloat16,
+                 device="cuda", generator=None, state_bits=32, weight_decay=0.0, **layer):
+        scores = {"score": L.SCORE_SIGMOID, "balance": True} if scores is None else scores
+        self.layer = ExpertLayer(tokens, H, I, E, top_k, dtype=dtype, device=device, generator=generator, scores=scores,
+                                 state_bits=state_bits, weight_decay=weight_decay, **layer)
+        dev = torch.device(device)
+        self.M, self.H, self.E, self.dtype, self.residual_scale, self.eps = tokens, H, E, dtype, residual_scale, eps
+        self.w_router = torch.randn(E, H, device=dev, generator=generator) * H ** -0.5
+        self.w_pre, self.w_post = torch.ones(H, device=dev), torch.ones(H, device=dev)
+        self.gate = None if gate_init is None else torch.full((H,), float(gate_init), device=dev)
+        self.params = {"w_router": self.w_router, "w_pre": self.w_pre, "w_post": self.w_post}
+        if self.gate is not None:
+            self.params["gate"] = self.gate
+        self.grads = {k: torch.zeros_like(p) for k, p in self.params.items()}
+        rows = lambda: torch.empty(tokens, H, dtype=dtype, device=dev)                # noqa: E731
+        self.z, self.out, self.dy, self.dr, self.dx = rows(), rows(), rows(), rows(), rows()
+        self.logits = torch.empty(tokens, E, device=dev)
+        self._workspace = torch.empty(L.moe_norm_residual_workspace_size(tokens, H), dtype=torch.uint8, device=dev)
+        states = [{k: torch.zeros(p.numel(), device=dev) for k in ("exp_avg", "exp_avg_sq")} for p in self.params.values()]
+        self._table = L.AdamWTable([{"param": p.view(-1), "grad": g.view(-1), **s}
+                                    for p, g, s in zip(self.params.values(), self.grads.values(), states)])
+        self._served = None
+        self._x = None                                    # the last forward's stream
+        self.steps = 0
+
+    def _enter(self, x, num_tokens, **out):
+        self.layer._batch("x", x, self.H, (self.dtype,))
+        L.moe_norm_residual(L.make_norm_residual_args(x, z=self.z, w_pre=self.w_pre, eps=self.eps, num_rows=num_tokens, **out))
+        torch.mm(self.z.float(), self.w_router.t(), out=self.logits)
+        self.layer.route(self.logits, num_tokens)
+
+    def _leave(self, x, y, num_tokens):
+        L.moe_norm_residual(L.make_norm_residual_args(y, h=self.out, r=x, gate=self.gate, w_post=self.w_post, eps=self.eps,
+                                                      residual_scale=self.residual_scale, num_rows=num_tokens))
+        return self.out
+
+    def forward(self, x, num_tokens=None):
+        """x [tokens, H] -> out [tokens, H] (the block's own buffer).  num_tokens [1] int32 on the
+        device: rows from there on are padding; their out is not written."""
+        if num_tokens is not None:
+            self.z.zero_()                                # (what padding rows hold goes through the router's product)
+        self._enter(x, num_tokens)
+        y = self.layer.forward(self.z)
+        self._x = x, y, num_tokens
+        return self._leave(x, y, num_tokens)
+
+    def backward(self, dout):
+        """dout [tokens, H] -> dx [tokens, H]; fills grads and the experts' grads.  x must still hold
+        what the last forward pass was given."""
+        if self._x is None:
+            raise RuntimeError("backward without a forward pass")
+        self.layer._batch("dout", dout, self.H, (self.dtype,))
+        x, y, num_tokens = self._x
+        self._x = None
+        if num_tokens is not None:
+            for t in (self.dy, self.dr, self.dx):
+                t.zero_()
+        how = {"eps": self.eps, "workspace": self._workspace, "num_rows": num_tokens}
+        L.moe_norm_residual_backward(L.make_norm_residual_backward_args(
+            y, dh=dout, gate=self.gate, w_post=self.w_post, residual_scale=self.residual_scale, dy=self.dy, dr=self.dr,
+            dgate=self.grads.get("gate"), dw_post=self.grads["w_post"], **how))
+        dz, dweights = self.layer.backward(self.dy)
+        dlogits = self.layer.route_backward(dweights)
+        torch.mm(dlogits.t(), self.z.float(), out=self.grads["w_router"])
+        dz.add_(torch.mm(dlogits, self.w_router))
+        L.moe_norm_residual_backward(L.make_norm_residual_backward_args(
+            x, dh=self.dr, dz=dz, w_pre=self.w_pre, dy=self.dx, dw_pre=self.grads["w_pre"], **how))
+        return self.dx
+
+    def step(self, lr, balance_rate=0.0, **adam):
+        """One AdamW step of all parameters from their grads, and one of the balance bias."""
+        self.steps += 1
+        L.moe_adamw_step(L.make_adamw_args(self._table, lr=lr, step=self.steps, **adam))
+        self.layer.step(lr, **adam)
+        if balance_rate:
+            self.layer.balance(balance_rate)
+        self._served = None
+
+    def serve(self, x, num_tokens=None):
+        """forward in FP8: the entry's norm writes the experts' input as E4M3 codes with 1x128 scales
+        beside the router's, the experts run in moe_fp8_block_scale_forward.  H, I multiples of
+        128, BF16.  The weights are quantised at the first call after a step."""
+        layer = self.layer
+        if self._served is None:
+            dev, I = x.device, layer.I
+            ws = torch.empty(L.moe_forward_workspace_size(self.M, self.H, I, self.E, layer.top_k, layer.block_m, layer.sorted_ids.numel()),
+                             dtype=torch.uint8, device=dev)
+            L.moe_workspace_init(ws)
+            q, q_scale = torch.zeros(self.M, self.H, dtype=torch.uint8, device=dev), torch.zeros(self.M, self.H // 128, device=dev)
+            y = torch.empty(self.M, self.H, dtype=torch.bfloat16, device=dev)
+            w13, w13_scale, w2, w2_scale = layer.quantized()
+            self._served = q, q_scale, y, (w13, w13_scale, w2, w2_scale, ws), L.make_fwd_args(
+                q, q_scale, w13, w13_scale, w2, w2_scale, layer.topk_weights, layer.sorted_ids, layer.expert_ids, layer.num_padded, y, ws,
+                layer.top_k, layer.block_m, device_status=layer.status)
+        q, q_scale, y, _, args = self._served
+        if num_tokens is not None:
+            self.z.zero_()
+        self._enter(x, num_tokens, q=q, q_scale=q_scale)
+        y.zero_()
+        L.moe_fp8_block_scale_forward(args)
+        return self._leave(x, y, num_tokens)
