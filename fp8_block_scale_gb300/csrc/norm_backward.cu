@@ -207,20 +207,19 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_kernel(const __grid
   uint32_t row = blockIdx.x * teams + mine;
   // the stages in turn: `at` holds this row, `free` is for the row stages - 1 further on
   const uint32_t first = smem_u32(memory) + (team / 32) * (At::kWeights * kPiece) +
-                         (threadIdx.x / 32) * (p.stages * (At::kUnits * kPiece));
-  const uint32_t end = first + p.stages * (At::kUnits * kPiece);
+                         (threadIdx.x / 32) * ((kKeep ? p.stages : 2) * (At::kUnits * kPiece));
+  const uint32_t end = first + (kKeep ? p.stages : 2) * (At::kUnits * kPiece);
   uint32_t at = first, free = first;
   int turn = 0;
+  const int stages = kKeep ? p.stages : 2;
   if constexpr (kFixed) {
-    for (int i = 0; i < p.stages - 1; ++i, free += At::kUnits * kPiece) fetch_row(free, row + i * step);
+    for (int i = 0; i < stages - (kKeep ? 1 : 0); ++i, free += At::kUnits * kPiece) fetch_row(free, row + i * step);
   }
   for (; row < live; row += step) {
     if constexpr (kShared) __syncwarp();    // (every lane is done with the row that was there)
-    fetch_row(free, row + (p.stages - 1) * step);
+    if constexpr (kKeep) fetch_row(free, row + (stages - 1) * step);
     if constexpr (kFixed) {
-      if (p.stages == 4)
-        asm volatile("cp.async.wait_group 3;" ::: "memory");
-      else if (p.stages == 3)
+      if (stages == 3)
         asm volatile("cp.async.wait_group 2;" ::: "memory");
       else
         asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -362,7 +361,12 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_kernel(const __grid
         if (p.dy.p) flush(p.dy, 0, at, row);
       }
     }
+    // (two stages: a row's place is asked for again as soon as it is done with)
     free = at;
+    if constexpr (!kKeep) {
+      if constexpr (kShared) __syncwarp();
+      fetch_row(at, row + 2 * step);
+    }
     at = at + At::kUnits * kPiece == end ? first : at + At::kUnits * kPiece;
   }
 
@@ -459,7 +463,7 @@ cudaError_t launch_teams(NormGradParams& p, int sms, int* ctas, cudaStream_t str
   const int64_t want = ceil_div(rows, teams);
   *ctas = static_cast<int>(want < sms ? want : sms < kMaxParts ? sms : kMaxParts);
   p.stages = 2;
-  while (kFixed && p.stages < kMostStages && At::bytes(p.team, teams, p.stages + 1) <= kMostShared) ++p.stages;
+  while (kFixed && kThreads <= kKeepThreads && p.stages < kMostStages && At::bytes(p.team, teams, p.stages + 1) <= kMostShared) ++p.stages;
   const int held = kFixed ? At::bytes(p.team, teams, p.stages) : 0, join = teams > 1 ? kHeld * kVec * 32 * p.team : 0;
   auto kernel = norm_backward_kernel<Tb, Ts, kVec, kPre, kPost, kGate, kThreads>;
   static std::atomic<bool> sized[64];            // per device: the attribute outlasts the call

@@ -41,6 +41,8 @@ class ExpertLayer:
     ``"balance": True`` among them the layer has a balance bias.
     """
 
+    scores = bias = None                                  # the plain router
+
     def __init__(self, tokens, H, I, E, top_k, block_m=16, dtype=torch.bfloat16, state_bits=32, weight_decay=0.0,
                  device="cuda", generator=None, scores=None):
         self.M, self.H, self.I, self.E, self.top_k, self.block_m, self.dtype = tokens, H, I, E, top_k, block_m, dtype
@@ -57,8 +59,9 @@ class ExpertLayer:
         self.plan_workspace = empty(max(L.moe_plan_workspace_size(tokens, top_k, E), 256), dt=torch.uint8)
         self.group_start, self.group_rows = empty(E, dt=torch.int32), empty(E, dt=torch.int32)
         self.route_slot = empty(R, dt=torch.int32)
-        self.scores = None if scores is None else {k: v for k, v in scores.items() if k != "balance"}
-        self.bias = torch.zeros(E, device=dev) if scores is not None and scores.get("balance") else None
+        if scores is not None:
+            self.scores = {k: v for k, v in scores.items() if k != "balance"}
+            self.bias = torch.zeros(E, device=dev) if scores.get("balance") else None
         self._routed = None                               # the last route's logits and token count
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
 
