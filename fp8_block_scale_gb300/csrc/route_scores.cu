@@ -330,7 +330,7 @@ __device__ __noinline__ bool all_equal(const RouteParams& p, int64_t t) {
 }
 
 // A token's ids and weights, from the lanes that hold its chosen.
-__device__ __forceinline__ void write_routes(const RouteParams& p, int64_t t, int lane, const Chosen& c, bool softmax, float m, float total) {
+__device__ __forceinline__ void write_routes(const RouteParams& p, uint32_t t, int lane, const Chosen& c, bool softmax, float m, float total) {
   const bool here = lane < c.n;
   float w = 0.f;
   if (p.renormalize) {
@@ -348,7 +348,7 @@ __device__ __forceinline__ void write_routes(const RouteParams& p, int64_t t, in
     w = (softmax ? __fdividef(expf(c.l - m), total) : sigmoid_precise(c.l)) * p.scale;
   }
   if (lane < p.top_k) {
-    const int64_t o = t * p.top_k + lane;
+    const uint32_t o = t * p.top_k + lane;                  // (M top_k is below 2^31)
     p.weights[o] = here ? w : 0.f;
     if (p.id_bits == 64)
       static_cast<int64_t*>(p.ids)[o] = here ? c.e : -1;
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPer > 16 ? 1 : kMode == 0 ? 6 : 
   const int lanes = kGroups ? p.lanes : 32, g = kGroups ? lane / p.lanes : 0, part = lane - g * lanes;
   const bool group = g < p.groups;
   const int first = g * p.group_size + (part << p.run), run_step = lanes << p.run, run_mask = (1 << p.run) - 1;
-  const int64_t live = p.num_tokens ? min(static_cast<int64_t>(max(*p.num_tokens, 0)), p.M) : p.M;
+  const uint32_t M = static_cast<uint32_t>(p.M), live = p.num_tokens ? min(static_cast<uint32_t>(max(*p.num_tokens, 0)), M) : M;
   const bool softmax = kMode == 2 || (kMode == 0 && p.score == MOE_SCORE_SOFTMAX);
   const bool biased = kMode != 0 && p.bias != nullptr;
 
@@ -463,16 +463,16 @@ __global__ void __launch_bounds__(32 * kWarps, kPer > 16 ? 1 : kMode == 0 ? 6 : 
   }
   if (kMode != 0) most_bias = warp_max(most_bias);
 
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < p.M;
-       t += static_cast<int64_t>(gridDim.x) * kWarps) {
+  for (uint32_t t = blockIdx.x * kWarps + warp; t < M; t += gridDim.x * kWarps) {
     Chosen c = {0, -1, 0.f};
     float m = 0.f, total = 1.f;
     if (t < live) {
       float inv = 1.f, err = 0.f;
-      int n = 0, way = 0;                                   // 1: many candidates, 2: in 64 bits
+      int n = 0, way = 0;                          // 1: many candidates, 2: in 64 bits
       bool stays = true;                                    // this lane's group
       float v[kPer];                                        // the logits, then the values (-inf: left out)
-      load_logits<kPer, kGroups>(v, p, t * p.ld + g * p.group_size, part, group);
+      const int64_t row = static_cast<int64_t>(t) * static_cast<int32_t>(p.ld);        // (both below 2^31)
+      load_logits<kPer, kGroups>(v, p, row + g * p.group_size, part, group);
       float a1 = v[0], a2 = -CUDART_INF_F;                  // the lane's (then group's) two largest
 #pragma unroll
       for (int i = 1; i < kPer; ++i) {
@@ -524,12 +524,15 @@ __global__ void __launch_bounds__(32 * kWarps, kPer > 16 ? 1 : kMode == 0 ? 6 : 
         }
         const bool pair = kMode != 0 && p.pair && a2 != -CUDART_INF_F;
         const float x = pair ? a1 + a2 : a1;
-        int rank = 0;
-        for (int j = 0; j < p.groups; ++j) {
-          const float other = __shfl_sync(kAll, x, j * lanes);
-          rank += other > x || (other == x && j < g);
+        // the topk_groups largest, one after another, of equal ones the lower
+        stays = false;
+        float cur = group ? x : -CUDART_INF_F;
+        for (int j = 0; j < p.topk_groups; ++j) {
+          const float top = warp_max(cur);
+          const uint32_t at = __ballot_sync(kAll, cur == top && group && !stays);
+          if (at == 0) break;
+          if ((lane ^ (__ffs(static_cast<int>(at)) - 1)) < lanes) stays = true, cur = -CUDART_INF_F;      // (lanes is a power of two)
         }
-        stays = group && rank < p.topk_groups;
         if (kMode != 0) {
           // a group that stays and one that goes nearer than their errors
           const float worst = -warp_max(stays ? -x : -CUDART_INF_F), best = warp_max(!stays && group ? x : -CUDART_INF_F);
@@ -580,10 +583,10 @@ __global__ void __launch_bounds__(32 * kWarps, kPer > 16 ? 1 : kMode == 0 ? 6 : 
           // the candidates, one a lane
           const int e = lane < n ? s_cand[warp][lane] : -1;
           const bool here = e >= 0 && MOE_IN_BOUNDS(e < p.E);
-          const float l = here ? logit_at(p.logits, p.dtype, t * p.ld + e) : 0.f;
+          const float l = here ? logit_at(p.logits, p.dtype, row + e) : 0.f;
           const float b = here && biased ? __ldg(p.bias + e) : 0.f;
           const float x = biased ? coarse_value<kMode>(l, b, m, inv) : l;
-          // rank: how many are above (equal ones: of lower index); idle lanes' keys are 0
+          // rank: how many are above (equal ones, frequent in 16 bits: of lower index); idle lanes' keys are 0
           const uint64_t key = here ? (static_cast<uint64_t>(order_key(x)) << 32) | static_cast<uint32_t>(~e) : 0;
           s_key[warp][lane] = key;
           __syncwarp();
@@ -828,7 +831,7 @@ auto route_grad_kernel_of(bool dense, int words) {
 moe_status check_route(int dtype, int id_bits, int score, int64_t M, int E, int top_k, int64_t ld, float scale) {
   if (!is_type(dtype) || (id_bits != 32 && id_bits != 64)) return MOE_ERR_DTYPE;
   if (!ok_routes(M, top_k < 1 ? 1 : top_k) || top_k < 1 || top_k > kRouteMaxTopK || E < 1 || E > kRouteMaxE || ld < E ||
-      ld > kMostElements || (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) || !(scale - scale == 0.f))
+      ld >= (int64_t(1) << 31) || (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) || !(scale - scale == 0.f))
     return MOE_ERR_SHAPE;
   return MOE_OK;
 }
@@ -915,7 +918,7 @@ moe_status moe_route_scores_backward(const moe_route_scores_backward_args* a, mo
   if (!a) return MOE_ERR_NULL;
   const moe_status bad = check_route(a->dtype, a->id_bits, a->score, a->M, a->E, a->top_k, a->ldlogits, a->routed_scale);
   if (bad != MOE_OK) return bad;
-  if (a->lddlogits < a->E || a->lddlogits > kMostElements) return MOE_ERR_SHAPE;
+  if (a->lddlogits < a->E || a->lddlogits >= (int64_t(1) << 31)) return MOE_ERR_SHAPE;
   if (a->M == 0) return MOE_OK;
   if (!a->logits || !a->topk_ids || !a->dweights || !a->dlogits) return MOE_ERR_NULL;
   const int eb = type_bytes(a->dtype), ib = a->id_bits / 8;

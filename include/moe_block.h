@@ -73,7 +73,7 @@ typedef struct moe_route_scores_args {
 } moe_route_scores_args;
 
 /* 1 <= E <= 2048; 1 <= groups <= 32, E % groups == 0; 1 <= topk_groups <=
- * groups; 1 <= top_k <= min(32, topk_groups * E / groups); ldlogits >= E;
+ * groups; 1 <= top_k <= min(32, topk_groups * E / groups); E <= ldlogits < 2^31;
  * M * top_k < 2^31.  Pointers aligned to their elements; the outputs overlap
  * no input and not one another. */
 moe_status moe_route_scores(const moe_route_scores_args* args, moe_stream_t stream);
