@@ -38,6 +38,13 @@ __device__ __forceinline__ float scale_to_pow2(float s) {
   return top + 1 >= 23 ? __uint_as_float(1u << 23) : __uint_as_float(1u << (top + 1));
 }
 
+// The larger one; a NaN stays (it reaches the scale: the codes alone could lose it).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Eight values over one scale as E4M3 codes, each from the correctly rounded quotient: the product
 // with the reciprocal, corrected twice by its residual (Markstein), which is exact where no
 // value that rounds to a code is near FP32's smallest; one of them by a divide otherwise.
@@ -268,10 +275,10 @@ __global__ void __launch_bounds__(1024, 1) norm_kernel(const __grid_constant__ N
           float amax = 0.f;
           if (live_column) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fmaxf(fabsf(h[v][i].x), fabsf(h[v][i].y)));
+            for (int i = 0; i < 4; ++i) amax = max_nan(amax, max_nan(fabsf(h[v][i].x), fabsf(h[v][i].y)));
           }
 #pragma unroll
-          for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          for (int o = 8; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
           float s = __fdiv_rn(amax, 448.f);
           if (p.pow2 && s > 0.f) s = scale_to_pow2(s);
           if (live_column && MOE_IN_BOUNDS(row < M)) {

@@ -2,17 +2,23 @@
 // step: softmax or sigmoid scores, a bias that only the choice sees, groups of
 // experts, top-k, renormalised weights.
 //
-// One warp per token.  The choice is that of 64-bit arithmetic, in three steps of
-// rising care.  Every expert's value is formed with the hardware's exponential
-// and reciprocal together with a bound on its error, which gives an interval that
-// holds the true value; the top_k-th largest lower end over the lanes is a
-// threshold that every chosen expert's upper end reaches.  The few experts that
-// reach it (a dozen for top_k = 8) go to a lane each and are formed again, to
-// a few units in the last place, and ranked against one another.  Only where two
-// neighbours of that order are nearer than their errors (once in some thousand
-// tokens) are the candidates' values formed in 64 bits.  GB300 has two 64-bit
-// lanes per SM and clock, so that forming all of them so would take a
-// hundred times as long as reading them.
+// One warp per token.  The choice is that of 64-bit arithmetic, in steps of rising care.  Every
+// expert's value is formed with the hardware's exponential and reciprocal, within a bound that
+// holds for all of the token's.  The top_k-th largest of the lanes' two largest values, less
+// two such errors, is a threshold that every chosen expert reaches.  The few experts that reach
+// it (a dozen for top_k = 8) go to a lane each and are ranked against one another.  Only where
+// two neighbours of that order, or a group that stays and one that goes, are nearer than their
+// errors (a few tokens in a thousand) are the values in question formed in 64 bits.  GB300 has two
+// 64-bit lanes per SM and clock: forming all of them so would take a hundred times as long as
+// reading them.
+//
+// Without a bias the scores' order is the logits' own, which are compared as they are.
+//
+// Instructions bound it, and of those mostly the ones that a token costs whatever E is: 16-bit
+// logits of 257 experts, top 9, take some 480 (65536 tokens: 30 us, 1.2 TB/s); sigmoid scores with
+// a bias, 8 groups and top 10 of 512 experts some 1050 (8192 tokens: 17.5 us).  Two tokens finished
+// side by side by half a warp each (10% fewer instructions, fewer warps) and warps that stay
+// for many tokens (40 us) were slower.
 #include <math_constants.h>
 
 #include <type_traits>
@@ -44,7 +50,7 @@ struct RouteParams {
 
 __device__ __forceinline__ float warp_max(float v) {   // NaN has no part
   float r;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));   // (all lanes: it may not move into a branch)
   return r;
 }
 __device__ __forceinline__ float warp_sum(float v) {
@@ -446,7 +452,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPer > 16 ? 1 : kMode == 0 ? 6 : 
   const bool biased = kMode != 0 && p.bias != nullptr;
 
   constexpr bool kHold = kMode != 0 && kPer <= 16;   // the bias stays in registers
-  float held[kPer];                                  // (unused: no registers)
+  float held[kPer];                                  // (only then)
   float most_bias = 0.f;                             // of the finite ones
   if (kHold) {
 #pragma unroll
@@ -496,7 +502,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPer > 16 ? 1 : kMode == 0 ? 6 : 
       if (kMode != 0) {
         inv = kMode == 2 ? reciprocal_coarse(total) : 1.f;
         err = kMode == 1 ? fmaf(fmaxf(m, 0.f), 1.2f, 5.f) : (10.f + kPer / 2) * inv;
-        err = fmaf(err, 0x1p-23f, fmaf(most_bias + 1.f, 0x1p-22f, 0x1p-120f));
+        err = fmaf(err, 0x1p-23f, fmaf(most_bias + inv, 0x1p-22f, 0x1p-120f));          // (and the addition's half: a score is at most inv)
         a1 = -CUDART_INF_F;
         float any = 0.f;
 #pragma unroll
@@ -580,7 +586,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPer > 16 ? 1 : kMode == 0 ? 6 : 
         if (n > 32) {
           way = 1;
         } else {
-          // the candidates, one a lane
+          // the candidates, one a lane, formed as before
           const int e = lane < n ? s_cand[warp][lane] : -1;
           const bool here = e >= 0 && MOE_IN_BOUNDS(e < p.E);
           const float l = here ? logit_at(p.logits, p.dtype, row + e) : 0.f;

@@ -120,7 +120,8 @@ moe_status moe_route_balance(const int32_t* load, const float* bias, float* out,
  *   h = residual_scale * r + gate * u              (r NULL: gate * u)
  *   z = N(h; w_pre)
  *   q, q_scale = z in E4M3 with one scale per 128 columns, as
- *                moe_quantize_act_1x128 (or _ue8m0) forms them
+ *                moe_quantize_act_1x128 (or _ue8m0) forms them; a NaN in a group
+ *                makes its scale NaN
  * z and q come from the unrounded h, and q from the unrounded z.  h, z and q
  * are nullable (one of them is written at least); r, gate and the weights are
  * too.  Padding rows are not touched.

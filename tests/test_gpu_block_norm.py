@@ -140,7 +140,12 @@ def test_forward_in_place_zero_rows_and_nan():
     assert (h[3] == 0).all() and (z[3] == 0).all() and (q[3] == 0).all() and (qs[3] == 0).all()
     for bad in (5, 6):
         assert z[bad].isnan().any()
+    # and its group's dequantised values, whichever of them it is
+    deq = q.view(torch.float8_e4m3fn).float().view(M, H // 128, 128) * qs[:, :, None]
+    for bad in (5, 6):
+        assert (deq[bad].isnan().any(1) == z[bad].view(H // 128, 128).isnan().any(1)).all()
     good = [i for i in range(M) if i not in (5, 6)]
+    assert not deq[good].isnan().any()
     assert not z[good].isnan().any() and not h[good].isnan().any()
     y2, r2 = y.clone(), r.clone()
     L.moe_norm_residual(L.make_norm_residual_args(y2, h=r2, z=y2, r=r2, w_post=w, w_pre=w))
