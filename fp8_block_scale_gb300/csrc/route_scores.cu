@@ -15,10 +15,12 @@
 // Without a bias the scores' order is the logits' own, which are compared as they are.
 //
 // Instructions bound it, and of those mostly the ones that a token costs whatever E is: 16-bit
-// logits of 257 experts, top 9, take some 480 (65536 tokens: 30 us, 1.2 TB/s); sigmoid scores with
-// a bias, 8 groups and top 10 of 512 experts some 1050 (8192 tokens: 17.5 us).  Two tokens finished
+// logits of 257 experts, top 9, take some 480 (65536 tokens: 30.4 us, 1.26 TB/s); sigmoid scores with
+// a bias, 8 groups and top 10 of 512 experts some 1080 (8192 tokens: 12.0 us).  Two tokens finished
 // side by side by half a warp each (10% fewer instructions, fewer warps) and warps that stay
-// for many tokens (40 us) were slower.
+// for many tokens (40 us) were slower.  The 64 bits count where a token is among the last ones: of
+// 8192, two or three have groups too near to tell, which cost 2 us until only the groups in
+// question were formed so.
 #include <math_constants.h>
 
 #include <type_traits>
@@ -30,7 +32,10 @@
 namespace moe {
 namespace {
 
-constexpr int kWarps = 8;
+// Warps of a CTA.  Where scores are compared a warp has one token, and small CTAs fill the places that
+// finished ones leave (8192 tokens of 512 experts in groups: 12.0 us, 12.3 with eight warps); where logits
+// are, a warp takes several of many tokens (65536 tokens of 257 experts: 30.4 us, 31.2 with four).
+constexpr int kWarps = 8, kWarpsScored = 4;
 constexpr uint32_t kAll = 0xffffffffu;
 
 struct RouteParams {
@@ -155,21 +160,23 @@ struct TopTwo {
   }
 };
 
-// Whether this lane's group is among those that stay, from its two largest values.
-__device__ __forceinline__ bool group_stays(const RouteParams& p, const TopTwo& top) {
+// Whether this lane's group is among the `slots` best of those in question, from its two largest values.
+__device__ __forceinline__ bool group_stays(const RouteParams& p, const TopTwo& top, bool in_question, int slots) {
   const int g = (threadIdx.x % 32) / p.lanes;
   const uint64_t key = top.k1 == 0 ? 0 : p.pair && top.k2 != 0 ? order_key(top.a1 + top.a2) : top.k1;
+  const uint32_t some = __ballot_sync(kAll, in_question);
   int rank = 0;
   for (int j = 0; j < p.groups; ++j) {
+    if (!((some >> (j * p.lanes)) & 1)) continue;
     const uint64_t other = __shfl_sync(kAll, key, j * p.lanes);
     rank += other > key || (other == key && j < g);
   }
-  return g < p.groups && rank < p.topk_groups;
+  return in_question && rank < slots;
 }
 
-// The groups in 64 bits, from the places `some` of this lane (the others cannot count).
+// The groups in question in 64 bits, from the places `some` of this lane (the others cannot count).
 template <int kMode>
-__device__ __noinline__ bool groups_exactly(const RouteParams& p, int64_t t, uint64_t some, float m) {
+__device__ __noinline__ bool groups_exactly(const RouteParams& p, int64_t t, uint64_t some, float m, bool in_question, int slots) {
   const int lane = threadIdx.x % 32;
   const double total = kMode == 2 ? softmax_total(p, t, m) : 1.0;
   TopTwo top;
@@ -182,7 +189,7 @@ __device__ __noinline__ bool groups_exactly(const RouteParams& p, int64_t t, uin
   }
   __syncwarp();
   top.merge(p.lanes);
-  return group_stays(p, top);
+  return group_stays(p, top, in_question, slots);
 }
 
 // The lane whose rank is this lane's number (ranks are distinct).
@@ -222,7 +229,7 @@ __device__ __noinline__ Chosen choose_exactly(const RouteParams& p, int64_t t, i
   bool kept = true;
   if (p.groups > 1) {
     top.merge(p.lanes);
-    kept = group_stays(p, top);
+    kept = group_stays(p, top, lane / p.lanes < p.groups, p.topk_groups);
   }
   Chosen c = {0, -1, 0.f};
   for (int j = 0; j < p.top_k; ++j) {
@@ -375,13 +382,13 @@ __device__ __forceinline__ void load_runs(float (&to)[kPer], const RouteParams& 
     if (i / kRun * step < left) load(first + i / kRun * step, &to[i]);
   }
 }
-// The bias of a lane's experts.
+// The bias of a lane's experts (in runs: on 16 bytes, too).
 template <int kPer, bool kGroups>
 __device__ __forceinline__ void load_bias(float (&to)[kPer], const RouteParams& p, int first, int part, bool group) {
   const float* src = p.bias + first;
   auto four = [&](int off, float* f) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) f[j] = __ldg(src + off + j);
+    const float4 v = __ldg(reinterpret_cast<const float4*>(src + off));
+    f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
   };
   if constexpr (kPer % 8 == 0) {
     if (p.run == 3) {
@@ -436,11 +443,12 @@ __device__ __forceinline__ void load_logits(float (&to)[kPer], const RouteParams
 // kMode: what the choice compares.  0: the logits; 1: sigmoid scores (and
 // bias); 2: softmax scores (and bias).  A lane holds kPer experts at most.
 template <int kPer, int kMode, bool kGroups>
-__global__ void __launch_bounds__(32 * kWarps, kPer > 16 ? 1 : kMode == 0 ? 6 : kGroups ? 3 : 4)
+__global__ void __launch_bounds__(32 * (kMode == 0 ? kWarps : kWarpsScored), kPer > 16 ? 1 : kMode == 0 ? 6 : 8)
     route_scores_kernel(const __grid_constant__ RouteParams p) {
+  constexpr int kTokens = kMode == 0 ? kWarps : kWarpsScored;
   using Mask = std::conditional_t<(kPer > 32), uint64_t, uint32_t>;
-  __shared__ __align__(16) uint64_t s_key[kWarps][32];
-  __shared__ int16_t s_cand[kWarps][32];
+  __shared__ __align__(16) uint64_t s_key[kTokens][32];
+  __shared__ int16_t s_cand[kTokens][32];
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -469,7 +477,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPer > 16 ? 1 : kMode == 0 ? 6 : 
   }
   if (kMode != 0) most_bias = warp_max(most_bias);
 
-  for (uint32_t t = blockIdx.x * kWarps + warp; t < M; t += gridDim.x * kWarps) {
+  for (uint32_t t = blockIdx.x * kTokens + warp; t < M; t += gridDim.x * kTokens) {
     Chosen c = {0, -1, 0.f};
     float m = 0.f, total = 1.f;
     if (t < live) {
@@ -541,15 +549,24 @@ __global__ void __launch_bounds__(32 * kWarps, kPer > 16 ? 1 : kMode == 0 ? 6 : 
         }
         if (kMode != 0) {
           // a group that stays and one that goes nearer than their errors
-          const float worst = -warp_max(stays ? -x : -CUDART_INF_F), best = warp_max(!stays && group ? x : -CUDART_INF_F);
-          if (best != -CUDART_INF_F && !(worst - best > 4.f * err) && !all_equal(p, t)) {
-            // the experts that may be among the two largest of their group, in 64 bits
-            const float floor = (pair ? a2 : a1) - 2.f * err;
-            uint64_t some = 0;
+          const float worst = -warp_max(stays ? -x : -CUDART_INF_F), best = warp_max(!stays && group ? x : -CUDART_INF_F), near = 4.f * err;
+          if (best != -CUDART_INF_F && !(worst - best > near)) {
+            // (equal experts, as of a router's first step, are equal whatever their error)
+            bool same = true;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i)
-              if (v[i] != -CUDART_INF_F && !(v[i] < floor)) some |= uint64_t(1) << i;
-            stays = groups_exactly<kMode>(p, t, some, m);
+            for (int i = 0; i < kPer; ++i) same &= v[i] == a1 || v[i] == -CUDART_INF_F;
+            if (!(__all_sync(kAll, same) && all_equal(p, t))) {
+              // which ones are in question: their experts that may be among their two largest, in 64 bits
+              const bool in_question = group && !(stays ? x - best > near : worst - x > near);
+              const int sure = __popc(__ballot_sync(kAll, stays && !in_question)) / lanes;
+              const float floor = (pair ? a2 : a1) - 2.f * err;
+              uint64_t some = 0;
+#pragma unroll
+              for (int i = 0; i < kPer; ++i)
+                if (v[i] != -CUDART_INF_F && !(v[i] < floor)) some |= uint64_t(1) << i;
+              const bool among = groups_exactly<kMode>(p, t, in_question ? some : 0, m, in_question, p.topk_groups - sure);
+              if (in_question) stays = among;
+            }
           }
         }
         if (!stays) low = second = -CUDART_INF_F;
@@ -627,12 +644,19 @@ __global__ void __launch_bounds__(32 * kWarps, kPer > 16 ? 1 : kMode == 0 ? 6 : 
       if (way == 2 || c.n < 0) c = choose_exactly(p, t, kMode != 0);
     }
     write_routes(p, t, lane, c, softmax, m, total);
+    if (kMode != 0) break;
   }
 }
 
 // The logits' gradient.  One warp per token: the chosen logits go to a lane each, the
 // row is written in whole lines (zeros, or for plain softmax every expert's
 // -s sum(dw s)), then the chosen places by their lanes, after a warp barrier.
+//
+// Zeros: the writes bound it (8192 tokens of 512 experts, FP32: 6.0 us, 3.0 TB/s into L2 and
+// HBM, launch included).  Dense rows: two loads one after the other (ids, their logits), two
+// sums over the warp and 360 instructions a token (65536 tokens of 257 experts in 16 bits: 32 us,
+// 2.25 TB/s); pairs of 16-bit logits, 42 us one at a time.  Loads of the next token ahead and both sums
+// in one exchange changed nothing; six CTAs an SM instead of eight 38 us.
 struct RouteGradParams {
   const void* logits;
   const void* ids;
@@ -666,15 +690,14 @@ __global__ void __launch_bounds__(32 * kWarps, kPer <= 9 ? 8 : 1)
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x % 32;
-  const int64_t live = p.num_tokens ? min(static_cast<int64_t>(max(*p.num_tokens, 0)), p.M) : p.M;
+  const uint32_t M = static_cast<uint32_t>(p.M), live = p.num_tokens ? min(static_cast<uint32_t>(max(*p.num_tokens, 0)), M) : M;
   const bool softmax = p.score == MOE_SCORE_SOFTMAX;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32; t < p.M;
-       t += static_cast<int64_t>(gridDim.x) * kWarps) {
-    T* row = static_cast<T*>(p.dlogits) + t * p.ldd;
+  for (uint32_t t = blockIdx.x * kWarps + threadIdx.x / 32; t < M; t += gridDim.x * kWarps) {
+    T* row = static_cast<T*>(p.dlogits) + static_cast<int64_t>(t) * static_cast<int32_t>(p.ldd);
     // a dense row: kPer words of one or two logits a lane, on their way before the rest
     // (16 bits: words start at even addresses, which may be one before the row)
     constexpr int kEach = 4 / static_cast<int>(sizeof(T)), kWords = kPer == 0 ? 1 : kPer;
-    const T* in = static_cast<const T*>(p.logits) + t * p.ld;
+    const T* in = static_cast<const T*>(p.logits) + static_cast<int64_t>(t) * static_cast<int32_t>(p.ld);
     const int back = kEach == 2 ? static_cast<int>(reinterpret_cast<uintptr_t>(in) >> 1) & 1 : 0;
     float s[kWords][kEach];
     if constexpr (kPer != 0) {
@@ -697,22 +720,28 @@ __global__ void __launch_bounds__(32 * kWarps, kPer <= 9 ? 8 : 1)
         }
       }
     }
-    int64_t e = -1;
+    int e = -1;
     float l = 0.f, dw = 0.f;
     if (t < live && lane < p.top_k) {
-      const int64_t o = t * p.top_k + lane;
-      e = p.id_bits == 64 ? __ldg(static_cast<const long long*>(p.ids) + o) : __ldg(static_cast<const int32_t*>(p.ids) + o);
+      const uint32_t o = t * p.top_k + lane;                  // (M top_k is below 2^31)
+      if (p.id_bits == 64) {
+        const long long id = __ldg(static_cast<const long long*>(p.ids) + o);
+        e = id >= 0 && id < p.E ? static_cast<int>(id) : -1;
+      } else {
+        e = __ldg(static_cast<const int32_t*>(p.ids) + o);
+      }
       dw = __ldg(p.dweights + o);
     }
     bool here = e >= 0 && e < p.E;
     if (here) {
-      l = logit_at(p.logits, kDtype, t * p.ld + e);
+      l = logit_at(in, kDtype, e);
       here = l != -CUDART_INF_F;
     }
     // an expert listed more than once counts by all of its terms: their sum and number
-    const uint32_t same = __match_any_sync(kAll, here ? static_cast<int>(e) : -1 - lane);
+    // (the match goes from one value to the next: idle lanes share theirs)
+    const uint32_t same = __match_any_sync(kAll, here ? e : -1);
     float sum_dw = dw, terms = 1.f;
-    if (__any_sync(kAll, __popc(same) > 1)) {
+    if (__any_sync(kAll, here && __popc(same) > 1)) {
       sum_dw = terms = 0.f;
       for (int j = 0; j < p.top_k; ++j) {
         const float x = __shfl_sync(kAll, dw, j);
@@ -890,13 +919,13 @@ moe_status moe_route_scores(const moe_route_scores_args* a, moe_stream_t stream)
   p.group_size = a->E / p.groups;
   p.lanes = 32;
   while (p.lanes * p.groups > 32) p.lanes /= 2;
-  // runs of 16 bytes where every group of every row starts on them and they waste no more than a
+  // runs of 16 bytes where every group of every row and of the bias starts on them and they waste no more than a
   // quarter of the places
   const int bytes = type_bytes(a->dtype), run = 16 / bytes;
   p.run = 0;
   p.per = static_cast<int>(ceil_div(p.group_size, p.lanes));
   const int padded = static_cast<int>(ceil_div(p.group_size, p.lanes * run)) * run;
-  if (aligned16(a->logits) && a->ldlogits * bytes % 16 == 0 && p.group_size % run == 0 && 4 * padded <= 5 * p.per) {
+  if (aligned16(a->logits) && aligned16(a->bias) && a->ldlogits * bytes % 16 == 0 && p.group_size % run == 0 && 4 * padded <= 5 * p.per) {
     p.run = bytes == 4 ? 2 : 3;
     p.per = padded;
   }
@@ -915,7 +944,9 @@ moe_status moe_route_scores(const moe_route_scores_args* a, moe_stream_t stream)
                              : (mode == 0   ? route_kernel_of<0, false>(p.per, p.run)
                                 : mode == 1 ? route_kernel_of<1, false>(p.per, p.run)
                                             : route_kernel_of<2, false>(p.per, p.run));
-  MOE_CUDA_TRY(launch_pdl(kernel, dim3(warp_grid(a->M, dev.sms)), dim3(32 * kWarps), 0, stream, 1, p));
+  const int warps = mode == 0 ? kWarps : kWarpsScored;
+  const unsigned grid = mode == 0 ? warp_grid(a->M, dev.sms) : static_cast<unsigned>(ceil_div(a->M, warps));
+  MOE_CUDA_TRY(launch_pdl(kernel, dim3(grid), dim3(32 * warps), 0, stream, 1, p));
   return MOE_OK;
 }
 
