@@ -120,6 +120,46 @@ def test_values_near_or_equal(kind):
             check(l, k, torch.bfloat16, score=score, groups=groups, topk_groups=keep)
 
 
+@pytest.mark.parametrize("near,keep", [(2, 4), (3, 2), (4, 5), (2, 1), (7, 4)])
+@pytest.mark.parametrize("score", [B.SIGMOID, B.SOFTMAX])
+def test_some_groups_too_near_to_tell(near, keep, score):
+    """`near` groups of eight around the cut whose two largest differ in last places only, the others far above or below."""
+    rng = np.random.default_rng(19 + near)
+    M, G, size, k = 64, 8, 16, 12
+    first = max(keep - 1 - near // 2, 0)                     # the cut lies among the groups first .. first + near - 1
+    l = np.zeros((M, G, size), np.float32)
+    for t in range(M):
+        for rank, g in enumerate(rng.permutation(G)):
+            at = rng.permutation(size)
+            among = first <= rank < first + near
+            top = np.float32(2.0 - 0.25 * (first if among else rank))
+            two = np.array([top, top - np.float32(0.0625)])
+            if among:
+                steps = rng.integers(-2, 3, 2) if t % 2 else np.array([1, -1]) * rng.integers(-2, 3)
+                two = two + steps.astype(np.float32) * np.spacing(two)
+            l[t, g] = -4.0 - rng.random(size)
+            l[t, g, at[:2]] = two
+    l = l.reshape(M, G * size)
+    bias = rng.integers(-1, 2, size) * 2.0 ** -25
+    for b in (None, np.zeros(G * size), np.tile(bias, G), rng.standard_normal(G * size) * 2.0 ** -27):
+        check(l, k, bias=b, score=score, groups=G, topk_groups=keep, group_score=B.GROUP_TOP2)
+        check(l, k, bias=b, score=score, groups=G, topk_groups=keep, group_score=B.GROUP_MAX, renormalize=False)
+
+
+@pytest.mark.parametrize("E,groups", [(512, 8), (64, 1), (257, 1)])
+def test_bias_off_its_16_bytes(E, groups):
+    rng = np.random.default_rng(E)
+    lg = device((rng.standard_normal((70, E))).astype(np.float32), torch.float32)
+    wide = torch.full((E + 8,), float("nan"), device="cuda")
+    ids, w = torch.zeros(70, 6, dtype=torch.int32, device="cuda"), torch.zeros(70, 6, device="cuda")
+    for off in (0, 1, 2, 3, 4):
+        bias = wide[off:off + E]
+        bias.copy_(torch.from_numpy(rng.standard_normal(E) * 0.1))
+        L.moe_route_scores(L.make_route_scores_args(lg, ids, w, bias=bias, groups=groups, topk_groups=max(groups // 2, 1)))
+        want, _ = B.route_scores(lg.double().cpu().numpy(), 6, bias=bias.cpu().numpy(), groups=groups, topk_groups=max(groups // 2, 1))
+        assert (ids.cpu().numpy() == want).all(), off
+
+
 def test_left_out_experts_empty_rows_and_padding():
     rng = np.random.default_rng(3)
     M, E, k = 40, 60, 5
