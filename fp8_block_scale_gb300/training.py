@@ -187,6 +187,8 @@ class ExpertLayer:
         """One step of the balance bias towards an even load, from the last route's."""
         if self.bias is None:
             raise RuntimeError("the layer has no balance bias")
+        if self._routed is None:
+            raise RuntimeError("balance without a route")
         L.moe_route_balance(self.group_rows, self.bias, rate)
 
     def step(self, lr, beta1=0.9, beta2=0.999, eps=1e-8, grad_scale=None, skip=None):
@@ -262,10 +264,20 @@ class ExpertBlock:
                                     for p, g, s in zip(self.params.values(), self.grads.values(), states)])
         self._served = None
         self._x = None                                    # the last forward's stream
-        self.steps = 0
+
+    @property
+    def steps(self):
+        return self.layer.steps
+
+    @staticmethod
+    def _apart(name, t, own):
+        if t.numel() and any(t.untyped_storage().data_ptr() == o.untyped_storage().data_ptr() for o in own):
+            raise ValueError(f"{name}: a buffer of the block itself")
 
     def _enter(self, x, num_tokens, **out):
         self.layer._batch("x", x, self.H, (self.dtype,))
+        self._apart("x", x, (self.z, self.out, self.layer.out))
+        self._x = None                                    # (the buffers are no longer the last forward's)
         L.moe_norm_residual(L.make_norm_residual_args(x, z=self.z, w_pre=self.w_pre, eps=self.eps, num_rows=num_tokens, **out))
         torch.mm(self.z.float(), self.w_router.t(), out=self.logits)
         self.layer.route(self.logits, num_tokens)
@@ -291,6 +303,7 @@ class ExpertBlock:
         if self._x is None:
             raise RuntimeError("backward without a forward pass")
         self.layer._batch("dout", dout, self.H, (self.dtype,))
+        self._apart("dout", dout, (self.dy, self.dr, self.dx, self.layer.dx))
         x, y, num_tokens = self._x
         self._x = None
         if num_tokens is not None:
@@ -309,10 +322,10 @@ class ExpertBlock:
         return self.dx
 
     def step(self, lr, balance_rate=0.0, **adam):
-        """One AdamW step of all parameters from their grads, and one of the balance bias."""
-        self.steps += 1
-        L.moe_adamw_step(L.make_adamw_args(self._table, lr=lr, step=self.steps, **adam))
-        self.layer.step(lr, **adam)
+        """One AdamW step of all parameters from their grads (the experts' keywords: ``ExpertLayer.step``;
+        a step that skip leaves out does not count for any), and one of the balance bias."""
+        self.layer.step(lr, **adam)                       # (it settles the steps' number)
+        L.moe_adamw_step(L.make_adamw_args(self._table, lr=lr, step=self.layer.steps, **adam))
         if balance_rate:
             self.layer.balance(balance_rate)
         self._served = None

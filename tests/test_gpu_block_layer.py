@@ -119,6 +119,48 @@ def test_block_refusals():
         plain.route(torch.zeros(16, 4, device="cuda"), num_tokens=torch.ones(1, dtype=torch.int32, device="cuda"))
 
 
+def test_balance_needs_a_route():
+    layer = ExpertLayer(16, 128, 64, 4, 2, scores={"score": L.SCORE_SIGMOID, "balance": True})
+    with pytest.raises(RuntimeError):
+        layer.balance(0.1)                         # (the loads are not there yet)
+    assert (layer.bias == 0).all()
+
+
+def test_block_keeps_passes_apart():
+    """A served batch ends what backward may use, and the block's own buffers are no inputs."""
+    b, x, dout = make(16, 128, 128, 4, 2, 5)
+    b.forward(x)
+    b.serve(x)
+    with pytest.raises(RuntimeError):
+        b.backward(dout)
+    for t in (b.out, b.z):
+        with pytest.raises(ValueError):
+            b.forward(t)
+    b.forward(x)
+    for t in (b.dx, b.dr, b.dy):
+        with pytest.raises(ValueError):
+            b.backward(t)
+    b.backward(dout)
+
+
+def test_skipped_steps_do_not_count():
+    """The block's parameters after a skipped step and a counted one: those of the counted one alone, bit for bit."""
+    results = []
+    for skipped in (False, True):
+        b, x, dout = make(16, 128, 64, 4, 2, 6)
+        b.forward(x)
+        b.backward(dout)
+        if skipped:
+            before = {k: v.clone() for k, v in b.params.items()}
+            b.step(1e-2, skip=torch.ones(1, dtype=torch.int32, device="cuda"))
+            assert all(torch.equal(before[k], v) for k, v in b.params.items())
+        b.step(1e-2)
+        torch.cuda.synchronize()
+        assert b.steps == 1
+        results.append({k: v.clone() for k, v in b.params.items()})
+    assert all(torch.equal(results[0][k], v) for k, v in results[1].items())
+
+
 def test_plain_router_has_a_gradient_too():
     """The softmax over the chosen logits: moe_route_topk's weights, renormalised."""
     layer = ExpertLayer(50, 128, 64, 9, 3, generator=gen(3))
