@@ -15,7 +15,7 @@
 // Without a bias the scores' order is the logits' own, which are compared as they are.
 //
 // Instructions bound it, and of those mostly the ones that a token costs whatever E is: 16-bit
-// logits of 257 experts, top 9, take some 480 (65536 tokens: 30.4 us, 1.26 TB/s); sigmoid scores with
+// logits of 257 experts, top 9, take some 460 (65536 tokens: 29.3 us, 1.31 TB/s); sigmoid scores with
 // a bias, 8 groups and top 10 of 512 experts some 1080 (8192 tokens: 12.0 us).  Two tokens finished
 // side by side by half a warp each (10% fewer instructions, fewer warps) and warps that stay
 // for many tokens (40 us) were slower.  The 64 bits count where a token is among the last ones: of
@@ -370,6 +370,12 @@ __device__ __forceinline__ void write_routes(const RouteParams& p, uint32_t t, i
   }
 }
 
+// The kernels' places a lane are 2, 4, 8, 9, 12, 16, 32 and 64.  Without runs of experts a kernel is
+// taken for more than the next smaller number, so that every lane has an expert in that many places (without
+// groups), and they need no comparison (65536 tokens of 257 experts: 29.3 us, 30.4 with it).
+template <int kPer>
+constexpr int kPlacesBelow = kPer > 32 ? 32 : kPer > 16 ? 16 : kPer > 12 ? 12 : kPer > 9 ? 9 : kPer > 8 ? 8 : kPer > 4 ? 4 : kPer > 2 ? 2 : 0;
+
 // A lane's places, `none` where it has no expert.  kRun experts in one load where rows allow it.
 template <int kPer, bool kGroups, int kRun, typename Load>
 __device__ __forceinline__ void load_runs(float (&to)[kPer], const RouteParams& p, int part, bool group, float none, Load load) {
@@ -377,6 +383,10 @@ __device__ __forceinline__ void load_runs(float (&to)[kPer], const RouteParams& 
   const int left = (!kGroups || group ? p.group_size : 0) - first;      // (a lane without a group has none)
 #pragma unroll
   for (int i = 0; i < kPer; i += kRun) {
+    if (!kGroups && kRun == 1 && i < kPlacesBelow<kPer>) {
+      load(first + i * step, &to[i]);
+      continue;
+    }
 #pragma unroll
     for (int j = 0; j < kRun; ++j) to[i + j] = none;
     if (i / kRun * step < left) load(first + i / kRun * step, &to[i]);
@@ -654,8 +664,8 @@ __global__ void __launch_bounds__(32 * (kMode == 0 ? kWarps : kWarpsScored), kPe
 //
 // Zeros: the writes bound it (8192 tokens of 512 experts, FP32: 6.0 us, 3.0 TB/s into L2 and
 // HBM, launch included).  Dense rows: two loads one after the other (ids, their logits), two
-// sums over the warp and 360 instructions a token (65536 tokens of 257 experts in 16 bits: 32 us,
-// 2.25 TB/s); pairs of 16-bit logits, 42 us one at a time.  Loads of the next token ahead and both sums
+// sums over the warp and 360 instructions a token (65536 tokens of 257 experts in 16 bits: 31.3 us,
+// 2.3 TB/s); pairs of 16-bit logits, 42 us one at a time.  Loads of the next token ahead and both sums
 // in one exchange changed nothing; six CTAs an SM instead of eight 38 us.
 struct RouteGradParams {
   const void* logits;
@@ -667,6 +677,11 @@ struct RouteGradParams {
   int E, top_k, score, renormalize, id_bits, vec;
   float scale;
 };
+
+// The next smaller of the dense kernels' words a lane, which a kernel is taken for more than: words below it
+// lie inside the row (but the first pair, which may begin one before it), and need no comparison (32.1 -> 31.3 us).
+template <int kPer>
+constexpr int kWordsBelow = kPer > 33 ? 33 : kPer > 16 ? 16 : kPer > 9 ? 9 : kPer > 5 ? 5 : kPer > 4 ? 4 : kPer > 2 ? 2 : 0;
 
 template <typename T> struct Logit;
 template <> struct Logit<float> {
@@ -700,6 +715,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPer <= 9 ? 8 : 1)
     const T* in = static_cast<const T*>(p.logits) + static_cast<int64_t>(t) * static_cast<int32_t>(p.ld);
     const int back = kEach == 2 ? static_cast<int>(reinterpret_cast<uintptr_t>(in) >> 1) & 1 : 0;
     float s[kWords][kEach];
+    constexpr int kSure = kWordsBelow<kPer>;
     if constexpr (kPer != 0) {
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
@@ -708,8 +724,8 @@ __global__ void __launch_bounds__(32 * kWarps, kPer <= 9 ? 8 : 1)
         for (int j = 0; j < kEach; ++j) s[i][j] = -CUDART_INF_F;
         if (t < live) {
           if constexpr (kEach == 1) {
-            if (at < p.E) s[i][0] = __ldg(in + at);
-          } else if (at >= 0 && at + 1 < p.E && p.vec) {
+            if (i < kSure || at < p.E) s[i][0] = __ldg(in + at);
+          } else if (((i > 0 && i < kSure) || (at >= 0 && at + 1 < p.E)) && p.vec) {
             const float2 v = Pack2<T>::load(__ldg(reinterpret_cast<const unsigned int*>(in + at)));
             s[i][0] = v.x, s[i][1] = v.y;
           } else {
@@ -795,8 +811,8 @@ __global__ void __launch_bounds__(32 * kWarps, kPer <= 9 ? 8 : 1)
       for (int i = 0; i < kWords; ++i) {
         const int at = kEach * (lane + 32 * i) - back;
         if constexpr (kEach == 1) {
-          if (at < p.E) row[at] = Logit<T>::round(s[i][0] * factor);
-        } else if (at >= 0 && at + 1 < p.E && p.vec) {
+          if (i < kSure || at < p.E) row[at] = Logit<T>::round(s[i][0] * factor);
+        } else if (((i > 0 && i < kSure) || (at >= 0 && at + 1 < p.E)) && p.vec) {
           *reinterpret_cast<unsigned int*>(row + at) = Pack2<T>::store(s[i][0] * factor, s[i][1] * factor);
         } else {
 #pragma unroll
@@ -838,7 +854,7 @@ unsigned warp_grid(int64_t tokens, int sms) {
   return static_cast<unsigned>(want < 1 ? 1 : want > most ? most : want);
 }
 
-// (places in runs: 4, 8, 12, 16, 32 and 64 hold whole runs of four, all but 4 and 12 of eight)
+// (kPlacesBelow has the same numbers; in runs: 4, 8, 12, 16, 32 and 64 hold whole runs of four, all but 4 and 12 of eight)
 template <int kMode, bool kGroups>
 auto route_kernel_of(int per, int run) {
   return per <= 2 && run == 0   ? route_scores_kernel<2, kMode, kGroups>
@@ -855,6 +871,7 @@ template <typename T>
 auto route_grad_kernel_of(bool dense, int words) {
   return !dense        ? route_scores_backward_kernel<T, 0>
          : words <= 2  ? route_scores_backward_kernel<T, 2>
+         : words <= 4  ? route_scores_backward_kernel<T, 4>
          : words <= 5  ? route_scores_backward_kernel<T, 5>
          : words <= 9  ? route_scores_backward_kernel<T, 9>
          : words <= 16 ? route_scores_backward_kernel<T, 16>

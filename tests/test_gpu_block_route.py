@@ -254,6 +254,17 @@ def test_gradient_of_repeated_unlisted_and_left_out_experts():
             check_gradient(l, ids, score, renorm, id_dtype=torch.int64)
 
 
+@pytest.mark.parametrize("score", [B.SIGMOID, B.SOFTMAX])
+def test_one_renormalised_weight_has_no_gradient(score):
+    """top_k 1: the weight is the factor itself, whatever the logits; not a rounding is left of its gradient."""
+    rng = np.random.default_rng(23)
+    l, ids = rng.standard_normal((500, 40)) * 3, rng.integers(0, 40, (500, 1))
+    dw = torch.from_numpy(rng.standard_normal((500, 1)).astype(np.float32)).cuda()
+    for dtype in (torch.float32, torch.bfloat16):
+        got = gradient(l, torch.from_numpy(ids).to(torch.int32).cuda(), dw, score, True, dtype, 2.5)
+        assert (got == 0).all()
+
+
 def test_gradient_against_differences():
     rng = np.random.default_rng(9)
     M, E, k = 6, 20, 4
