@@ -15,7 +15,7 @@
 // Without a bias the scores' order is the logits' own, which are compared as they are.
 //
 // Instructions bound it, and of those mostly the ones that a token costs whatever E is: 16-bit
-// logits of 257 experts, top 9, take some 460 (65536 tokens: 29.3 us, 1.31 TB/s); sigmoid scores with
+// logits of 257 experts, top 9, take some 470 (65536 tokens: 29.3 us, 1.31 TB/s); sigmoid scores with
 // a bias, 8 groups and top 10 of 512 experts some 1080 (8192 tokens: 12.0 us).  Two tokens finished
 // side by side by half a warp each (10% fewer instructions, fewer warps) and warps that stay
 // for many tokens (40 us) were slower.  The 64 bits count where a token is among the last ones: of
@@ -34,7 +34,7 @@ namespace {
 
 // Warps of a CTA.  Where scores are compared a warp has one token, and small CTAs fill the places that
 // finished ones leave (8192 tokens of 512 experts in groups: 12.0 us, 12.3 with eight warps); where logits
-// are, a warp takes several of many tokens (65536 tokens of 257 experts: 30.4 us, 31.2 with four).
+// are, a warp takes several of many tokens (65536 tokens of 257 experts: 3% less than with four).
 constexpr int kWarps = 8, kWarpsScored = 4;
 constexpr uint32_t kAll = 0xffffffffu;
 
@@ -664,7 +664,7 @@ __global__ void __launch_bounds__(32 * (kMode == 0 ? kWarps : kWarpsScored), kPe
 //
 // Zeros: the writes bound it (8192 tokens of 512 experts, FP32: 6.0 us, 3.0 TB/s into L2 and
 // HBM, launch included).  Dense rows: two loads one after the other (ids, their logits), two
-// sums over the warp and 360 instructions a token (65536 tokens of 257 experts in 16 bits: 31.3 us,
+// sums over the warp and 340 instructions a token (65536 tokens of 257 experts in 16 bits: 31.3 us,
 // 2.3 TB/s); pairs of 16-bit logits, 42 us one at a time.  Loads of the next token ahead and both sums
 // in one exchange changed nothing; six CTAs an SM instead of eight 38 us.
 struct RouteGradParams {
