@@ -26,6 +26,7 @@
 #include <type_traits>
 
 #include "../../include/moe_block.h"
+#include "route_layout.h"
 #include "router.cuh"
 #include "train.cuh"
 
@@ -38,17 +39,14 @@ namespace {
 constexpr int kWarps = 8, kWarpsScored = 4;
 constexpr uint32_t kAll = 0xffffffffu;
 
-struct RouteParams {
+struct RouteParams : RouteLayout {
   const void* logits;
   const float* bias;
   void* ids;
   float* weights;
   const int32_t* num_tokens;
   int64_t M, ld;
-  int E, top_k, groups, topk_groups, group_size;
-  int lanes;        // lanes per group, a power of two: lane = group * lanes + part
-  int per;          // experts per lane, in runs of 1 << run
-  int run;
+  int top_k, topk_groups;
   int pair, score, renormalize, dtype, id_bits;
   float scale;
 };
@@ -96,11 +94,17 @@ __device__ __forceinline__ double sigmoid64(float l) {
   return (l >= 0.f ? 1.0 : e) / (1.0 + e);
 }
 
-// The expert of this lane's i-th place, or -1: a group's lanes take runs of 1 << run experts in turn.
-__device__ __forceinline__ int expert_at(const RouteParams& p, int i, int lane) {
-  const int off = ((((i >> p.run) * p.lanes + lane % p.lanes) << p.run) | (i & ((1 << p.run) - 1))), g = lane / p.lanes;
-  return g < p.groups && off < p.group_size ? g * p.group_size + off : -1;
+// Places of a lane as a mask, its lowest one, and how many the careful paths hold beside a kernel of kPer.
+template <int kPer>
+using PlaceMask = std::conditional_t<(kPer > 64), unsigned __int128, std::conditional_t<(kPer > 32), uint64_t, uint32_t>>;
+__device__ __forceinline__ int first_place(uint32_t m) { return __ffs(static_cast<int>(m)) - 1; }
+__device__ __forceinline__ int first_place(uint64_t m) { return __ffsll(static_cast<long long>(m)) - 1; }
+__device__ __forceinline__ int first_place(unsigned __int128 m) {
+  const uint64_t low = static_cast<uint64_t>(m);
+  return low ? first_place(low) : 64 + first_place(static_cast<uint64_t>(m >> 64));
 }
+template <int kPer>
+constexpr int kMostPlaces = kPer > 64 ? 128 : 64;
 
 // What a token's selection leaves with lane j < n: its j-th expert and logit.
 struct Chosen {
@@ -175,13 +179,13 @@ __device__ __forceinline__ bool group_stays(const RouteParams& p, const TopTwo& 
 }
 
 // The groups in question in 64 bits, from the places `some` of this lane (the others cannot count).
-template <int kMode>
-__device__ __noinline__ bool groups_exactly(const RouteParams& p, int64_t t, uint64_t some, float m, bool in_question, int slots) {
+template <int kMode, typename Mask>
+__device__ __noinline__ bool groups_exactly(const RouteParams& p, int64_t t, Mask some, float m, bool in_question, int slots) {
   const int lane = threadIdx.x % 32;
   const double total = kMode == 2 ? softmax_total(p, t, m) : 1.0;
   TopTwo top;
   while (some) {
-    const int e = expert_at(p, __ffsll(static_cast<long long>(some)) - 1, lane);
+    const int e = route_expert_at(p, first_place(some), lane);
     some &= some - 1;
     const float l = logit_at(p.logits, p.dtype, t * p.ld + e);
     const double s = kMode == 1 ? sigmoid64(l) : exp(static_cast<double>(l) - m) / total;
@@ -202,6 +206,7 @@ __device__ __forceinline__ int place(int16_t* at, int rank, int lane) {
 
 // Everything in 64 bits, for any values: a NaN, or many experts too near to tell apart.
 // Every expert's key once, then groups, then top_k rounds of a warp-wide maximum.
+template <int kMost>
 __device__ __noinline__ Chosen choose_exactly(const RouteParams& p, int64_t t, int by_score) {
   const int lane = threadIdx.x % 32;
   const bool softmax = p.score == MOE_SCORE_SOFTMAX;
@@ -212,11 +217,11 @@ __device__ __noinline__ Chosen choose_exactly(const RouteParams& p, int64_t t, i
     m = static_cast<double>(warp_max(top));
     total = softmax_total(p, t, m);
   }
-  uint64_t keys[64];                            // 0: left out (p.per <= 64)
+  uint64_t keys[kMost];                         // 0: left out
   TopTwo top;
 #pragma unroll 4
-  for (int i = 0; i < p.per; ++i) {
-    const int e = expert_at(p, i, lane);
+  for (int i = 0; i < p.per && MOE_IN_BOUNDS(i < kMost); ++i) {
+    const int e = route_expert_at(p, i, lane);
     const float l = e >= 0 ? logit_at(p.logits, p.dtype, t * p.ld + e) : -CUDART_INF_F, b = e >= 0 && p.bias ? __ldg(p.bias + e) : 0.f;
     double v = static_cast<double>(l);
     if (by_score) v = (softmax ? exp(v - m) / total : sigmoid64(l)) + static_cast<double>(b);
@@ -236,7 +241,7 @@ __device__ __noinline__ Chosen choose_exactly(const RouteParams& p, int64_t t, i
     uint64_t key = 0;
     int at = 0x7fffffff, place = -1;
     for (int i = 0; i < p.per && kept; ++i)
-      if (keys[i] > key) key = keys[i], at = expert_at(p, i, lane), place = i;
+      if (keys[i] > key) key = keys[i], at = route_expert_at(p, i, lane), place = i;
     const uint64_t own = key;
     const int mine = at;
 #pragma unroll
@@ -284,31 +289,32 @@ __device__ __forceinline__ float coarse_value(float l, float b, float m, float i
 // The choice where more experts reach the threshold than a warp has lanes (many
 // equal logits, as of a router's first step): top_k rounds of a warp-wide maximum.
 // n = -1: two of them are too near to tell.
-template <int kMode>
+template <int kMode, int kMost>
 __device__ __noinline__ Chosen choose_of_many(const RouteParams& p, int64_t t, bool kept, float m, float inv, float err) {
   const int lane = threadIdx.x % 32;
   const bool by_value = kMode != 0 && p.bias;          // without a bias experts go by their logits
   Chosen c = {0, -1, 0.f};
-  float values[64];                                    // (p.per <= 64)
-  uint64_t taken = 0;                                  // places that are left out or chosen
+  using Mask = PlaceMask<kMost>;
+  float values[kMost];
+  Mask taken = 0;                                      // places that are left out or chosen
 #pragma unroll 4
-  for (int i = 0; i < p.per; ++i) {
-    const int e = kept ? expert_at(p, i, lane) : -1;
+  for (int i = 0; i < p.per && MOE_IN_BOUNDS(i < kMost); ++i) {
+    const int e = kept ? route_expert_at(p, i, lane) : -1;
     const float l = e >= 0 ? logit_at(p.logits, p.dtype, t * p.ld + e) : -CUDART_INF_F, b = e >= 0 && by_value ? __ldg(p.bias + e) : 0.f;
     values[i] = by_value ? coarse_value<kMode>(l, b, m, inv) : l;
-    if (l == -CUDART_INF_F || b == -CUDART_INF_F) taken |= uint64_t(1) << i;
+    if (l == -CUDART_INF_F || b == -CUDART_INF_F) taken |= Mask(1) << i;
   }
   float cv = 0.f, cb = 0.f;
   for (int j = 0; j < p.top_k; ++j) {
     float best = -CUDART_INF_F;
     int at = 0x7fffffff, place = 0;
     for (int i = 0; i < p.per; ++i)
-      if (!((taken >> i) & 1) && (values[i] > best || at == 0x7fffffff)) best = values[i], place = i, at = expert_at(p, i, lane);
+      if (!((taken >> i) & 1) && (values[i] > best || at == 0x7fffffff)) best = values[i], place = i, at = route_expert_at(p, i, lane);
     const bool some = at != 0x7fffffff;
     const float top = warp_max(some ? best : -CUDART_INF_F);
     const int won = __reduce_min_sync(kAll, some && best == top ? at : 0x7fffffff);
     if (won == 0x7fffffff) break;                      // none left
-    if (some && at == won) taken |= uint64_t(1) << place;
+    if (some && at == won) taken |= Mask(1) << place;
     if (lane == j) c.e = won, cv = top;
     c.n = j + 1;
   }
@@ -324,7 +330,7 @@ __device__ __noinline__ Chosen choose_of_many(const RouteParams& p, int64_t t, b
   const float kv = __shfl_sync(kAll, cv, c.n - 1), kl = __shfl_sync(kAll, c.l, c.n - 1), kb = __shfl_sync(kAll, cb, c.n - 1);
   for (int i = 0; i < p.per; ++i)
     if (!((taken >> i) & 1) && !(kv - values[i] > near)) {
-      const int e = expert_at(p, i, lane);
+      const int e = route_expert_at(p, i, lane);
       close |= !(logit_at(p.logits, p.dtype, t * p.ld + e) == kl && __ldg(p.bias + e) == kb);
     }
   if (__any_sync(kAll, close)) c.n = -1;
@@ -370,7 +376,7 @@ __device__ __forceinline__ void write_routes(const RouteParams& p, uint32_t t, i
   }
 }
 
-// The kernels' places a lane are 2, 4, 8, 9, 12, 16, 32 and 64.  Without runs of experts a kernel is
+// The kernels' places a lane are 2, 4, 8, 9, 12, 16, 32, 64 and (groups only) 128.  Without runs of experts a kernel is
 // taken for more than the next smaller number, so that every lane has an expert in that many places (without
 // groups), and they need no comparison (65536 tokens of 257 experts: 29.3 us, 30.4 with it).
 template <int kPer>
@@ -456,7 +462,7 @@ template <int kPer, int kMode, bool kGroups>
 __global__ void __launch_bounds__(32 * (kMode == 0 ? kWarps : kWarpsScored), kPer > 16 ? 1 : kMode == 0 ? 6 : 8)
     route_scores_kernel(const __grid_constant__ RouteParams p) {
   constexpr int kTokens = kMode == 0 ? kWarps : kWarpsScored;
-  using Mask = std::conditional_t<(kPer > 32), uint64_t, uint32_t>;
+  using Mask = PlaceMask<kPer>;
   __shared__ __align__(16) uint64_t s_key[kTokens][32];
   __shared__ int16_t s_cand[kTokens][32];
   pdl_wait();
@@ -528,7 +534,7 @@ __global__ void __launch_bounds__(32 * (kMode == 0 ? kWarps : kWarpsScored), kPe
           const float s = kMode == 1 ? reciprocal_coarse(1.f + exp_coarse(-v[i])) : exp_coarse(v[i] - m) * inv;
           float x = s + (kHold ? held[i] : 0.f);
           if (!kHold && biased) {
-            const int e = i < p.per ? expert_at(p, i, lane) : -1;
+            const int e = i < p.per ? route_expert_at(p, i, lane) : -1;
             x = s + (e >= 0 ? __ldg(p.bias + e) : 0.f);
           }
           v[i] = v[i] == -CUDART_INF_F ? v[i] : x;
@@ -570,11 +576,11 @@ __global__ void __launch_bounds__(32 * (kMode == 0 ? kWarps : kWarpsScored), kPe
               const bool in_question = group && !(stays ? x - best > near : worst - x > near);
               const int sure = __popc(__ballot_sync(kAll, stays && !in_question)) / lanes;
               const float floor = (pair ? a2 : a1) - 2.f * err;
-              uint64_t some = 0;
+              Mask some = 0;
 #pragma unroll
               for (int i = 0; i < kPer; ++i)
-                if (v[i] != -CUDART_INF_F && !(v[i] < floor)) some |= uint64_t(1) << i;
-              const bool among = groups_exactly<kMode>(p, t, in_question ? some : 0, m, in_question, p.topk_groups - sure);
+                if (v[i] != -CUDART_INF_F && !(v[i] < floor)) some |= Mask(1) << i;
+              const bool among = groups_exactly<kMode, Mask>(p, t, in_question ? some : Mask(0), m, in_question, p.topk_groups - sure);
               if (in_question) stays = among;
             }
           }
@@ -602,7 +608,7 @@ __global__ void __launch_bounds__(32 * (kMode == 0 ? kWarps : kWarpsScored), kPe
         for (uint32_t some = __ballot_sync(kAll, cand != 0); some; some = __ballot_sync(kAll, cand != 0)) {
           if (cand) {
             const int pos = n + __popc(some & below);
-            const int i = (kPer > 32 ? __ffsll(static_cast<long long>(cand)) : __ffs(static_cast<int>(cand))) - 1;
+            const int i = first_place(cand);
             cand &= cand - 1;
             if (pos < 32) s_cand[warp][pos] = static_cast<int16_t>(first + ((i >> p.run) * run_step + (i & run_mask)));
           }
@@ -650,8 +656,8 @@ __global__ void __launch_bounds__(32 * (kMode == 0 ? kWarps : kWarpsScored), kPe
           }
         }
       }
-      if (way == 1) c = choose_of_many<kMode>(p, t, stays, m, inv, err);
-      if (way == 2 || c.n < 0) c = choose_exactly(p, t, kMode != 0);
+      if (way == 1) c = choose_of_many<kMode, kMostPlaces<kPer>>(p, t, stays, m, inv, err);
+      if (way == 2 || c.n < 0) c = choose_exactly<kMostPlaces<kPer>>(p, t, kMode != 0);
     }
     write_routes(p, t, lane, c, softmax, m, total);
     if (kMode != 0) break;
@@ -854,17 +860,20 @@ unsigned warp_grid(int64_t tokens, int sms) {
   return static_cast<unsigned>(want < 1 ? 1 : want > most ? most : want);
 }
 
-// (kPlacesBelow has the same numbers; in runs: 4, 8, 12, 16, 32 and 64 hold whole runs of four, all but 4 and 12 of eight)
+// (kPlacesBelow has the same numbers)
 template <int kMode, bool kGroups>
-auto route_kernel_of(int per, int run) {
-  return per <= 2 && run == 0   ? route_scores_kernel<2, kMode, kGroups>
-         : per <= 4 && run < 3  ? route_scores_kernel<4, kMode, kGroups>
-         : per <= 8             ? route_scores_kernel<8, kMode, kGroups>
-         : per <= 9 && run == 0 ? route_scores_kernel<9, kMode, kGroups>
-         : per <= 12 && run < 3 ? route_scores_kernel<12, kMode, kGroups>
-         : per <= 16            ? route_scores_kernel<16, kMode, kGroups>
-         : per <= 32            ? route_scores_kernel<32, kMode, kGroups>
-                                : route_scores_kernel<64, kMode, kGroups>;
+auto route_kernel_of(int places) {
+  if constexpr (kGroups) {
+    if (places > 64) return route_scores_kernel<128, kMode, kGroups>;
+  }
+  return places == 2    ? route_scores_kernel<2, kMode, kGroups>
+         : places == 4  ? route_scores_kernel<4, kMode, kGroups>
+         : places == 8  ? route_scores_kernel<8, kMode, kGroups>
+         : places == 9  ? route_scores_kernel<9, kMode, kGroups>
+         : places == 12 ? route_scores_kernel<12, kMode, kGroups>
+         : places == 16 ? route_scores_kernel<16, kMode, kGroups>
+         : places == 32 ? route_scores_kernel<32, kMode, kGroups>
+                        : route_scores_kernel<64, kMode, kGroups>;
 }
 
 template <typename T>
@@ -920,7 +929,13 @@ moe_status moe_route_scores(const moe_route_scores_args* a, moe_stream_t stream)
   const void* ptrs[] = {a->logits, a->bias, a->topk_ids, a->topk_weights, a->num_tokens};
   for (const void* p : ptrs)
     if (p && !on_device(p, dev.device)) return MOE_ERR_DEVICE;
+  // (all groups staying is no grouping)
+  const int groups = a->topk_groups == a->groups ? 1 : a->groups;
   RouteParams p;
+  static_cast<RouteLayout&>(p) =
+      route_layout(a->E, groups, eb, aligned16(a->logits) && aligned16(a->bias) && a->ldlogits * eb % 16 == 0);
+  const int places = route_places(p);
+  if (p.per > places || (groups == 1 && places > 64)) return MOE_ERR_SHAPE;      // (no size: the layout's test goes through all)
   p.logits = a->logits;
   p.bias = a->bias;
   p.ids = a->topk_ids;
@@ -928,24 +943,8 @@ moe_status moe_route_scores(const moe_route_scores_args* a, moe_stream_t stream)
   p.num_tokens = a->num_tokens;
   p.M = a->M;
   p.ld = a->ldlogits;
-  p.E = a->E;
   p.top_k = a->top_k;
-  // (all groups staying is no grouping)
-  p.groups = a->topk_groups == a->groups ? 1 : a->groups;
-  p.topk_groups = p.groups == 1 ? 1 : a->topk_groups;
-  p.group_size = a->E / p.groups;
-  p.lanes = 32;
-  while (p.lanes * p.groups > 32) p.lanes /= 2;
-  // runs of 16 bytes where every group of every row and of the bias starts on them and they waste no more than a
-  // quarter of the places
-  const int bytes = type_bytes(a->dtype), run = 16 / bytes;
-  p.run = 0;
-  p.per = static_cast<int>(ceil_div(p.group_size, p.lanes));
-  const int padded = static_cast<int>(ceil_div(p.group_size, p.lanes * run)) * run;
-  if (aligned16(a->logits) && aligned16(a->bias) && a->ldlogits * bytes % 16 == 0 && p.group_size % run == 0 && 4 * padded <= 5 * p.per) {
-    p.run = bytes == 4 ? 2 : 3;
-    p.per = padded;
-  }
+  p.topk_groups = groups == 1 ? 1 : a->topk_groups;
   p.pair = a->group_score == MOE_GROUP_TOP2;
   p.score = a->score;
   p.renormalize = a->renormalize;
@@ -955,12 +954,12 @@ moe_status moe_route_scores(const moe_route_scores_args* a, moe_stream_t stream)
   // without a bias the scores' order is the logits'; sums of two scores have none such
   const bool scored = a->bias || (p.groups > 1 && p.pair);
   const int mode = !scored ? 0 : a->score == MOE_SCORE_SIGMOID ? 1 : 2;
-  auto kernel = p.groups > 1 ? (mode == 0   ? route_kernel_of<0, true>(p.per, p.run)
-                                : mode == 1 ? route_kernel_of<1, true>(p.per, p.run)
-                                            : route_kernel_of<2, true>(p.per, p.run))
-                             : (mode == 0   ? route_kernel_of<0, false>(p.per, p.run)
-                                : mode == 1 ? route_kernel_of<1, false>(p.per, p.run)
-                                            : route_kernel_of<2, false>(p.per, p.run));
+  auto kernel = p.groups > 1 ? (mode == 0   ? route_kernel_of<0, true>(places)
+                                : mode == 1 ? route_kernel_of<1, true>(places)
+                                            : route_kernel_of<2, true>(places))
+                             : (mode == 0   ? route_kernel_of<0, false>(places)
+                                : mode == 1 ? route_kernel_of<1, false>(places)
+                                            : route_kernel_of<2, false>(places));
   const int warps = mode == 0 ? kWarps : kWarpsScored;
   const unsigned grid = mode == 0 ? warp_grid(a->M, dev.sms) : static_cast<unsigned>(ceil_div(a->M, warps));
   MOE_CUDA_TRY(launch_pdl(kernel, dim3(grid), dim3(32 * warps), 0, stream, 1, p));
