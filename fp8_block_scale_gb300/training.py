@@ -214,19 +214,24 @@ class ExpertLayer:
             copied.record()
             self._skipped = flag, copied
 
-    def quantized(self):
+    def quantized(self, out=None):
         """The trained weights as the FP8 forward takes them: (w13 interleaved,
-        w13_scale, w2, w2_scale).  H, I multiples of 128; BF16 weights, ValueError for others."""
-        out = []
-        for w in self.models:
-            E, rows, cols = w.shape
-            q = torch.empty(E, rows, cols, dtype=torch.uint8, device=w.device)
-            s = torch.empty(E, rows // 128, cols // 128, dtype=torch.float32, device=w.device)
-            L.moe_quantize_weight_128x128(w, q, s)
-            out.append((q, s))
-        w13 = torch.empty_like(out[0][0])
-        L.moe_prep_weights(out[0][0], w13)
-        return w13, out[0][1], out[1][0], out[1][1]
+        w13_scale, w2, w2_scale).  H, I multiples of 128; BF16 weights, ValueError for others.
+        out: what an earlier call returned, written again instead of new tensors."""
+        if out is None:
+            out = tuple(t for w in self.models for t in (
+                torch.empty(w.shape, dtype=torch.uint8, device=w.device),
+                torch.empty(w.shape[0], w.shape[1] // 128, w.shape[2] // 128, dtype=torch.float32, device=w.device)))
+        w13, w13_scale, w2, w2_scale = out
+        rows = torch.empty_like(w13)                      # (before they are interleaved)
+        L.moe_quantize_weight_128x128(self.models[0], rows, w13_scale)
+        L.moe_quantize_weight_128x128(self.models[1], w2, w2_scale)
+        L.moe_prep_weights(rows, w13)
+        return out
+
+    def weights_version(self):
+        """Another value after each step of the layer and each write of torch's to the weights."""
+        return self._calls, tuple(0 if w.is_inference() else w._version for w in self.models)
 
 
 class ExpertBlock:
@@ -262,7 +267,8 @@ class ExpertBlock:
         states = [{k: torch.zeros(p.numel(), device=dev) for k in ("exp_avg", "exp_avg_sq")} for p in self.params.values()]
         self._table = L.AdamWTable([{"param": p.view(-1), "grad": g.view(-1), **s}
                                     for p, g, s in zip(self.params.values(), self.grads.values(), states)])
-        self._served = None
+        self._serving = None                              # what serve keeps, and the weights whose codes it holds
+        self._served_version = None
         self._x = None                                    # the last forward's stream
 
     @property
@@ -328,25 +334,51 @@ class ExpertBlock:
         L.moe_adamw_step(L.make_adamw_args(self._table, lr=lr, step=self.layer.steps, **adam))
         if balance_rate:
             self.layer.balance(balance_rate)
-        self._served = None
+
+    def _serving_buffers(self):
+        layer, dev, I = self.layer, self.z.device, self.layer.I
+        ws = torch.empty(L.moe_forward_workspace_size(self.M, self.H, I, self.E, layer.top_k, layer.block_m, layer.sorted_ids.numel()),
+                         dtype=torch.uint8, device=dev)
+        L.moe_workspace_init(ws)
+        q, q_scale = torch.zeros(self.M, self.H, dtype=torch.uint8, device=dev), torch.zeros(self.M, self.H // 128, device=dev)
+        y = torch.empty(self.M, self.H, dtype=torch.bfloat16, device=dev)
+        codes = layer.quantized()
+        return q, q_scale, y, codes, ws, L.make_fwd_args(
+            q, q_scale, *codes, layer.topk_weights, layer.sorted_ids, layer.expert_ids, layer.num_padded, y, ws,
+            layer.top_k, layer.block_m, device_status=layer.status)
+
+    def refresh(self):
+        """Forms the FP8 weights that ``serve`` reads anew, where they lie.  Needed after writes to the
+        experts' weights that neither ``step`` (the block's or the layer's) nor torch has made."""
+        self._quantise()
+
+    def _quantise(self):
+        """What serve keeps, with the codes of the present weights."""
+        version = self.layer.weights_version()
+        capturing = torch.cuda.is_current_stream_capturing()     # (nothing has run yet then)
+        if self._serving is None:
+            serving = self._serving_buffers()
+            if capturing:
+                return serving                            # the graph's own
+            self._serving = serving
+        else:
+            self.layer.quantized(out=self._serving[3])
+        self._served_version = None if capturing else version
+        return self._serving
 
     def serve(self, x, num_tokens=None):
         """forward in FP8: the entry's norm writes the experts' input as E4M3 codes with 1x128 scales
         beside the router's, the experts run in moe_fp8_block_scale_forward.  H, I multiples of
-        128, BF16.  The weights are quantised at the first call after a step."""
+        128, BF16.
+
+        The weights are quantised when they have changed since the last call: by a step of the block or of
+        its layer, or by torch's writes to ``layer.models`` (other writes: ``refresh``).  A captured call
+        reads the codes where they lie, so that its replays follow the next call outside the graph; if the
+        weights have changed before it, or nothing was served yet, the graph forms the codes itself, at each replay."""
         layer = self.layer
-        if self._served is None:
-            dev, I = x.device, layer.I
-            ws = torch.empty(L.moe_forward_workspace_size(self.M, self.H, I, self.E, layer.top_k, layer.block_m, layer.sorted_ids.numel()),
-                             dtype=torch.uint8, device=dev)
-            L.moe_workspace_init(ws)
-            q, q_scale = torch.zeros(self.M, self.H, dtype=torch.uint8, device=dev), torch.zeros(self.M, self.H // 128, device=dev)
-            y = torch.empty(self.M, self.H, dtype=torch.bfloat16, device=dev)
-            w13, w13_scale, w2, w2_scale = layer.quantized()
-            self._served = q, q_scale, y, (w13, w13_scale, w2, w2_scale, ws), L.make_fwd_args(
-                q, q_scale, w13, w13_scale, w2, w2_scale, layer.topk_weights, layer.sorted_ids, layer.expert_ids, layer.num_padded, y, ws,
-                layer.top_k, layer.block_m, device_status=layer.status)
-        q, q_scale, y, _, args = self._served
+        fresh = self._serving is not None and self._served_version == layer.weights_version()
+        serving = self._serving if fresh else self._quantise()
+        q, q_scale, y, _, _, args = serving
         if num_tokens is not None:
             self.z.zero_()
         self._enter(x, num_tokens, q=q, q_scale=q_scale)
