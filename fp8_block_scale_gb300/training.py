@@ -280,10 +280,15 @@ class ExpertBlock:
         if t.numel() and any(t.untyped_storage().data_ptr() == o.untyped_storage().data_ptr() for o in own):
             raise ValueError(f"{name}: a buffer of the block itself")
 
-    def _enter(self, x, num_tokens, **out):
+    def _take(self, x, *own):
+        """ValueError unless x is a batch and lies apart from what the pass writes."""
         self.layer._batch("x", x, self.H, (self.dtype,))
-        self._apart("x", x, (self.z, self.out, self.layer.out))
+        self._apart("x", x, (self.z, self.out, *own))
+
+    def _enter(self, x, num_tokens, **out):
         self._x = None                                    # (the buffers are no longer the last forward's)
+        if num_tokens is not None:
+            self.z.zero_()                                # (what padding rows hold goes through the router's product)
         L.moe_norm_residual(L.make_norm_residual_args(x, z=self.z, w_pre=self.w_pre, eps=self.eps, num_rows=num_tokens, **out))
         torch.mm(self.z.float(), self.w_router.t(), out=self.logits)
         self.layer.route(self.logits, num_tokens)
@@ -295,17 +300,19 @@ class ExpertBlock:
 
     def forward(self, x, num_tokens=None):
         """x [tokens, H] -> out [tokens, H] (the block's own buffer).  num_tokens [1] int32 on the
-        device: rows from there on are padding; their out is not written."""
-        if num_tokens is not None:
-            self.z.zero_()                                # (what padding rows hold goes through the router's product)
+        device: rows from there on are padding; their out is not written.
+
+        x is read again by ``backward``: it may be no buffer of the block or its layer."""
+        layer = self.layer
+        self._take(x, self.dy, self.dr, self.dx, layer.out, layer.dx, layer.xs, layer.pre, layer.h, layer.ys, layer.dys, layer.dh)
         self._enter(x, num_tokens)
         y = self.layer.forward(self.z)
         self._x = x, y, num_tokens
         return self._leave(x, y, num_tokens)
 
     def backward(self, dout):
-        """dout [tokens, H] -> dx [tokens, H]; fills grads and the experts' grads.  x must still hold
-        what the last forward pass was given."""
+        """dout [tokens, H] -> dx [tokens, H]; fills grads and the experts' grads.  x and num_tokens must
+        still hold what the last forward pass was given."""
         if self._x is None:
             raise RuntimeError("backward without a forward pass")
         self.layer._batch("dout", dout, self.H, (self.dtype,))
@@ -375,12 +382,11 @@ class ExpertBlock:
         its layer, or by torch's writes to ``layer.models`` (other writes: ``refresh``).  A captured call
         reads the codes where they lie, so that its replays follow the next call outside the graph; if the
         weights have changed before it, or nothing was served yet, the graph forms the codes itself, at each replay."""
+        self._take(x)
         layer = self.layer
         fresh = self._serving is not None and self._served_version == layer.weights_version()
         serving = self._serving if fresh else self._quantise()
         q, q_scale, y, _, _, args = serving
-        if num_tokens is not None:
-            self.z.zero_()
         self._enter(x, num_tokens, q=q, q_scale=q_scale)
         y.zero_()
         L.moe_fp8_block_scale_forward(args)
