@@ -6,8 +6,8 @@
 // gather in registers, each thread's columns over all of its rows; every CTA leaves its sums
 // in the workspace, and a second launch adds them in a fixed order.
 //
-// HBM bounds it: 8192 x 4096 with an FP32 stream and a channel gate 94 us (6.4 TB/s), 16384 x
-// 7168 with a full gate 294 us (6.4 TB/s).  Few rows: two launches and the parts (64 x 4096: 6.0 us).
+// HBM bounds it: 8192 x 4096 with an FP32 stream and a channel gate 95 us (6.4 TB/s), 16384 x
+// 7168 with a full gate 293 us (6.4 TB/s).  Few rows: two launches and the parts (64 x 4096: 6.0 us).
 #include <atomic>
 #include <type_traits>
 
@@ -36,7 +36,11 @@ struct NormGradParams {
 
 // The row sums that everything else follows from, with k = gate y (w_post + offset) and
 // t = dz (w_pre + offset): one round of them, because the sum that the branch's norm needs is
-// linear in dH:  sum k dH = sum k dh + R_h sum k t - R_h^3 mean(t h) sum k h.
+// linear in dH:  sum k dH = sum k dh + R_h (sum k t - (R_h mean(t h)) (R_h sum k h)).
+// A root's cube leaves FP32's range long before the root does (rows beyond 1e13, or of zeros with
+// an eps below 1e-26), so each of its factors meets a sum or an element first.  Nothing hides the
+// chain of scalars between a row's sums and its outputs, so it is kept short: with one more
+// multiplication after another 16384 x 7168 with a full gate takes 297 to 301 us instead of 293.
 enum { kHH, kTH, kYY, kKD, kKT, kKH, kRowSums = 8 };
 
 // Sums of eight values over a warp: lane l ends with the total of value (l / 4) % 8.
@@ -289,12 +293,13 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_kernel(const __grid
     join_sums8(&s_parts[turn][mine * warps][0], warps, lane, s);
     turn ^= 1;                              // (the next row's parts: a thread behind still reads these)
     const float root_h = pre ? rsqrtf(fmaf(s[kHH], inv_h, p.eps)) : 0.f, root_y = post ? rsqrtf(fmaf(s[kYY], inv_h, p.eps)) : 1.f;
-    const float back_h = pre ? root_h * root_h * root_h * (s[kTH] * inv_h) : 0.f;
     const float token = token_gate ? __ldg(static_cast<const float*>(p.gate.p) + row) : 1.f;
-    const float dot = fmaf(root_h, s[kKT], s[kKD]) - back_h * s[kKH];      // sum k dH (without a token's gate)
-    const float back_y = post ? root_y * root_y * root_y * (token * dot * inv_h) : 0.f;
+    const float mean_h = root_h * (s[kTH] * inv_h);                                             // of t h R
+    const float dot = fmaf(root_h, fmaf(-mean_h, root_h * s[kKH], s[kKT]), s[kKD]);             // sum k dH (without a token's gate)
+    const float mean_y = root_y * inv_h * dot;
     if (token_gate && p.dgate.p && tid == 0) static_cast<float*>(const_cast<void*>(p.dgate.p))[row] = root_y * dot;
-    const float2 rh2 = both(root_h), bh2 = both(-back_h), ry2 = both(root_y), by2 = both(-back_y), token2 = both(token);
+    // the factors of h R and of y R (with a token's gate)
+    const float2 rh2 = both(root_h), bh2 = both(-mean_h * root_h), by2 = both(-mean_y * root_y), ry2 = both(root_y * token);
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
       const int c = column(v);
@@ -316,9 +321,9 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_kernel(const __grid
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            z[i] = mul2(z[i], rh2);
+            x[i] = mul2(x[i], rh2);
             acc[0][v][i] = fma2(z[i], x[i], acc[0][v][i]);
-            d[i] = fma2(z[i], w_pre[i], fma2(x[i], bh2, d[i]));
+            d[i] = fma2(mul2(z[i], rh2), w_pre[i], fma2(x[i], bh2, d[i]));
           }
         }
         if (p.dr.p) {
@@ -330,28 +335,28 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_kernel(const __grid
         if ((post || gate == MOE_GATE_CHANNEL) && !kKeep) {
           if constexpr (kFixed) weights(At::kAtPost, w); else factor(c, w);
         }
+        if (post) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], ry2);
+        }
         if (gate == MOE_GATE_FULL) {
           float2 o[4];                      // dH u, u = y R(y) (w_post + offset) or y
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            o[i] = mul2(d[i], y[i]);
-            if (post) o[i] = mul2(mul2(o[i], w[i]), ry2);
-          }
+          for (int i = 0; i < 4; ++i) o[i] = mul2(d[i], post ? mul2(y[i], w[i]) : y[i]);
           if (!kKeep) get(of_branch, p.gate, At::kAtG, at, row, c, g);
           if (p.dgate.p) put(of_branch, p.dgate, At::kAtG, at, row, c, o);
 #pragma unroll
           for (int i = 0; i < 4; ++i) d[i] = mul2(d[i], g[i]);
-        } else if (gate == MOE_GATE_NONE) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) d[i] = mul2(d[i], token2);
         }
         if (post || gate == MOE_GATE_CHANNEL) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            d[i] = mul2(d[i], ry2);
             acc[1][v][i] = fma2(d[i], y[i], acc[1][v][i]);
-            d[i] = post ? fma2(d[i], w[i], mul2(y[i], by2)) : mul2(d[i], w[i]);
+            d[i] = post ? fma2(mul2(d[i], ry2), w[i], mul2(y[i], by2)) : mul2(d[i], w[i]);
           }
+        } else if (gate == MOE_GATE_NONE) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[i] = mul2(d[i], ry2);
         }
         if (p.dy.p) put(of_branch, p.dy, 0, at, row, c, d);
       }

@@ -127,7 +127,8 @@ moe_status moe_route_balance(const int32_t* load, const float* bias, float* out,
  * too.  Padding rows are not touched.
  *
  * Squares are added in FP32: rows whose sum of squares passes its range
- * (magnitudes beyond about 1e18) give z = 0; a NaN or an infinity stays in its row.
+ * (magnitudes beyond about 1e17) are normed to 0, and with eps = 0 rows of magnitudes
+ * below about 1e-19 lose bits; a NaN or an infinity stays in its row.
  * ------------------------------------------------------------------------ */
 #define MOE_GATE_NONE 0
 #define MOE_GATE_CHANNEL 1   /* gate [H], weight_dtype     */
@@ -179,7 +180,8 @@ moe_status moe_norm_residual(const moe_norm_args* args, moe_stream_t stream);
  * dw_pre, dw_post and a channel gate's dgate are FP32 [H], a token gate's FP32
  * [M], a full one's [M, lddgate] dtype.  accumulate != 0: the three sums over
  * rows are added to what their buffers hold.  Padding rows are not touched and
- * add nothing (a token gate's dgate is not touched there either). */
+ * add nothing (a token gate's dgate is not touched there either).  Rows may have
+ * whatever magnitude the forward pass takes. */
 typedef struct moe_norm_backward_args {
   const void* y;               /* [M, ldy] dtype                                          */
   const void* h;               /* [M, ldh] stream_dtype (with dz; NULL: y)                */
