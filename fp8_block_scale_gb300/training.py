@@ -25,6 +25,8 @@ calls moe_route_scores, ``route_backward`` gives the logits' gradient and
 experts, norm, gate and residual, forward, backward and served in FP8.
 """
 
+import math
+
 import torch
 
 from . import _lib as L
@@ -270,6 +272,7 @@ class ExpertBlock:
         self._serving = None                              # what serve keeps, and the weights whose codes it holds
         self._served_version = None
         self._x = None                                    # the last forward's stream
+        self._load, self._loaded = torch.zeros(E, dtype=torch.int32, device=dev), False        # its experts' loads
 
     @property
     def steps(self):
@@ -306,7 +309,10 @@ class ExpertBlock:
         layer = self.layer
         self._take(x, self.dy, self.dr, self.dx, layer.out, layer.dx, layer.xs, layer.pre, layer.h, layer.ys, layer.dys, layer.dh)
         self._enter(x, num_tokens)
-        y = self.layer.forward(self.z)
+        if layer.bias is not None:
+            self._load.copy_(layer.group_rows)            # (a served batch has its own)
+            self._loaded = True
+        y = layer.forward(self.z)
         self._x = x, y, num_tokens
         return self._leave(x, y, num_tokens)
 
@@ -335,12 +341,26 @@ class ExpertBlock:
         return self.dx
 
     def step(self, lr, balance_rate=0.0, **adam):
-        """One AdamW step of all parameters from their grads (the experts' keywords: ``ExpertLayer.step``;
-        a step that skip leaves out does not count for any), and one of the balance bias."""
-        self.layer.step(lr, **adam)                       # (it settles the steps' number)
-        L.moe_adamw_step(L.make_adamw_args(self._table, lr=lr, step=self.layer.steps, **adam))
+        """One AdamW step of all parameters from their grads (the experts' keywords: ``ExpertLayer.step``),
+        and one of the balance bias towards an even load, from the last forward pass's.  A step that skip leaves
+        out does not count for any of them."""
+        layer = self.layer
+        if balance_rate and layer.bias is None:
+            raise RuntimeError("the layer has no balance bias")
+        if balance_rate and not self._loaded:
+            raise RuntimeError("balance without a forward pass")
+        if not math.isfinite(balance_rate):
+            raise ValueError(f"balance_rate: {balance_rate}")
+        layer.step(lr, **adam)                            # (it settles the steps' number)
+        L.moe_adamw_step(L.make_adamw_args(self._table, lr=lr, step=layer.steps, **adam))
         if balance_rate:
-            self.layer.balance(balance_rate)
+            skip = adam.get("skip")
+            if skip is None:
+                L.moe_route_balance(self._load, layer.bias, balance_rate)
+            else:
+                moved = torch.empty_like(layer.bias)
+                L.moe_route_balance(self._load, layer.bias, balance_rate, out=moved)
+                torch.where(skip.view(-1)[:1] == 0, moved, layer.bias, out=layer.bias)
 
     def _serving_buffers(self):
         layer, dev, I = self.layer, self.z.device, self.layer.I
