@@ -2,6 +2,8 @@
 // arithmetic without CUDA, so that the host can check every size.
 #pragma once
 
+#include <math.h>
+
 #ifdef __CUDACC__
 #define MOE_HOST_DEVICE __host__ __device__ __forceinline__
 #else
@@ -55,6 +57,17 @@ inline int route_places(const RouteLayout& p) {
 MOE_HOST_DEVICE int route_expert_at(const RouteLayout& p, int i, int lane) {
   const int off = ((((i >> p.run) * p.lanes + lane % p.lanes) << p.run) | (i & ((1 << p.run) - 1))), g = lane / p.lanes;
   return g < p.groups && off < p.group_size ? g * p.group_size + off : -1;
+}
+
+// How far a softmax score may be off, in units of 2^-23 of 1 / total (the score of the largest logit), where a
+// lane of `places` adds its experts' exponentials.  With x the distance to the largest logit an exponential is off by 2 +
+// 1.7 x units of itself (2 + 1.173 x by the hardware's, x / 2 from the rounding of x), and so is a score,
+// most at x = 0.  Below it stand the total's errors: its terms', 2 + 1.7 times the average of x over the softmax;
+// half a unit for each of places + 5 additions; the reciprocal's 1 and the product's half.  That average is at most
+// W((E - 1) / e), of E - 1 experts at one distance (W: Lambert's, W(y) <= ln((y + e^3) / 4)).  One unit to spare.
+inline float route_softmax_units(int E, int places) {
+  const double average = log((static_cast<double>(E) / 2.718281828459045 + 20.085536923187668) / 4.0);
+  return static_cast<float>(2.0 + (2.0 + 1.7 * average) + 0.5 * (places + 5) + 1.5 + 1.0);
 }
 
 }  // namespace moe

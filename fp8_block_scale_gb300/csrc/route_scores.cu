@@ -49,6 +49,7 @@ struct RouteParams : RouteLayout {
   int top_k, topk_groups;
   int pair, score, renormalize, dtype, id_bits;
   float scale;
+  float softmax_units;
 };
 
 __device__ __forceinline__ float warp_max(float v) {   // NaN has no part
@@ -510,11 +511,9 @@ __global__ void __launch_bounds__(32 * (kMode == 0 ? kWarps : kWarpsScored), kPe
         a1 = max_nan(a1, v[i]);
       }
       bool nan = a1 != a1;
-      // No value is further than `err` from its true one.  In units of 2^-23 a score is off by
-      // the fast exponential's 2 + 1.173 |x| and the divide's and sum's 3, times itself: for a
-      // sigmoid that is most at the largest logit, or at 0.  For softmax |x| / 2 more from the
-      // rounding of x = l - m, and the total's: half a unit for each of kPer + 5 additions and an
-      // average of its terms' own (exp(-x) (2 + 1.7 x) <= 3); most where x = 0.
+      // No value is further than `err` from its true one.  In units of 2^-23 a sigmoid is off by the fast
+      // exponential's 2 + 1.173 |x| and the divide's and sum's 3, times itself: most at the largest
+      // logit, or at 0.  For softmax see route_softmax_units.
       err = 0.f;
       if (kMode != 0 || (softmax && !p.renormalize)) m = warp_max(a1);
       if (kMode == 2 || (kMode == 0 && softmax && !p.renormalize)) {
@@ -525,7 +524,7 @@ __global__ void __launch_bounds__(32 * (kMode == 0 ? kWarps : kWarpsScored), kPe
       }
       if (kMode != 0) {
         inv = kMode == 2 ? reciprocal_coarse(total) : 1.f;
-        err = kMode == 1 ? fmaf(fmaxf(m, 0.f), 1.2f, 5.f) : (10.f + kPer / 2) * inv;
+        err = kMode == 1 ? fmaf(fmaxf(m, 0.f), 1.2f, 5.f) : p.softmax_units * inv;
         err = fmaf(err, 0x1p-23f, fmaf(most_bias + inv, 0x1p-22f, 0x1p-120f));          // (and the addition's half: a score is at most inv)
         a1 = -CUDART_INF_F;
         float any = 0.f;
@@ -951,6 +950,7 @@ moe_status moe_route_scores(const moe_route_scores_args* a, moe_stream_t stream)
   p.dtype = a->dtype;
   p.id_bits = a->id_bits;
   p.scale = a->routed_scale;
+  p.softmax_units = route_softmax_units(a->E, places);
   // without a bias the scores' order is the logits'; sums of two scores have none such
   const bool scored = a->bias || (p.groups > 1 && p.pair);
   const int mode = !scored ? 0 : a->score == MOE_SCORE_SIGMOID ? 1 : 2;
