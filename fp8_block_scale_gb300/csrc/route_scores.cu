@@ -552,7 +552,8 @@ __global__ void __launch_bounds__(32 * (kMode == 0 ? kWarps : kWarpsScored), kPe
           a1 = fmaxf(a1, b1);
         }
         const bool pair = kMode != 0 && p.pair && a2 != -CUDART_INF_F;
-        const float x = pair ? a1 + a2 : a1;
+        // (half of a group's value where scores are compared: sums of two of the type's lowest value stay in range)
+        const float x = kMode == 0 ? a1 : pair ? fmaf(0.5f, a1, 0.5f * a2) : 0.5f * a1;
         // the topk_groups largest, one after another, of equal ones the lower
         stays = false;
         float cur = group ? x : -CUDART_INF_F;
@@ -564,7 +565,7 @@ __global__ void __launch_bounds__(32 * (kMode == 0 ? kWarps : kWarpsScored), kPe
         }
         if (kMode != 0) {
           // a group that stays and one that goes nearer than their errors
-          const float worst = -warp_max(stays ? -x : -CUDART_INF_F), best = warp_max(!stays && group ? x : -CUDART_INF_F), near = 4.f * err;
+          const float worst = -warp_max(stays ? -x : -CUDART_INF_F), best = warp_max(!stays && group ? x : -CUDART_INF_F), near = 2.f * err;
           if (best != -CUDART_INF_F && !(worst - best > near)) {
             // (equal experts, as of a router's first step, are equal whatever their error)
             bool same = true;
