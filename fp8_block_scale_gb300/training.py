@@ -244,7 +244,8 @@ class ExpertBlock:
       out = residual_scale x + gate * N(y; w_post)
 
     All parameters are FP32; the experts are an ``ExpertLayer`` (``layer``), whose keywords
-    are passed on.  The router's product is a library product in FP32.  gate: a learned
+    are passed on.  The router's product is a library product of FP32 values, by torch's setting for those
+    (torch.backends.cuda.matmul: TF32 where that allows it).  gate: a learned
     factor for each channel, starting at gate_init; None for none.
     """
 
@@ -279,6 +280,12 @@ class ExpertBlock:
         return self.layer.steps
 
     @staticmethod
+    def _product(a, b, out=None):
+        """The router's product and its gradients: FP32 whatever torch.autocast says."""
+        with torch.autocast("cuda", enabled=False):
+            return torch.mm(a, b, out=out)
+
+    @staticmethod
     def _apart(name, t, own):
         if t.numel() and any(t.untyped_storage().data_ptr() == o.untyped_storage().data_ptr() for o in own):
             raise ValueError(f"{name}: a buffer of the block itself")
@@ -293,7 +300,7 @@ class ExpertBlock:
         if num_tokens is not None:
             self.z.zero_()                                # (what padding rows hold goes through the router's product)
         L.moe_norm_residual(L.make_norm_residual_args(x, z=self.z, w_pre=self.w_pre, eps=self.eps, num_rows=num_tokens, **out))
-        torch.mm(self.z.float(), self.w_router.t(), out=self.logits)
+        self._product(self.z.float(), self.w_router.t(), out=self.logits)
         self.layer.route(self.logits, num_tokens)
 
     def _leave(self, x, y, num_tokens):
@@ -334,8 +341,8 @@ class ExpertBlock:
             dgate=self.grads.get("gate"), dw_post=self.grads["w_post"], **how))
         dz, dweights = self.layer.backward(self.dy)
         dlogits = self.layer.route_backward(dweights)
-        torch.mm(dlogits.t(), self.z.float(), out=self.grads["w_router"])
-        dz.add_(torch.mm(dlogits, self.w_router))
+        self._product(dlogits.t(), self.z.float(), out=self.grads["w_router"])
+        dz.add_(self._product(dlogits, self.w_router))    # (rounded once more: the experts' part lies in 16 bits)
         L.moe_norm_residual_backward(L.make_norm_residual_backward_args(
             x, dh=self.dr, dz=dz, w_pre=self.w_pre, dy=self.dx, dw_pre=self.grads["w_pre"], **how))
         return self.dx
