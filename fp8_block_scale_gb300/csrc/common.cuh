@@ -420,6 +420,30 @@ __device__ __forceinline__ float2 e4m3x2_to_f32(uint16_t v) {
   return __half22float2(h);
 }
 
+// Smallest power of two >= s (s > 0, finite), computed on the bit pattern.
+__device__ __forceinline__ float pow2_round_up(float s) {
+  const uint32_t b = __float_as_uint(s);
+  const uint32_t ex = (b >> 23) & 0xFFu;
+  const uint32_t man = b & 0x7FFFFFu;
+  if (ex != 0) {
+    if (man == 0) return s;
+    if (ex >= 254) return s;  // 2^128 does not exist in FP32: leave such scales alone
+    return __uint_as_float((ex + 1) << 23);
+  }
+  // subnormal: value = man * 2^-149
+  const int p = 31 - __clz(man);  // highest set bit
+  if ((man & (man - 1)) == 0) return s;
+  if (p + 1 >= 23) return __uint_as_float(1u << 23);  // 2^-126, the smallest normal
+  return __uint_as_float(1u << (p + 1));
+}
+
+// The larger one; a NaN stays.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Start moving `bytes` (a multiple of 16, 16-byte aligned) from global
 // memory into L2 without waiting for them.
 __device__ __forceinline__ void prefetch_l2_bulk(const void* p, uint32_t bytes) {

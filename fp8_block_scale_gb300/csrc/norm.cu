@@ -29,23 +29,6 @@ struct NormParams {
   float residual_scale, weight_offset, eps;
 };
 
-// Smallest power of two >= s (as the quantisers round: a scale above 2^127 is kept).
-__device__ __forceinline__ float scale_to_pow2(float s) {
-  const uint32_t b = __float_as_uint(s), ex = b >> 23;
-  if ((b & 0x7FFFFFu) == 0 || ex >= 254) return s;
-  if (ex != 0) return __uint_as_float((ex + 1) << 23);
-  const int top = 31 - __clz(b);
-  if ((b & (b - 1)) == 0) return s;
-  return top + 1 >= 23 ? __uint_as_float(1u << 23) : __uint_as_float(1u << (top + 1));
-}
-
-// The larger one; a NaN stays (it reaches the scale: the codes alone could lose it).
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 // Eight values over one scale as E4M3 codes, each from the correctly rounded quotient: the product
 // with the reciprocal, corrected twice by its residual (Markstein), which is exact where no
 // value that rounds to a code is near FP32's smallest; one of them by a divide otherwise.
@@ -273,6 +256,7 @@ __global__ void __launch_bounds__(1024, 1) norm_kernel(const __grid_constant__ N
         }
         if (p.q) {
           // (a group of 128 columns is 16 neighbouring lanes: all of them or none have columns)
+          // (a NaN reaches the scale: the codes alone could lose it)
           float amax = 0.f;
           if (live_column) {
 #pragma unroll
@@ -281,7 +265,7 @@ __global__ void __launch_bounds__(1024, 1) norm_kernel(const __grid_constant__ N
 #pragma unroll
           for (int o = 8; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
           float s = __fdiv_rn(amax, 448.f);
-          if (p.pow2 && s > 0.f) s = scale_to_pow2(s);
+          if (p.pow2 && s > 0.f) s = pow2_round_up(s);
           if (live_column && MOE_IN_BOUNDS(row < M)) {
             *reinterpret_cast<uint2*>(p.q + static_cast<int64_t>(row) * p.H + c) = codes_of(h[v], s);
             if (lane % 16 == 0) p.q_scale[static_cast<int64_t>(row) * (p.H / 128) + c / 128] = s;

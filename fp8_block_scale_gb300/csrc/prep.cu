@@ -32,23 +32,6 @@ __global__ void interleave_kernel(const uint4* __restrict__ src, uint4* __restri
 
 // ---------------------------------------------------------------- UE8M0
 
-// Smallest power of two >= s (s > 0, finite), computed on the bit pattern.
-__device__ __forceinline__ float pow2_round_up(float s) {
-  const uint32_t b = __float_as_uint(s);
-  const uint32_t ex = (b >> 23) & 0xFFu;
-  const uint32_t man = b & 0x7FFFFFu;
-  if (ex != 0) {
-    if (man == 0) return s;
-    if (ex >= 254) return s;  // 2^128 does not exist in FP32: leave such scales alone
-    return __uint_as_float((ex + 1) << 23);
-  }
-  // subnormal: value = man * 2^-149
-  const int p = 31 - __clz(man);  // highest set bit
-  if ((man & (man - 1)) == 0) return s;
-  if (p + 1 >= 23) return __uint_as_float(1u << 23);  // 2^-126, the smallest normal
-  return __uint_as_float(1u << (p + 1));
-}
-
 __global__ void __launch_bounds__(256) requant_ue8m0_kernel(uint8_t* __restrict__ w, float* __restrict__ scale,
                                                             uint8_t* __restrict__ exp_out, int rows, int cols) {
   const int rb_n = rows / 128, cb_n = cols / 128;

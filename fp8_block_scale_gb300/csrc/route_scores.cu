@@ -274,11 +274,6 @@ __device__ __forceinline__ float reciprocal_coarse(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {      // a NaN stays
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 
 // What the choice compares, to the error that the kernel states for it.
 template <int kMode>
