@@ -684,17 +684,18 @@ struct RouteGradParams {
 template <int kPer>
 constexpr int kWordsBelow = kPer > 33 ? 33 : kPer > 16 ? 16 : kPer > 9 ? 9 : kPer > 5 ? 5 : kPer > 4 ? 4 : kPer > 2 ? 2 : 0;
 
+// (the row may be written in place: plain loads, not those of memory that stays as it is)
 template <typename T> struct Logit;
 template <> struct Logit<float> {
-  static constexpr int kDtype = MOE_TYPE_FP32;
+  static __device__ __forceinline__ float load(const float* p) { return *p; }
   static __device__ __forceinline__ float round(float v) { return v; }
 };
 template <> struct Logit<__nv_bfloat16> {
-  static constexpr int kDtype = MOE_TYPE_BF16;
+  static __device__ __forceinline__ float load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
   static __device__ __forceinline__ __nv_bfloat16 round(float v) { return __float2bfloat16_rn(v); }
 };
 template <> struct Logit<__half> {
-  static constexpr int kDtype = MOE_TYPE_FP16;
+  static __device__ __forceinline__ float load(const __half* p) { return __half2float(*p); }
   static __device__ __forceinline__ __half round(float v) { return __float2half_rn(v); }
 };
 
@@ -702,7 +703,6 @@ template <> struct Logit<__half> {
 template <typename T, int kPer>
 __global__ void __launch_bounds__(32 * kWarps, kPer <= 9 ? 8 : 1)
     route_scores_backward_kernel(const __grid_constant__ RouteGradParams p) {
-  constexpr int kDtype = Logit<T>::kDtype;
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x % 32;
@@ -725,14 +725,14 @@ __global__ void __launch_bounds__(32 * kWarps, kPer <= 9 ? 8 : 1)
         for (int j = 0; j < kEach; ++j) s[i][j] = -CUDART_INF_F;
         if (t < live) {
           if constexpr (kEach == 1) {
-            if (i < kSure || at < p.E) s[i][0] = __ldg(in + at);
+            if (i < kSure || at < p.E) s[i][0] = in[at];
           } else if (((i > 0 && i < kSure) || (at >= 0 && at + 1 < p.E)) && p.vec) {
-            const float2 v = Pack2<T>::load(__ldg(reinterpret_cast<const unsigned int*>(in + at)));
+            const float2 v = Pack2<T>::load(*reinterpret_cast<const unsigned int*>(in + at));
             s[i][0] = v.x, s[i][1] = v.y;
           } else {
 #pragma unroll
             for (int j = 0; j < kEach; ++j)
-              if (at + j >= 0 && at + j < p.E) s[i][j] = logit_at(in, kDtype, at + j);
+              if (at + j >= 0 && at + j < p.E) s[i][j] = Logit<T>::load(in + at + j);
           }
         }
       }
@@ -751,7 +751,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPer <= 9 ? 8 : 1)
     }
     bool here = e >= 0 && e < p.E;
     if (here) {
-      l = logit_at(in, kDtype, e);
+      l = Logit<T>::load(in + e);
       here = l != -CUDART_INF_F;
     }
     // an expert listed more than once counts by all of its terms: their sum and number
@@ -766,6 +766,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPer <= 9 ? 8 : 1)
       }
     }
     float own;                                      // the gradient at this lane's expert
+    __syncwarp();                                   // (every lane has its logits: the row may be written)
     if (kPer == 0) {
       if (p.renormalize) {
         // scores over a common factor that cannot vanish, as in the forward pass
