@@ -220,10 +220,12 @@ class ExpertLayer:
         """The trained weights as the FP8 forward takes them: (w13 interleaved,
         w13_scale, w2, w2_scale).  H, I multiples of 128; BF16 weights, ValueError for others.
         out: what an earlier call returned, written again instead of new tensors."""
+        kinds = [k for w in self.models for k in (
+            (tuple(w.shape), torch.uint8), ((w.shape[0], w.shape[1] // 128, w.shape[2] // 128), torch.float32))]
         if out is None:
-            out = tuple(t for w in self.models for t in (
-                torch.empty(w.shape, dtype=torch.uint8, device=w.device),
-                torch.empty(w.shape[0], w.shape[1] // 128, w.shape[2] // 128, dtype=torch.float32, device=w.device)))
+            out = tuple(torch.empty(shape, dtype=dtype, device=self.models[0].device) for shape, dtype in kinds)
+        elif [(tuple(t.shape), t.dtype) for t in out] != kinds or not all(t.is_contiguous() for t in out):
+            raise ValueError("out: what an earlier call returned is expected")
         w13, w13_scale, w2, w2_scale = out
         rows = torch.empty_like(w13)                      # (before they are interleaved)
         L.moe_quantize_weight_128x128(self.models[0], rows, w13_scale)
@@ -232,7 +234,8 @@ class ExpertLayer:
         return out
 
     def weights_version(self):
-        """Another value after each step of the layer and each write of torch's to the weights."""
+        """Another value after each step of the layer and each write of torch's to the weights (tensors
+        made in inference mode keep no count of those)."""
         return self._calls, tuple(0 if w.is_inference() else w._version for w in self.models)
 
 
@@ -383,7 +386,8 @@ class ExpertBlock:
 
     def refresh(self):
         """Forms the FP8 weights that ``serve`` reads anew, where they lie.  Needed after writes to the
-        experts' weights that neither ``step`` (the block's or the layer's) nor torch has made."""
+        experts' weights that neither ``step`` (the block's or the layer's) nor torch has made, and
+        after torch's where the block was made in inference mode."""
         self._quantise()
 
     def _quantise(self):
