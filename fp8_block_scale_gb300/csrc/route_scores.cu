@@ -15,9 +15,9 @@
 // Without a bias the scores' order is the logits' own, which are compared as they are.
 //
 // Instructions bound it, and of those mostly the ones that a token costs whatever E is: 16-bit
-// logits of 257 experts, top 9, take some 470 (65536 tokens: 29.3 us, 1.31 TB/s); sigmoid scores with
-// a bias, 8 groups and top 10 of 512 experts some 1080 (8192 tokens: 12.0 us).  Two tokens finished
-// side by side by half a warp each (10% fewer instructions, fewer warps) and warps that stay
+// logits of 257 experts, top 9, take some 470 (65536 tokens: 29.5 us, 1.31 TB/s); sigmoid scores with
+// a bias, 8 groups and top 10 of 512 experts some 1080 (8192 tokens: 11.2 to 12.2 us, by their near
+// ties).  Two tokens finished side by side by half a warp each (10% fewer instructions, fewer warps) and warps that stay
 // for many tokens (40 us) were slower.  The 64 bits count where a token is among the last ones: of
 // 8192, two or three have groups too near to tell, which cost 2 us until only the groups in
 // question were formed so.
@@ -375,6 +375,10 @@ __device__ __forceinline__ void write_routes(const RouteParams& p, uint32_t t, i
 // The kernels' places a lane are 2, 4, 8, 9, 12, 16, 32, 64 and (groups only) 128.  Without runs of experts a kernel is
 // taken for more than the next smaller number, so that every lane has an expert in that many places (without
 // groups), and they need no comparison (65536 tokens of 257 experts: 29.3 us, 30.4 with it).
+// Steps are by about a third up to 16, then double.  9 is for 256 experts and up to a lane's width more (257 to 288
+// in 16 bits, 65536 tokens: 28.8 to 29.6 us, 30.7 to 30.9 with 12 places) and 33 to 36 in each of eight groups (8192
+// tokens: 11.0 to 11.5, 11.5 to 11.9).  More than 64 places take all registers: 8192 tokens of 2040 experts in
+// 17 groups 250 us, of 2048 in 16 groups 59.
 template <int kPer>
 constexpr int kPlacesBelow = kPer > 32 ? 32 : kPer > 16 ? 16 : kPer > 12 ? 12 : kPer > 9 ? 9 : kPer > 8 ? 8 : kPer > 4 ? 4 : kPer > 2 ? 2 : 0;
 
@@ -665,8 +669,8 @@ __global__ void __launch_bounds__(32 * (kMode == 0 ? kWarps : kWarpsScored), kPe
 //
 // Zeros: the writes bound it (8192 tokens of 512 experts, FP32: 6.0 us, 3.0 TB/s into L2 and
 // HBM, launch included).  Dense rows: two loads one after the other (ids, their logits), two
-// sums over the warp and 340 instructions a token (65536 tokens of 257 experts in 16 bits: 31.3 us,
-// 2.3 TB/s); pairs of 16-bit logits, 42 us one at a time.  Loads of the next token ahead and both sums
+// sums over the warp and 350 instructions a token (65536 tokens of 257 experts in 16 bits: 32.2 us with
+// the balance step, 2.2 TB/s); pairs of 16-bit logits, 42 us one at a time.  Loads of the next token ahead and both sums
 // in one exchange changed nothing; six CTAs an SM instead of eight 38 us.
 struct RouteGradParams {
   const void* logits;
@@ -681,6 +685,8 @@ struct RouteGradParams {
 
 // The next smaller of the dense kernels' words a lane, which a kernel is taken for more than: words below it
 // lie inside the row (but the first pair, which may begin one before it), and need no comparison (32.1 -> 31.3 us).
+// 16-bit rows of 256, 512 and 2048 experts need one word more than a power of two, for that pair: 5, 9 and 33.  65536 x 256
+// takes 30.4 us, 42.6 with nine words a lane, and 32768 x 512 31.7, 67 with sixteen.
 template <int kPer>
 constexpr int kWordsBelow = kPer > 33 ? 33 : kPer > 16 ? 16 : kPer > 9 ? 9 : kPer > 5 ? 5 : kPer > 4 ? 4 : kPer > 2 ? 2 : 0;
 

@@ -247,7 +247,8 @@ class ExpertBlock:
       out = residual_scale x + gate * N(y; w_post)
 
     All parameters are FP32; the experts are an ``ExpertLayer`` (``layer``), whose keywords
-    are passed on.  The router's product is a library product of FP32 values, by torch's setting for those
+    are passed on.  z and out come from a pass each over the stream (blocks in a row could share one:
+    moe_norm_residual forms both).  The router's product is a library product of FP32 values, by torch's setting for those
     (torch.backends.cuda.matmul: TF32 where that allows it).  gate: a learned
     factor for each channel, starting at gate_init; None for none.
     """

@@ -39,7 +39,9 @@ extern "C" {
  * (MOE_GROUP_MAX) or the sum of its two largest (MOE_GROUP_TOP2; one alone
  * counts by itself; without a bias c = s here).  Of the topk_groups largest
  * groups, the top_k experts with the largest c are chosen, in falling order.
- * Values are compared as in 64 bits; of equal ones the lower index comes first.
+ * Values are compared as in 64 bits; of equal ones the lower index comes first.  (A bias
+ * beside which scores vanish in FP32 is right but slow, 50 times at its type's lowest
+ * value: leave experts out by -inf.)
  *   topk_weights[t, j] = routed_scale * s_j / (sum of s over the chosen)
  *                                                 with renormalize
  *   topk_weights[t, j] = routed_scale * s_j       without
@@ -48,6 +50,11 @@ extern "C" {
  * leaves out) and weight 0.  Renormalised weights are right however small
  * the scores are.  A NaN, in the logits or the bias, counts as the largest value and
  * stays in the weights that its score is part of; ids are always distinct.
+ *
+ * Accuracy, in units of 2^-23 and with x the distance of a logit from the largest one (softmax) or
+ * from 0 (sigmoid): a score is within 4 + |x| / 2 units of itself, a renormalised weight within
+ * twice that and 5 more.  A plain softmax weight is divided by a total of hardware exponentials, off
+ * by up to 2 + 1.7 ln E units and half a unit for each of E / 32 + 5 additions (groups: up to 133).
  * ------------------------------------------------------------------------ */
 #define MOE_SCORE_SOFTMAX 0
 #define MOE_SCORE_SIGMOID 1
@@ -86,7 +93,8 @@ moe_status moe_route_scores(const moe_route_scores_args* args, moe_stream_t stre
  *   softmax, renormalize: dl_j = scale p_j (dw_j - sum_i dw_i p_i)
  *   softmax:              dl_e = scale s_e ([e listed] dw_e - sum_i dw_i s_i), every e
  * and zero for the other logits and for padding tokens.  An expert listed twice
- * counts as two terms. */
+ * counts as two terms.  Plain softmax forms its scores by hardware exponentials, within (2 +
+ * 1.7 |x|) 2^-23 of themselves before the total's error; what lies below 2^-126 may be 0. */
 typedef struct moe_route_scores_backward_args {
   const void* logits;          /* [M, ldlogits] dtype                                     */
   const void* topk_ids;        /* [M, top_k] int32 or int64                               */
