@@ -360,7 +360,7 @@ class ExpertBlock:
             raise RuntimeError("the layer has no balance bias")
         if balance_rate and not self._loaded:
             raise RuntimeError("balance without a forward pass")
-        if not math.isfinite(balance_rate):
+        if balance_rate and not math.isfinite(balance_rate):
             raise ValueError(f"balance_rate: {balance_rate}")
         layer.step(lr, **adam)                            # (it settles the steps' number)
         L.moe_adamw_step(L.make_adamw_args(self._table, lr=lr, step=layer.steps, **adam))

@@ -66,3 +66,6 @@ def test_a_step_that_cannot_balance_changes_nothing():
     with pytest.raises(ValueError):
         b.step(1e-2, balance_rate=float("nan"))
     assert b.steps == 0
+    b.backward(x)
+    b.step(1e-2, balance_rate=None)                    # (as without)
+    assert b.steps == 1
